@@ -66,7 +66,11 @@ typedef enum {
     ZI_ERR_IO = 8          /* a file could not be opened or read */
 } zi_status;
 
-typedef enum { ZI_F16 = 1, ZI_BF16 = 2 } zi_dtype;
+typedef enum {
+    ZI_F16 = 1,
+    ZI_BF16 = 2,
+    ZI_F32 = 3 /* layer norm, embedding and orthogonalisation only: a plan's type is 16 bits wide */
+} zi_dtype;
 
 /* zi_problem.flags */
 #define ZI_FLAG_F32_OUT 0x1u /* Y and dW^t are written in fp32 instead of the input
@@ -658,6 +662,85 @@ zi_status zi_tier_trace_get(zi_tier *tier, int64_t *ids, int64_t cap, int64_t *l
  * buffers < 2, a window outside 1..buffers or steps < 1. */
 zi_status zi_tier_simulate_reads(const int64_t *trace, int64_t len, int32_t buffers, int32_t window, int32_t steps,
                                  int64_t *reads_per_step);
+
+/* ---- operators next to the block ---------------------------------------------
+ *
+ * What a training step runs on the device around the tiled feed-forward block:
+ * the token embedding that makes its input, the layer norm in front of it with
+ * the residual sum, and the orthogonalised update of a weight's gradient.
+ * They take no context: every launch goes to `stream` (a hipStream_t of the
+ * current device, passed as void*; NULL: the null stream), in order with what
+ * the caller enqueues there, and the calls return at once.  They allocate
+ * nothing, keep nothing between calls and can be captured into a HIP graph.
+ * A workspace is caller-owned device memory, 256-byte aligned, whose contents
+ * need no preparation and mean nothing afterwards; calls that may overlap (on
+ * two streams) need one each.  Device pointers are aligned to their element;
+ * rows are contiguous, and lie a stride of elements apart (0: as many as they
+ * have).  ZI_ERR_ARG, ZI_ERR_SHAPE, ZI_ERR_ALIGN and ZI_ERR_BUDGET (workspace
+ * too small) come before anything is enqueued, ZI_ERR_HIP when a launch fails. */
+
+/* A layer norm over rows of D elements. */
+typedef struct {
+    int64_t T;                   /* rows: 0 .. 2^31 - 1                                     */
+    int64_t D;                   /* columns: 1 .. 2^31 - 1                                  */
+    int64_t ldx, ldr, lds, ldy;  /* row strides: ldx of X and dX, ldr of R and dS, lds of S,
+                                    ldy of Y and dY; 0 = D                                  */
+    int32_t x_dtype;             /* the residual stream: X, S, dS, dX                       */
+    int32_t y_dtype;             /* the block's side: Y, R, dY.  Equal to x_dtype, or one of
+                                    the two is ZI_F32                                       */
+    int32_t p_dtype;             /* gamma, beta                                             */
+    float eps;                   /* >= 0                                                    */
+} zi_norm;
+
+/* Forward: S = RNE(X + R) (without R, S is X itself),
+ *   mean = sum_i S_i / D, rstd = 1 / sqrt(sum_i (S_i - mean)^2 / D + eps),
+ *   Y = RNE((S - mean) rstd gamma + beta)
+ * for every row, sums in fp32.  R, and with it S, may be NULL; S may be NULL
+ * with R (the sum is then not kept); gamma and beta NULL stand for ones and
+ * zeros; mean and rstd (fp32, T each) may be NULL.  S may be X or R itself, and
+ * Y may be X, R or S, where stride and type agree; outputs overlap nothing
+ * otherwise. */
+zi_status zi_layer_norm_fwd(const zi_norm *norm, const void *X, const void *R, const void *gamma, const void *beta,
+                            void *S, void *Y, float *mean, float *rstd, void *stream);
+
+/* Backward, from the forward's S, mean and rstd: with h = (S - mean) rstd and
+ * g = dY gamma, for every row
+ *   dX = RNE(rstd (g - sum(g) / D - h sum(g h) / D) + dS),
+ * and over the rows dgamma = sum dY h, dbeta = sum dY (fp32, overwritten, the
+ * same bits every time).  dS, the gradient that reaches S along the residual
+ * stream, may be NULL (zero); so may gamma (ones), dgamma and dbeta (not
+ * formed: then no workspace is needed).  dX may be dS, S or dY itself, where
+ * stride and type agree.  With T = 0, dgamma and dbeta are zero.  y_dtype is
+ * dY's type: ZI_F32 for the dX of zi_tiled_linear_bwd. */
+uint64_t zi_layer_norm_bwd_bytes(int64_t T, int64_t D);
+zi_status zi_layer_norm_bwd(const zi_norm *norm, const void *dY, const void *S, const void *gamma, const float *mean,
+                            const float *rstd, const void *dS, void *dX, float *dgamma, float *dbeta,
+                            void *workspace, uint64_t workspace_bytes, void *stream);
+
+/* A table of V rows of D elements, looked up by T token ids.  An id outside
+ * [0, V) marks padding: a zero row of X, and no gradient. */
+typedef struct {
+    int64_t T;           /* tokens: 0 .. 2^31 - 1025                     */
+    int64_t V;           /* rows of the table: 1 .. 2^31 - 1             */
+    int64_t D;           /* columns: 1 .. 65535 * 2048                   */
+    int64_t ldw, ldx;    /* row strides of W and dW, of X and dX; 0 = D  */
+    int32_t w_dtype;     /* W, dW                                        */
+    int32_t x_dtype;     /* X, dX                                        */
+    int32_t ids64;       /* ids are int64 (else int32)                   */
+    float scale;         /* finite                                       */
+    int32_t accumulate;  /* gradient: add to dW (else overwrite it all)  */
+} zi_embedding;
+
+/* X[t] = RNE(scale W[id_t]). */
+zi_status zi_embedding_fwd(const zi_embedding *emb, const void *ids, const void *W, void *X, void *stream);
+
+/* dW[v] (+)= scale * sum of dX[t] over the tokens with id_t = v, for every row
+ * v: summed in fp32 in an order that depends on the ids alone, rounded once.
+ * Without `accumulate`, rows without a token are written as zero; with it,
+ * they are not touched. */
+uint64_t zi_embedding_bwd_bytes(int64_t T, int64_t V, int64_t D);
+zi_status zi_embedding_bwd(const zi_embedding *emb, const void *ids, const void *dX, void *dW, void *workspace,
+                           uint64_t workspace_bytes, void *stream);
 
 /* Page-locked host memory (hipHostMalloc) for W^t / dW^t; 4096-byte aligned. */
 zi_status zi_host_alloc(uint64_t bytes, void **out);

@@ -1,0 +1,563 @@
+// zi_norm.hip -- layer norm in front of a block, forward and backward.
+//
+// Forward, row by row (D elements):
+//   S = RNE(X + R)                (R, the block's output before it, is optional)
+//   mean = sum S / D,  var = sum (S - mean)^2 / D,  rstd = 1 / sqrt(var + eps)
+//   Y = (S - mean) rstd gamma + beta
+// Backward, with h = (S - mean) rstd and g = dY gamma:
+//   dX = rstd (g - mean(g) - h mean(g h)) + dS
+//   dgamma = sum over rows of dY h,  dbeta = sum over rows of dY
+// All sums are held in fp32; a row's variance is summed from the differences to
+// its mean, so that a large mean costs no digits; S, Y and dX are rounded once.
+//
+// A row is held in registers by NT threads, V vectors of eight elements each,
+// so that it is read once: the kernels are bound by HBM.  Rows longer than
+// the largest of these take a form that reads the row again for each sum.
+#include <hip/hip_runtime.h>
+#include <math.h>
+#include <stdint.h>
+
+#include "../../include/zi.h"
+#include "zi_host.h"
+#include "zi_vec.h"
+
+namespace {
+
+using namespace zi;
+
+struct NormArgs {
+    int64_t T, D;
+    int64_t ldx, ldr, lds, ldy;
+    float eps, width;  // width: D, which sums are divided by (a constant row's mean is exact)
+    int32_t p_dtype;
+    const void *X, *R;  // forward inputs
+    void *S, *Y;        // forward outputs; the backward reads S, and Y is dY
+    const void *gamma, *beta;
+    float *mean, *rstd;
+    const void *dS;  // backward
+    void *dX;
+    float *part;  // [gridDim.x][2][D]: each workgroup's sums of dY h and of dY
+};
+
+// Sum over the NT threads that hold a row; every one of them gets it.  `slots`:
+// LDS words of this sum alone (NT / 64 of them), so that one barrier is enough.
+template <int NT>
+__device__ __forceinline__ float row_sum(float x, float *slots) {
+    if constexpr (NT <= 64) return lane_sum<NT>(x);
+    x = lane_sum<64>(x);
+    if ((threadIdx.x & 63) == 0) slots[threadIdx.x >> 6] = x;
+    __syncthreads();
+    float s = 0.f;
+#pragma unroll
+    for (int w = 0; w < NT / 64; ++w) s += slots[w];
+    return s;
+}
+
+template <int NT>
+constexpr int kRows = NT < 256 ? 256 / NT : 1;  // rows of a workgroup at a time
+template <int NT>
+constexpr int kBlock = NT < 256 ? 256 : NT;
+
+template <typename XT, typename YT, bool RES, int NT, int V>
+__global__ __launch_bounds__(kBlock<NT>) void norm_fwd_kernel(NormArgs a) {
+    __shared__ float slots[2][2][NT <= 64 ? 1 : NT / 64];
+    const int t = threadIdx.x % NT;
+    int par = 0;  // two rows in a row use different slots
+    for (int64_t at = (int64_t)blockIdx.x * kRows<NT>; at < a.T; at += (int64_t)gridDim.x * kRows<NT>, par ^= 1) {
+        const int64_t row = at + threadIdx.x / NT;
+        const int64_t D = row < a.T ? a.D : 0;  // past the last row: no elements
+        const XT *x = static_cast<const XT *>(a.X) + row * a.ldx;
+        const YT *r = static_cast<const YT *>(a.R) + row * a.ldr;
+        XT *sp = static_cast<XT *>(a.S) + row * a.lds;
+        YT *y = static_cast<YT *>(a.Y) + row * a.ldy;
+        float s[V][8];
+#pragma unroll
+        for (int c = 0; c < V; ++c) {
+            const int64_t i = (int64_t)(t + c * NT) * 8;
+            load_n(x + i, D - i, s[c]);
+        }
+        if constexpr (RES) {
+            float u[V][8];
+#pragma unroll
+            for (int c = 0; c < V; ++c) {
+                const int64_t i = (int64_t)(t + c * NT) * 8;
+                load_n(r + i, D - i, u[c]);
+            }
+#pragma unroll
+            for (int c = 0; c < V; ++c) {
+                const int64_t i = (int64_t)(t + c * NT) * 8;
+                // the statistics are those of the stored sum, which the backward reads
+#pragma unroll
+                for (int e = 0; e < 8; ++e) s[c][e] = (float)(XT)(s[c][e] + u[c][e]);
+                if (a.S) store_n(sp + i, D - i, s[c]);
+            }
+        }
+        float sum = 0.f;
+#pragma unroll
+        for (int c = 0; c < V; ++c)
+#pragma unroll
+            for (int e = 0; e < 8; ++e) sum += s[c][e];
+        const float mean = row_sum<NT>(sum, slots[par][0]) / a.width;
+        float sq = 0.f;
+#pragma unroll
+        for (int c = 0; c < V; ++c) {
+            const int64_t i = (int64_t)(t + c * NT) * 8;
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                s[c][e] -= mean;
+                if (i + e < D) sq += s[c][e] * s[c][e];
+            }
+        }
+        const float rstd = 1.0f / sqrtf(row_sum<NT>(sq, slots[par][1]) / a.width + a.eps);
+        if (t == 0 && row < a.T) {
+            if (a.mean) a.mean[row] = mean;
+            if (a.rstd) a.rstd[row] = rstd;
+        }
+#pragma unroll
+        for (int c = 0; c < V; ++c) {
+            const int64_t i = (int64_t)(t + c * NT) * 8;
+            float g[8], b[8];
+#pragma unroll
+            for (int e = 0; e < 8; ++e) s[c][e] *= rstd;
+            if (a.gamma) {
+                load_n(a.gamma, a.p_dtype, i, D - i, g);
+#pragma unroll
+                for (int e = 0; e < 8; ++e) s[c][e] *= g[e];
+            }
+            if (a.beta) {
+                load_n(a.beta, a.p_dtype, i, D - i, b);
+#pragma unroll
+                for (int e = 0; e < 8; ++e) s[c][e] += b[e];
+            }
+            store_n(y + i, D - i, s[c]);
+        }
+    }
+}
+
+// Rows of any length: three passes over the row, which the caches serve.
+template <typename XT, typename YT, bool RES>
+__global__ __launch_bounds__(1024) void norm_fwd_long_kernel(NormArgs a) {
+    constexpr int NT = 1024;
+    __shared__ float slots[2][NT / 64];
+    const int64_t row = blockIdx.x;
+    const XT *x = static_cast<const XT *>(a.X) + row * a.ldx;
+    const YT *r = static_cast<const YT *>(a.R) + row * a.ldr;
+    XT *sp = static_cast<XT *>(a.S) + row * a.lds;
+    YT *y = static_cast<YT *>(a.Y) + row * a.ldy;
+    // the row's sum as stored; from the first pass on it may have replaced X or R
+    auto value = [&](int64_t i, bool first, float (&s)[8]) __attribute__((always_inline)) {
+        if (RES && a.S && !first) {
+            load_n(sp + i, a.D - i, s);
+            return;
+        }
+        load_n(x + i, a.D - i, s);
+        if constexpr (RES) {
+            float u[8];
+            load_n(r + i, a.D - i, u);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) s[e] = (float)(XT)(s[e] + u[e]);
+        }
+    };
+    float s[8], sum = 0.f, sq = 0.f;
+    for (int64_t i = threadIdx.x * 8; i < a.D; i += NT * 8) {
+        value(i, true, s);
+        if (RES && a.S) store_n(sp + i, a.D - i, s);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) sum += s[e];
+    }
+    const float mean = row_sum<NT>(sum, slots[0]) / a.width;
+    for (int64_t i = threadIdx.x * 8; i < a.D; i += NT * 8) {
+        value(i, false, s);
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+            if (i + e < a.D) sq += (s[e] - mean) * (s[e] - mean);
+    }
+    const float rstd = 1.0f / sqrtf(row_sum<NT>(sq, slots[1]) / a.width + a.eps);
+    if (threadIdx.x == 0) {
+        if (a.mean) a.mean[row] = mean;
+        if (a.rstd) a.rstd[row] = rstd;
+    }
+    for (int64_t i = threadIdx.x * 8; i < a.D; i += NT * 8) {
+        float g[8], b[8];
+        value(i, false, s);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) s[e] = (s[e] - mean) * rstd;
+        if (a.gamma) {
+            load_n(a.gamma, a.p_dtype, i, a.D - i, g);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) s[e] *= g[e];
+        }
+        if (a.beta) {
+            load_n(a.beta, a.p_dtype, i, a.D - i, b);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) s[e] += b[e];
+        }
+        store_n(y + i, a.D - i, s);
+    }
+}
+
+// A workgroup takes rows blockIdx.x, + gridDim.x, ... (kRows of them at a time)
+// and holds its sums of dY h and dY in registers over all of them.
+template <typename XT, typename YT, int NT, int V>
+__global__ __launch_bounds__(kBlock<NT>) void norm_bwd_kernel(NormArgs a) {
+    __shared__ float slots[2][2][NT <= 64 ? 1 : NT / 64];
+    __shared__ float fold[NT < 256 ? 256 * 8 : 1];
+    const int t = threadIdx.x % NT, sub = threadIdx.x / NT;
+    float ag[V][8], ab[V][8];
+#pragma unroll
+    for (int c = 0; c < V; ++c)
+#pragma unroll
+        for (int e = 0; e < 8; ++e) ag[c][e] = ab[c][e] = 0.f;
+    int par = 0;  // the sums of two rows in a row use different slots
+    for (int64_t first = (int64_t)blockIdx.x * kRows<NT>; first < a.T; first += (int64_t)gridDim.x * kRows<NT>, par ^= 1) {
+        const int64_t row = first + sub;
+        const int64_t D = row < a.T ? a.D : 0;
+        const XT *x = static_cast<const XT *>(a.S) + row * a.lds;
+        const YT *dy = static_cast<const YT *>(a.Y) + row * a.ldy;
+        const XT *ds = static_cast<const XT *>(a.dS) + row * a.ldr;
+        XT *dx = static_cast<XT *>(a.dX) + row * a.ldx;
+        float h[V][8], d[V][8];
+#pragma unroll
+        for (int c = 0; c < V; ++c) {
+            const int64_t i = (int64_t)(t + c * NT) * 8;
+            load_n(x + i, D - i, h[c]);
+            load_n(dy + i, D - i, d[c]);
+        }
+        const float mean = row < a.T ? a.mean[row] : 0.f, rstd = row < a.T ? a.rstd[row] : 0.f;
+        float sg = 0.f, sgh = 0.f;
+#pragma unroll
+        for (int c = 0; c < V; ++c) {
+            const int64_t i = (int64_t)(t + c * NT) * 8;
+            float g[8];
+            if (a.gamma) load_n(a.gamma, a.p_dtype, i, D - i, g);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                // past the row's end dY reads zero, and so do the sums
+                h[c][e] = (h[c][e] - mean) * rstd;
+                ag[c][e] += d[c][e] * h[c][e];
+                ab[c][e] += d[c][e];
+                if (a.gamma) d[c][e] *= g[e];
+                sg += d[c][e];
+                sgh += d[c][e] * h[c][e];
+            }
+        }
+        const float mg = row_sum<NT>(sg, slots[par][0]) / a.width;
+        const float mgh = row_sum<NT>(sgh, slots[par][1]) / a.width;
+#pragma unroll
+        for (int c = 0; c < V; ++c) {
+            const int64_t i = (int64_t)(t + c * NT) * 8;
+            float o[8];
+#pragma unroll
+            for (int e = 0; e < 8; ++e) o[e] = (d[c][e] - mg - h[c][e] * mgh) * rstd;
+            if (a.dS) {
+                float u[8];
+                load_n(ds + i, D - i, u);
+#pragma unroll
+                for (int e = 0; e < 8; ++e) o[e] += u[e];
+            }
+            store_n(dx + i, D - i, o);
+        }
+    }
+    if (!a.part) return;
+    float *pg = a.part + (int64_t)blockIdx.x * 2 * a.D, *pb = pg + a.D;
+    if constexpr (NT >= 256) {
+#pragma unroll
+        for (int c = 0; c < V; ++c) {
+            const int64_t i = (int64_t)(t + c * NT) * 8;
+            store_n(pg + i, a.D - i, ag[c]);
+            store_n(pb + i, a.D - i, ab[c]);
+        }
+    } else {  // the workgroup's rows are summed here, in order
+#pragma unroll
+        for (int c = 0; c < V; ++c)
+#pragma unroll
+            for (int w = 0; w < 2; ++w) {
+                __syncthreads();
+#pragma unroll
+                for (int e = 0; e < 8; ++e) fold[threadIdx.x * 8 + e] = w ? ab[c][e] : ag[c][e];
+                __syncthreads();
+                for (int j = threadIdx.x; j < NT * 8; j += 256) {
+                    float s = 0.f;
+                    for (int k = 0; k < kRows<NT>; ++k) s += fold[k * NT * 8 + j];
+                    const int64_t i = (int64_t)c * NT * 8 + j;
+                    if (i < a.D) (w ? pb : pg)[i] = s;
+                }
+            }
+    }
+}
+
+// dX of rows of any length; dgamma and dbeta are left to norm_cols_kernel.
+template <typename XT, typename YT>
+__global__ __launch_bounds__(1024) void norm_bwd_long_kernel(NormArgs a) {
+    constexpr int NT = 1024;
+    __shared__ float slots[2][NT / 64];
+    const int64_t row = blockIdx.x;
+    const XT *x = static_cast<const XT *>(a.S) + row * a.lds;
+    const YT *dy = static_cast<const YT *>(a.Y) + row * a.ldy;
+    const XT *ds = static_cast<const XT *>(a.dS) + row * a.ldr;
+    XT *dx = static_cast<XT *>(a.dX) + row * a.ldx;
+    const float mean = a.mean[row], rstd = a.rstd[row];
+    auto value = [&](int64_t i, float (&h)[8], float (&d)[8]) __attribute__((always_inline)) {
+        float g[8];
+        load_n(x + i, a.D - i, h);
+        load_n(dy + i, a.D - i, d);
+        if (a.gamma) load_n(a.gamma, a.p_dtype, i, a.D - i, g);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            h[e] = (h[e] - mean) * rstd;
+            if (a.gamma) d[e] *= g[e];
+        }
+    };
+    float h[8], d[8], sg = 0.f, sgh = 0.f;
+    for (int64_t i = threadIdx.x * 8; i < a.D; i += NT * 8) {
+        value(i, h, d);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            sg += d[e];
+            sgh += d[e] * h[e];
+        }
+    }
+    const float mg = row_sum<NT>(sg, slots[0]) / a.width;
+    const float mgh = row_sum<NT>(sgh, slots[1]) / a.width;
+    for (int64_t i = threadIdx.x * 8; i < a.D; i += NT * 8) {
+        float u[8];
+        value(i, h, d);
+        if (a.dS) load_n(ds + i, a.D - i, u);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            d[e] = (d[e] - mg - h[e] * mgh) * rstd;
+            if (a.dS) d[e] += u[e];
+        }
+        store_n(dx + i, a.D - i, d);
+    }
+}
+
+// Sums of dY h and dY over every gridDim.y-th row, 8 columns a thread (long
+// rows only; runs before the dX kernel, which may overwrite dY).
+template <typename XT, typename YT>
+__global__ __launch_bounds__(256) void norm_cols_kernel(NormArgs a) {
+    const int64_t i = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 8;
+    if (i >= a.D) return;
+    float ag[8] = {}, ab[8] = {};
+    for (int64_t row = blockIdx.y; row < a.T; row += gridDim.y) {
+        float h[8], d[8];
+        load_n(static_cast<const XT *>(a.S) + row * a.lds + i, a.D - i, h);
+        load_n(static_cast<const YT *>(a.Y) + row * a.ldy + i, a.D - i, d);
+        const float mean = a.mean[row], rstd = a.rstd[row];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            ag[e] += d[e] * ((h[e] - mean) * rstd);
+            ab[e] += d[e];
+        }
+    }
+    float *pg = a.part + (int64_t)blockIdx.y * 2 * a.D;
+    store_n(pg + i, a.D - i, ag);
+    store_n(pg + a.D + i, a.D - i, ab);
+}
+
+// dgamma and dbeta from the partial sums, in a fixed order: 64 columns and 16
+// shares of the partial sums a workgroup.
+__global__ __launch_bounds__(1024) void norm_fold_kernel(const float *part, int64_t D, int32_t parts, float *dgamma,
+                                                         float *dbeta) {
+    __shared__ float sum[16][64];
+    const int lane = threadIdx.x & 63, share = threadIdx.x >> 6;
+    const int64_t col = (int64_t)blockIdx.x * 64 + lane;  // of [dgamma, dbeta]
+    float s = 0.f;
+    if (col < 2 * D)
+        for (int p = share; p < parts; p += 16) s += part[p * 2 * D + col];
+    sum[share][lane] = s;
+    __syncthreads();
+    if (share || col >= 2 * D) return;
+#pragma unroll
+    for (int k = 1; k < 16; ++k) s += sum[k][lane];
+    if (col < D) {
+        if (dgamma) dgamma[col] = s;
+    } else {
+        if (dbeta) dbeta[col - D] = s;
+    }
+}
+
+// ---- launches ---------------------------------------------------------------------
+
+int64_t min64(int64_t x, int64_t y) { return x < y ? x : y; }
+
+constexpr int64_t kMostGroups = 1 << 20;  // workgroups of a forward (a grid ends below 2^32 threads)
+constexpr int64_t kMostHeld = 32768;  // longest row that is held in registers
+constexpr int kParts = 512;           // most workgroups that hold partial sums
+
+// f(NT, V) for the threads and vectors that hold a row of D elements.
+template <typename F>
+hipError_t with_shape(int64_t D, F &&f) {
+#define ZI_SHAPE(NT, V) \
+    if (D <= (int64_t)NT * V * 8) return f(std::integral_constant<int, NT>{}, std::integral_constant<int, V>{})
+    ZI_SHAPE(16, 1);
+    ZI_SHAPE(64, 1);
+    ZI_SHAPE(64, 2);
+    ZI_SHAPE(256, 1);
+    ZI_SHAPE(256, 2);
+    ZI_SHAPE(1024, 1);
+    ZI_SHAPE(1024, 2);
+    ZI_SHAPE(1024, 3);
+    ZI_SHAPE(1024, 4);
+#undef ZI_SHAPE
+    return hipErrorInvalidValue;
+}
+
+template <typename XT, typename YT, bool RES>
+hipError_t run_fwd(const NormArgs &a, hipStream_t s) {
+    if (a.D > kMostHeld) {
+        hipLaunchKernelGGL((norm_fwd_long_kernel<XT, YT, RES>), dim3((unsigned)a.T), dim3(1024), 0, s, a);
+        return hipGetLastError();
+    }
+    return with_shape(a.D, [&](auto nt, auto v) {
+        constexpr int NT = decltype(nt)::value, V = decltype(v)::value;
+        const unsigned grid = (unsigned)min64((a.T + kRows<NT> - 1) / kRows<NT>, kMostGroups);
+        hipLaunchKernelGGL((norm_fwd_kernel<XT, YT, RES, NT, V>), dim3(grid), dim3(kBlock<NT>), 0, s, a);
+        return hipGetLastError();
+    });
+}
+
+template <typename XT, typename YT>
+hipError_t run_bwd(const NormArgs &a, float *dgamma, float *dbeta, hipStream_t s) {
+    int parts = 0;
+    hipError_t e = hipSuccess;
+    if (a.T > 0 && a.D > kMostHeld) {
+        if (a.part) {
+            parts = (int)min64(a.T, 64);
+            const dim3 grid((unsigned)((a.D + 2047) / 2048), (unsigned)parts);
+            hipLaunchKernelGGL((norm_cols_kernel<XT, YT>), grid, dim3(256), 0, s, a);
+            if ((e = hipGetLastError()) != hipSuccess) return e;
+        }
+        hipLaunchKernelGGL((norm_bwd_long_kernel<XT, YT>), dim3((unsigned)a.T), dim3(1024), 0, s, a);
+        if ((e = hipGetLastError()) != hipSuccess) return e;
+    } else if (a.T > 0) {
+        e = with_shape(a.D, [&](auto nt, auto v) {
+            constexpr int NT = decltype(nt)::value, V = decltype(v)::value;
+            parts = (int)min64((a.T + kRows<NT> - 1) / kRows<NT>, kParts);
+            hipLaunchKernelGGL((norm_bwd_kernel<XT, YT, NT, V>), dim3((unsigned)parts), dim3(kBlock<NT>), 0, s, a);
+            return hipGetLastError();
+        });
+        if (e != hipSuccess) return e;
+    }
+    if (!dgamma && !dbeta) return hipSuccess;
+    hipLaunchKernelGGL(norm_fold_kernel, dim3((unsigned)((2 * a.D + 63) / 64)), dim3(1024), 0, s, a.part, a.D, parts,
+                       dgamma, dbeta);
+    return hipGetLastError();
+}
+
+// f(type of X, type of Y) for the pairs of types that the operator takes: equal
+// ones, and either type in fp32 beside the other in 16 bits.
+template <typename F>
+hipError_t with_types(int32_t x, int32_t y, F &&f) {
+    if (x == ZI_F32 && y == ZI_F32) return f(float{}, float{});
+    if (x == ZI_F32 && y == ZI_F16) return f(float{}, f16_t{});
+    if (x == ZI_F32 && y == ZI_BF16) return f(float{}, bf16_t{});
+    if (x == ZI_F16 && y == ZI_F16) return f(f16_t{}, f16_t{});
+    if (x == ZI_F16 && y == ZI_F32) return f(f16_t{}, float{});
+    if (x == ZI_BF16 && y == ZI_BF16) return f(bf16_t{}, bf16_t{});
+    if (x == ZI_BF16 && y == ZI_F32) return f(bf16_t{}, float{});
+    return hipErrorInvalidValue;
+}
+
+bool known(int32_t d) { return d == ZI_F16 || d == ZI_BF16 || d == ZI_F32; }
+uint64_t size_of(int32_t d) { return d == ZI_F32 ? 4 : 2; }
+
+zi_status check(const zi_norm *n, NormArgs *a) {
+    if (!n) return fail(ZI_ERR_ARG, "norm is NULL");
+    if (n->T < 0 || n->T > INT32_MAX) return fail(ZI_ERR_SHAPE, "T = %lld: 0 .. 2^31 - 1 rows", (long long)n->T);
+    if (n->D < 1 || n->D > INT32_MAX) return fail(ZI_ERR_SHAPE, "D = %lld: 1 .. 2^31 - 1 columns", (long long)n->D);
+    if (!known(n->x_dtype) || !known(n->y_dtype) || !known(n->p_dtype))
+        return fail(ZI_ERR_ARG, "unknown dtype (x %d, y %d, p %d)", n->x_dtype, n->y_dtype, n->p_dtype);
+    if (n->x_dtype != n->y_dtype && n->x_dtype != ZI_F32 && n->y_dtype != ZI_F32)
+        return fail(ZI_ERR_ARG, "x_dtype and y_dtype are two different 16-bit types");
+    if (!(n->eps >= 0.f) || !(n->eps < INFINITY)) return fail(ZI_ERR_ARG, "eps = %g", (double)n->eps);
+    const int64_t ld[4] = {n->ldx, n->ldr, n->lds, n->ldy};
+    for (int64_t l : ld)
+        if (l != 0 && l < n->D) return fail(ZI_ERR_SHAPE, "a row stride of %lld is less than D", (long long)l);
+    *a = NormArgs{};
+    a->T = n->T;
+    a->D = n->D;
+    a->ldx = n->ldx ? n->ldx : n->D;
+    a->ldr = n->ldr ? n->ldr : n->D;
+    a->lds = n->lds ? n->lds : n->D;
+    a->ldy = n->ldy ? n->ldy : n->D;
+    a->eps = n->eps;
+    a->width = (float)n->D;
+    a->p_dtype = n->p_dtype;
+    return ZI_OK;
+}
+
+bool aligned(const void *p, uint64_t to) { return ((uintptr_t)p & (to - 1)) == 0; }
+
+}  // namespace
+
+extern "C" zi_status zi_layer_norm_fwd(const zi_norm *n, const void *X, const void *R, const void *gamma,
+                                       const void *beta, void *S, void *Y, float *mean, float *rstd, void *stream) {
+    clear_error();
+    NormArgs a;
+    zi_status st = check(n, &a);
+    if (st != ZI_OK) return st;
+    if (n->T == 0) return ZI_OK;
+    if (!X || !Y) return fail(ZI_ERR_ARG, "X and Y are required");
+    if (S && !R) return fail(ZI_ERR_ARG, "S is written with R only (without it, S is X)");
+    const uint64_t xs = size_of(n->x_dtype), ys = size_of(n->y_dtype), ps = size_of(n->p_dtype);
+    if (!aligned(X, xs) || !aligned(S, xs) || !aligned(R, ys) || !aligned(Y, ys) || !aligned(gamma, ps) ||
+        !aligned(beta, ps) || !aligned(mean, 4) || !aligned(rstd, 4))
+        return fail(ZI_ERR_ALIGN, "a pointer is not aligned to its element");
+    a.X = X;
+    a.R = R;
+    a.S = S;
+    a.Y = Y;
+    a.gamma = gamma;
+    a.beta = beta;
+    a.mean = mean;
+    a.rstd = rstd;
+    hipStream_t s = static_cast<hipStream_t>(stream);
+    const hipError_t e = with_types(n->x_dtype, n->y_dtype, [&](auto x, auto y) {
+        return R ? run_fwd<decltype(x), decltype(y), true>(a, s) : run_fwd<decltype(x), decltype(y), false>(a, s);
+    });
+    if (e != hipSuccess) return fail(ZI_ERR_HIP, "layer norm forward: %s", hipGetErrorString(e));
+    return ZI_OK;
+}
+
+extern "C" uint64_t zi_layer_norm_bwd_bytes(int64_t T, int64_t D) {
+    if (T < 0 || D < 1) return 0;
+    return (uint64_t)min64(T, kParts) * 2 * (uint64_t)D * 4;
+}
+
+extern "C" zi_status zi_layer_norm_bwd(const zi_norm *n, const void *dY, const void *S, const void *gamma,
+                                       const float *mean, const float *rstd, const void *dS, void *dX, float *dgamma,
+                                       float *dbeta, void *workspace, uint64_t workspace_bytes, void *stream) {
+    clear_error();
+    NormArgs a;
+    zi_status st = check(n, &a);
+    if (st != ZI_OK) return st;
+    if (n->T > 0 && (!dY || !S || !mean || !rstd || !dX))
+        return fail(ZI_ERR_ARG, "dY, S, mean, rstd and dX are required");
+    const uint64_t xs = size_of(n->x_dtype), ys = size_of(n->y_dtype), ps = size_of(n->p_dtype);
+    if (!aligned(S, xs) || !aligned(dS, xs) || !aligned(dX, xs) || !aligned(dY, ys) || !aligned(gamma, ps) ||
+        !aligned(mean, 4) || !aligned(rstd, 4) || !aligned(dgamma, 4) || !aligned(dbeta, 4))
+        return fail(ZI_ERR_ALIGN, "a pointer is not aligned to its element");
+    const bool sums = dgamma || dbeta;
+    if (sums && n->T > 0) {
+        const uint64_t need = zi_layer_norm_bwd_bytes(n->T, n->D);
+        if (!workspace || workspace_bytes < need)
+            return fail(ZI_ERR_BUDGET, "the workspace holds %llu B, dgamma and dbeta need %llu",
+                        (unsigned long long)(workspace ? workspace_bytes : 0), (unsigned long long)need);
+        if (!aligned(workspace, 256)) return fail(ZI_ERR_ALIGN, "the workspace is not 256-byte aligned");
+    }
+    a.S = const_cast<void *>(S);
+    a.Y = const_cast<void *>(dY);
+    a.gamma = gamma;
+    a.mean = const_cast<float *>(mean);
+    a.rstd = const_cast<float *>(rstd);
+    a.dS = dS;
+    a.dX = dX;
+    a.part = sums ? static_cast<float *>(workspace) : nullptr;
+    hipStream_t s = static_cast<hipStream_t>(stream);
+    const hipError_t e = with_types(n->x_dtype, n->y_dtype, [&](auto x, auto y) {
+        return run_bwd<decltype(x), decltype(y)>(a, dgamma, dbeta, s);
+    });
+    if (e != hipSuccess) return fail(ZI_ERR_HIP, "layer norm backward: %s", hipGetErrorString(e));
+    return ZI_OK;
+}

@@ -1,0 +1,96 @@
+// zi_vec.h -- device helpers of the row kernels (layer norm, embedding):
+// vectors of eight elements of fp32, fp16 or bf16, held as fp32.
+#pragma once
+
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include "../../include/zi.h"
+
+namespace zi {
+
+typedef _Float16 f16_t;
+typedef __bf16 bf16_t;
+
+// Rows start wherever their stride puts them, so vectors are only as aligned
+// as their elements; the hardware's global loads and stores take any address.
+typedef uint16_t u16x8_u __attribute__((ext_vector_type(8), aligned(2)));
+typedef float f32x4_u __attribute__((ext_vector_type(4), aligned(4)));
+
+template <typename T>
+__device__ __forceinline__ float to_f32(uint16_t b) {
+    return (float)__builtin_bit_cast(T, b);
+}
+
+// Eight consecutive elements.
+__device__ __forceinline__ void load8(const float *p, float (&v)[8]) {
+    const f32x4_u a = *reinterpret_cast<const f32x4_u *>(p), b = *reinterpret_cast<const f32x4_u *>(p + 4);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+        v[e] = a[e];
+        v[4 + e] = b[e];
+    }
+}
+template <typename T>
+__device__ __forceinline__ void load8(const T *p, float (&v)[8]) {
+    const u16x8_u a = *reinterpret_cast<const u16x8_u *>(p);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) v[e] = to_f32<T>(a[e]);
+}
+
+// One round to nearest even into T (none for fp32).
+__device__ __forceinline__ void store8(float *p, const float (&v)[8]) {
+    *reinterpret_cast<f32x4_u *>(p) = f32x4_u{v[0], v[1], v[2], v[3]};
+    *reinterpret_cast<f32x4_u *>(p + 4) = f32x4_u{v[4], v[5], v[6], v[7]};
+}
+template <typename T>
+__device__ __forceinline__ void store8(T *p, const float (&v)[8]) {
+    u16x8_u a;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) a[e] = __builtin_bit_cast(uint16_t, (T)v[e]);
+    *reinterpret_cast<u16x8_u *>(p) = a;
+}
+
+// The first n (any n; nothing at or below 0) of eight elements; the others
+// read as zero, and nothing past the n-th is touched.
+template <typename T>
+__device__ __forceinline__ void load_n(const T *p, int64_t n, float (&v)[8]) {
+    if (n >= 8) {
+        load8(p, v);
+    } else {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) v[e] = e < n ? (float)p[e] : 0.f;
+    }
+}
+template <typename T>
+__device__ __forceinline__ void store_n(T *p, int64_t n, const float (&v)[8]) {
+    if (n >= 8) {
+        store8(p, v);
+    } else {
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+            if (e < n) p[e] = (T)v[e];
+    }
+}
+
+// load_n of an array whose type is known at run time only (the same for
+// every lane).
+__device__ __forceinline__ void load_n(const void *p, int dtype, int64_t at, int64_t n, float (&v)[8]) {
+    if (dtype == ZI_F32)
+        load_n(static_cast<const float *>(p) + at, n, v);
+    else if (dtype == ZI_F16)
+        load_n(static_cast<const f16_t *>(p) + at, n, v);
+    else
+        load_n(static_cast<const bf16_t *>(p) + at, n, v);
+}
+
+// Sum over groups of N consecutive lanes (N a power of two, at most 64); every
+// lane gets it.
+template <int N>
+__device__ __forceinline__ float lane_sum(float x) {
+#pragma unroll
+    for (int m = 1; m < N; m <<= 1) x += __shfl_xor(x, m, 64);
+    return x;
+}
+
+}  // namespace zi

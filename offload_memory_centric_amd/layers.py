@@ -1,0 +1,147 @@
+"""What a training step runs on the device around the tiled block, for torch tensors.
+
+Layer norm with the residual sum, the token embedding and its gradient, each
+in its forward and its backward call over caller-owned outputs; every step
+runs in libzi.so.  Calls enqueue on ``stream`` (a torch stream or a handle such
+as ``Context.streams[0]``; by default torch's current stream) and return at
+once.  As with any stream, tensors made on another one must be complete
+before, and be kept until the work is done.
+"""
+from __future__ import annotations
+
+import torch
+
+from . import zi
+
+_CODES = {torch.float16: zi.ZI_F16, torch.bfloat16: zi.ZI_BF16, torch.float32: zi.ZI_F32}
+
+
+def workspace(nbytes: int, device="cuda") -> torch.Tensor:
+    """Device memory for a call's workspace; one per stream that may run such calls."""
+    return torch.empty(max(int(nbytes), 256), dtype=torch.uint8, device=device)
+
+
+def _code(t, name: str) -> int:
+    code = _CODES.get(t.dtype)
+    if code is None:
+        raise TypeError("%s has dtype %s, expected float16, bfloat16 or float32" % (name, t.dtype))
+    return code
+
+
+def _here(t, name: str) -> None:
+    if t.device.type != "cuda":
+        raise ValueError("%s must be a device tensor" % name)
+
+
+def _rows(t, rows: int, cols: int, name: str, dtype=None) -> int:
+    """The row stride of a [rows, cols] device tensor whose rows are contiguous."""
+    if dtype is not None and t.dtype != dtype:
+        raise TypeError("%s has dtype %s, expected %s" % (name, t.dtype, dtype))
+    _here(t, name)
+    if t.dim() != 2 or t.shape[0] != rows or t.shape[1] != cols:
+        raise ValueError("%s has shape %s, expected (%d, %d)" % (name, tuple(t.shape), rows, cols))
+    if cols > 1 and t.stride(1) != 1:
+        raise ValueError("the rows of %s must be contiguous" % name)
+    ld = t.stride(0) if rows > 1 else cols
+    if ld < cols:
+        raise ValueError("the rows of %s overlap" % name)
+    return ld
+
+
+def _vector(t, n: int, name: str, dtype=None) -> None:
+    if dtype is not None and t.dtype != dtype:
+        raise TypeError("%s has dtype %s, expected %s" % (name, t.dtype, dtype))
+    _here(t, name)
+    if t.dim() != 1 or t.shape[0] != n or (n > 1 and t.stride(0) != 1):
+        raise ValueError("%s must be a contiguous vector of %d elements" % (name, n))
+
+
+def _bytes(work) -> int:
+    if work is None:
+        return 0
+    _here(work, "work")
+    if not work.is_contiguous():
+        raise ValueError("work must be contiguous")
+    return work.numel() * work.element_size()
+
+
+def _on(stream, t):
+    return torch.cuda.current_stream(t.device) if stream is None else stream
+
+
+def _matrix(t, name: str):
+    if t.dim() != 2:
+        raise ValueError("%s must be a matrix" % name)
+    return t.shape
+
+
+def _params(gamma, beta, D: int) -> int:
+    code = zi.ZI_F32
+    for t, name in ((gamma, "gamma"), (beta, "beta")):
+        if t is not None:
+            _vector(t, D, name)
+            code = _code(t, name)
+    if gamma is not None and beta is not None and gamma.dtype != beta.dtype:
+        raise TypeError("gamma and beta have different dtypes")
+    return code
+
+
+def layer_norm_fwd(X, gamma, beta, Y, mean=None, rstd=None, eps: float = 1e-5, R=None, S=None, stream=None) -> None:
+    """S = X + R (S = X without R), Y = (S - mean) * rstd * gamma + beta over rows (zi_layer_norm_fwd).
+
+    X and S, the residual stream, share a dtype; R and Y, the block's side, another: the two are equal or one
+    of them is fp32.  gamma, beta, mean, rstd and S (with R) may be None."""
+    T, D = _matrix(X, "X")
+    ldx, ldy = _rows(X, T, D, "X"), _rows(Y, T, D, "Y")
+    ldr = 0 if R is None else _rows(R, T, D, "R", Y.dtype)
+    lds = 0 if S is None else _rows(S, T, D, "S", X.dtype)
+    for t, name in ((mean, "mean"), (rstd, "rstd")):
+        if t is not None:
+            _vector(t, T, name, torch.float32)
+    norm = zi.zi_norm(T, D, ldx, ldr, lds, ldy, _code(X, "X"), _code(Y, "Y"), _params(gamma, beta, D), eps)
+    zi.zi_layer_norm_fwd(norm, X, R, gamma, beta, S, Y, mean, rstd, _on(stream, X))
+
+
+def layer_norm_bwd_bytes(T: int, D: int) -> int:
+    """Workspace bytes of layer_norm_bwd."""
+    return zi.zi_layer_norm_bwd_bytes(T, D)
+
+
+def layer_norm_bwd(dY, S, gamma, mean, rstd, dX, dgamma, dbeta, work, dS=None, stream=None) -> None:
+    """dX, dgamma and dbeta of layer_norm_fwd's Y, plus dS, the gradient that reaches S past the norm
+    (zi_layer_norm_bwd).  dgamma and dbeta are fp32 and overwritten; both None: not formed, and work unused."""
+    T, D = _matrix(S, "S")
+    lds, ldy, ldx = _rows(S, T, D, "S"), _rows(dY, T, D, "dY"), _rows(dX, T, D, "dX", S.dtype)
+    ldr = 0 if dS is None else _rows(dS, T, D, "dS", S.dtype)
+    _vector(mean, T, "mean", torch.float32)
+    _vector(rstd, T, "rstd", torch.float32)
+    for t, name in ((dgamma, "dgamma"), (dbeta, "dbeta")):
+        if t is not None:
+            _vector(t, D, name, torch.float32)
+    norm = zi.zi_norm(T, D, ldx, ldr, lds, ldy, _code(S, "S"), _code(dY, "dY"), _params(gamma, None, D), 0.0)
+    zi.zi_layer_norm_bwd(norm, dY, S, gamma, mean, rstd, dS, dX, dgamma, dbeta, work, _bytes(work), _on(stream, S))
+
+
+def _embedding(ids, W, X, scale, accumulate, names) -> zi.zi_embedding:
+    if ids.dtype not in (torch.int32, torch.int64):
+        raise TypeError("ids has dtype %s, expected int32 or int64" % ids.dtype)
+    (V, D), T = _matrix(W, names[0]), ids.numel()
+    _vector(ids, T, "ids")
+    return zi.zi_embedding(T, V, D, _rows(W, V, D, names[0]), _rows(X, T, D, names[1]), _code(W, names[0]),
+                           _code(X, names[1]), ids.dtype == torch.int64, scale, accumulate)
+
+
+def embedding_fwd(ids, W, X, scale: float = 1.0, stream=None) -> None:
+    """X[t] = scale * W[ids[t]] (zi_embedding_fwd); an id outside the table gives a zero row."""
+    zi.zi_embedding_fwd(_embedding(ids, W, X, scale, False, ("W", "X")), ids, W, X, _on(stream, W))
+
+
+def embedding_bwd_bytes(T: int, V: int, D: int) -> int:
+    """Workspace bytes of embedding_bwd."""
+    return zi.zi_embedding_bwd_bytes(T, V, D)
+
+
+def embedding_bwd(ids, dX, dW, work, scale: float = 1.0, accumulate: bool = False, stream=None) -> None:
+    """dW[v] = scale * sum of dX[t] over ids[t] == v, added to dW with ``accumulate`` (zi_embedding_bwd)."""
+    zi.zi_embedding_bwd(_embedding(ids, dW, dX, scale, accumulate, ("dW", "dX")), ids, dX, dW, work, _bytes(work),
+                        _on(stream, dW))

@@ -19,7 +19,7 @@ LIB_PATH = os.path.join(_HERE, "libzi.so")
  ZI_ERR_IO) = range(9)
 STATUS_NAMES = ["ZI_OK", "ZI_ERR_ARG", "ZI_ERR_SHAPE", "ZI_ERR_BUDGET", "ZI_ERR_NOT_PINNED",
                 "ZI_ERR_ALIGN", "ZI_ERR_HIP", "ZI_ERR_STATE", "ZI_ERR_IO"]
-ZI_F16, ZI_BF16 = 1, 2
+ZI_F16, ZI_BF16, ZI_F32 = 1, 2, 3
 ZI_FLAG_F32_OUT = 0x1
 ZI_NOALLOC_SCRATCH_BYTES = 64 << 20  # static tile buffer of zi_tiled_linear_fwd_noalloc
 DTYPE_CODES = {"f16": ZI_F16, "bf16": ZI_BF16}
@@ -97,6 +97,18 @@ class zi_tier_stats(ctypes.Structure):
 
     def as_dict(self) -> dict:
         return {k: getattr(self, k) for k, _ in self._fields_}
+
+
+class zi_norm(ctypes.Structure):
+    _fields_ = [("T", ctypes.c_int64), ("D", ctypes.c_int64), ("ldx", ctypes.c_int64), ("ldr", ctypes.c_int64),
+                ("lds", ctypes.c_int64), ("ldy", ctypes.c_int64), ("x_dtype", ctypes.c_int32),
+                ("y_dtype", ctypes.c_int32), ("p_dtype", ctypes.c_int32), ("eps", ctypes.c_float)]
+
+
+class zi_embedding(ctypes.Structure):
+    _fields_ = [("T", ctypes.c_int64), ("V", ctypes.c_int64), ("D", ctypes.c_int64), ("ldw", ctypes.c_int64),
+                ("ldx", ctypes.c_int64), ("w_dtype", ctypes.c_int32), ("x_dtype", ctypes.c_int32),
+                ("ids64", ctypes.c_int32), ("scale", ctypes.c_float), ("accumulate", ctypes.c_int32)]
 
 
 ZI_STATS_KERNELS = 16
@@ -204,6 +216,12 @@ _sigs = {
     "zi_tier_trace_get": (_S, [_P, ctypes.POINTER(ctypes.c_int64), ctypes.c_int64, ctypes.POINTER(ctypes.c_int64)]),
     "zi_tier_simulate_reads": (_S, [ctypes.POINTER(ctypes.c_int64), ctypes.c_int64, ctypes.c_int32, ctypes.c_int32,
                                     ctypes.c_int32, ctypes.POINTER(ctypes.c_int64)]),
+    "zi_layer_norm_fwd": (_S, [ctypes.POINTER(zi_norm)] + [_P] * 9),
+    "zi_layer_norm_bwd_bytes": (ctypes.c_uint64, [ctypes.c_int64, ctypes.c_int64]),
+    "zi_layer_norm_bwd": (_S, [ctypes.POINTER(zi_norm)] + [_P] * 10 + [ctypes.c_uint64, _P]),
+    "zi_embedding_fwd": (_S, [ctypes.POINTER(zi_embedding), _P, _P, _P, _P]),
+    "zi_embedding_bwd_bytes": (ctypes.c_uint64, [ctypes.c_int64, ctypes.c_int64, ctypes.c_int64]),
+    "zi_embedding_bwd": (_S, [ctypes.POINTER(zi_embedding), _P, _P, _P, _P, ctypes.c_uint64, _P]),
     "zi_host_alloc": (_S, [ctypes.c_uint64, ctypes.POINTER(_P)]),
     "zi_host_free": (_S, [_P]),
     "zi_last_error": (ctypes.c_char_p, []),
@@ -497,6 +515,35 @@ def zi_tier_simulate_reads(trace, buffers: int, steps: int, window: int = 0) -> 
     out = (ctypes.c_int64 * max(1, int(steps)))()
     _check(_lib.zi_tier_simulate_reads(t, len(trace), int(buffers), int(window or buffers), int(steps), out))
     return list(out[:int(steps)])
+
+
+def zi_layer_norm_fwd(norm: zi_norm, X, R, gamma, beta, S, Y, mean, rstd, stream=None) -> None:
+    _check(_lib.zi_layer_norm_fwd(ctypes.byref(norm), _ptr(X), _ptr(R), _ptr(gamma), _ptr(beta), _ptr(S), _ptr(Y),
+                                  _ptr(mean), _ptr(rstd), _stream(stream)))
+
+
+def zi_layer_norm_bwd_bytes(T: int, D: int) -> int:
+    return int(_lib.zi_layer_norm_bwd_bytes(int(T), int(D)))
+
+
+def zi_layer_norm_bwd(norm: zi_norm, dY, S, gamma, mean, rstd, dS, dX, dgamma, dbeta, workspace,
+                      workspace_bytes: int, stream=None) -> None:
+    _check(_lib.zi_layer_norm_bwd(ctypes.byref(norm), _ptr(dY), _ptr(S), _ptr(gamma), _ptr(mean), _ptr(rstd),
+                                  _ptr(dS), _ptr(dX), _ptr(dgamma), _ptr(dbeta), _ptr(workspace),
+                                  int(workspace_bytes), _stream(stream)))
+
+
+def zi_embedding_fwd(emb: zi_embedding, ids, W, X, stream=None) -> None:
+    _check(_lib.zi_embedding_fwd(ctypes.byref(emb), _ptr(ids), _ptr(W), _ptr(X), _stream(stream)))
+
+
+def zi_embedding_bwd_bytes(T: int, V: int, D: int) -> int:
+    return int(_lib.zi_embedding_bwd_bytes(int(T), int(V), int(D)))
+
+
+def zi_embedding_bwd(emb: zi_embedding, ids, dX, dW, workspace, workspace_bytes: int, stream=None) -> None:
+    _check(_lib.zi_embedding_bwd(ctypes.byref(emb), _ptr(ids), _ptr(dX), _ptr(dW), _ptr(workspace),
+                                 int(workspace_bytes), _stream(stream)))
 
 
 def zi_host_alloc(nbytes: int) -> int:
