@@ -742,6 +742,29 @@ uint64_t zi_embedding_bwd_bytes(int64_t T, int64_t V, int64_t D);
 zi_status zi_embedding_bwd(const zi_embedding *emb, const void *ids, const void *dX, void *dW, void *workspace,
                            uint64_t workspace_bytes, void *stream);
 
+/* Orthogonalising an update (as the Muon optimiser does): X = G / (|G| + eps),
+ * |G| the root of the sum of squares; then `steps` times
+ *   A = X X^T (X^T X where G has more rows than columns),
+ *   X <- a X + (b A + c A^2) X (X (b A + c A^2)),
+ * which acts on the singular values of X by an odd polynomial; O = RNE(X) in
+ * bf16.  The products take fp16 operands and fp32 sums; what X carries over
+ * from step to step is held in 22 bits.  O is within about 1e-3 |O| of the
+ * exact polynomial, so that bf16 holds all of its accuracy.  With NaN or an
+ * infinity in G, O is NaN; with G zero, O is zero.  O overlaps neither G nor
+ * the workspace. */
+#define ZI_ORTH_MOST 262144
+typedef struct {
+    int64_t M, K;      /* rows and columns of G and O: 1 .. ZI_ORTH_MOST      */
+    int64_t ldg, ldo;  /* row strides; 0 = K                                  */
+    int32_t dtype;     /* G: zi_dtype                                         */
+    int32_t steps;     /* 1 .. 100; usually 5                                 */
+    float a, b, c;     /* usually 3.4445, -4.7750, 2.0315                     */
+    float eps;         /* >= 0; usually 1e-7                                  */
+} zi_orth;
+uint64_t zi_orthogonalize_bytes(int64_t M, int64_t K);
+zi_status zi_orthogonalize(const zi_orth *orth, const void *G, void *O, void *workspace, uint64_t workspace_bytes,
+                           void *stream);
+
 /* Page-locked host memory (hipHostMalloc) for W^t / dW^t; 4096-byte aligned. */
 zi_status zi_host_alloc(uint64_t bytes, void **out);
 zi_status zi_host_free(void *ptr);

@@ -18,7 +18,9 @@ OBJDIR = os.path.join(HERE, "_build")
 
 ARCH = "gfx950"
 SOURCES = ["zi_kernels.hip", "zi_api.cpp", "zi_plan.cpp", "zi_adam.cpp", "zi_source.cpp", "zi_noalloc.hip",
-           "zi_norm.hip", "zi_embed.hip"]
+           "zi_norm.hip", "zi_embed.hip", "zi_orth.hip", "zi_orth_gemm.hip"]
+# sources with matrix-core instructions in inline assembly
+MFMA_SOURCES = ["zi_kernels.hip", "zi_orth_gemm.hip"]
 COMMON = ["-O3", "-std=c++17", "-fPIC", "-Wall", "-Wno-unused-function",
           "-I" + os.path.join(ROOT, "include")]
 # Packed fp32 VALU forms are kept out of every device code object.
@@ -82,7 +84,8 @@ def build(verbose: bool = False) -> str:
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError("link failed: %s\n%s\n%s" % (" ".join(cmd), r.stdout, r.stderr))
-    check_device_asm()
+    for src in MFMA_SOURCES:
+        check_device_asm(src)
     os.replace(tmp, LIB)
     if verbose:
         print("built", LIB)

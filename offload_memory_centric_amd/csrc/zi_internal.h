@@ -55,6 +55,43 @@ struct GemmArgs {
 // dtype: 1 = fp16, 2 = bf16.  Returns the launch status (hipGetLastError).
 hipError_t launch_gemm(GemmOp op, int dtype, const GemmArgs &a, hipStream_t stream);
 
+// A step x <- a x + (b A + c A^2) x, A = x x^T, of the orthogonalised update
+// (zi_orth.hip).  Matrices are kept with their diagonals apart: A = D + O, with
+// D in fp32 and O (zero on the diagonal) in fp16 as an operand and in fp32 for
+// the linear term; likewise a + bA + cA^2 = diag(bd) + B.
+//   Gram   acc = x x^T        D, O (C: fp16, o32: fp32 on and below the diagonal)
+//   Poly   acc = O O          bd, B (C: fp16)
+//   Apply  acc = B x          x (hi, lo: two fp16 planes), or `out` after the last step
+// The first two are symmetric: tiles on and below the diagonal are formed, and
+// those below it written on both sides.
+enum class OrthOp : int { Gram = 0, Poly = 1, Apply = 2 };
+struct OrthArgs : GemmArgs {
+    int32_t pieces;       // workgroups that share the reduction of each of the last split_tail tiles
+    const float *scale;   // Gram, Apply: true x = *scale times the planes
+    float ca, cb, cc;     // a, b, c
+    float *o32;           // [rows][ldc], as O
+    float *diag, *bdiag;  // D, bd
+    const uint16_t *hi;   // Apply: the planes of x, [rows][ldc]
+    uint16_t *lo;
+    uint16_t *hi_out;     // the new planes (lo is replaced in place); null: write `out`
+    uint16_t *out;        // bf16
+    int64_t out_p, out_q, out_ld;  // its extents along p and q, and its row stride
+    int32_t out_t;                 // it is stored transposed: element (p, q) at out[q * out_ld + p]
+};
+
+// One of the products, on 256 x 256 tiles or (large false) 128 x 128 ones.  rows,
+// cols and red are multiples of 64.  split_part holds orth_split_bytes(large) and
+// split_cnt kOrthSplits counters, zero between launches.
+hipError_t launch_orth(OrthOp op, bool large, const OrthArgs &a, hipStream_t stream);
+
+// Tiles of a launch whose reduction is split, and their pieces: at most one
+// workgroup a compute unit with large tiles, two with small ones.
+constexpr int kOrthUnits = 256;
+constexpr int kOrthSplits = 2 * kOrthUnits;
+constexpr uint64_t orth_split_bytes(bool large) {
+    return large ? (uint64_t)kOrthUnits * 256 * 256 * 4 : (uint64_t)kOrthSplits * 128 * 128 * 4;
+}
+
 // Workgroups (one macro-tile each) that launch_gemm runs for a product with
 // `rows` output rows and `cols` output columns: the macro-tile is 256 x 256,
 // or 192 x 320 / 320 x 192 (rows x columns) where that tile covers a forward's

@@ -1,8 +1,8 @@
 """What a training step runs on the device around the tiled block, for torch tensors.
 
 Layer norm with the residual sum, the token embedding and its gradient, each
-in its forward and its backward call over caller-owned outputs; every step
-runs in libzi.so.  Calls enqueue on ``stream`` (a torch stream or a handle such
+in its forward and its backward call, and the orthogonalised update of a
+weight, over caller-owned outputs; every step runs in libzi.so.  Calls enqueue on ``stream`` (a torch stream or a handle such
 as ``Context.streams[0]``; by default torch's current stream) and return at
 once.  As with any stream, tensors made on another one must be complete
 before, and be kept until the work is done.
@@ -145,3 +145,18 @@ def embedding_bwd(ids, dX, dW, work, scale: float = 1.0, accumulate: bool = Fals
     """dW[v] = scale * sum of dX[t] over ids[t] == v, added to dW with ``accumulate`` (zi_embedding_bwd)."""
     zi.zi_embedding_bwd(_embedding(ids, dW, dX, scale, accumulate, ("dW", "dX")), ids, dX, dW, work, _bytes(work),
                         _on(stream, dW))
+
+
+def orthogonalize_bytes(M: int, K: int) -> int:
+    """Workspace bytes of orthogonalize."""
+    return zi.zi_orthogonalize_bytes(M, K)
+
+
+def orthogonalize(G, O, work, steps: int = 5, coeffs=(3.4445, -4.7750, 2.0315), eps: float = 1e-7,
+                  stream=None) -> None:
+    """O (bf16) = the update G with its singular values driven towards one by `steps` Newton-Schulz steps
+    (zi_orthogonalize)."""
+    M, K = _matrix(G, "G")
+    a, b, c = coeffs
+    orth = zi.zi_orth(M, K, _rows(G, M, K, "G"), _rows(O, M, K, "O", torch.bfloat16), _code(G, "G"), steps, a, b, c, eps)
+    zi.zi_orthogonalize(orth, G, O, work, _bytes(work), _on(stream, G))

@@ -111,6 +111,13 @@ class zi_embedding(ctypes.Structure):
                 ("ids64", ctypes.c_int32), ("scale", ctypes.c_float), ("accumulate", ctypes.c_int32)]
 
 
+class zi_orth(ctypes.Structure):
+    _fields_ = [("M", ctypes.c_int64), ("K", ctypes.c_int64), ("ldg", ctypes.c_int64), ("ldo", ctypes.c_int64),
+                ("dtype", ctypes.c_int32), ("steps", ctypes.c_int32), ("a", ctypes.c_float), ("b", ctypes.c_float),
+                ("c", ctypes.c_float), ("eps", ctypes.c_float)]
+
+
+ZI_ORTH_MOST = 262144
 ZI_STATS_KERNELS = 16
 
 
@@ -222,6 +229,8 @@ _sigs = {
     "zi_embedding_fwd": (_S, [ctypes.POINTER(zi_embedding), _P, _P, _P, _P]),
     "zi_embedding_bwd_bytes": (ctypes.c_uint64, [ctypes.c_int64, ctypes.c_int64, ctypes.c_int64]),
     "zi_embedding_bwd": (_S, [ctypes.POINTER(zi_embedding), _P, _P, _P, _P, ctypes.c_uint64, _P]),
+    "zi_orthogonalize_bytes": (ctypes.c_uint64, [ctypes.c_int64, ctypes.c_int64]),
+    "zi_orthogonalize": (_S, [ctypes.POINTER(zi_orth), _P, _P, _P, ctypes.c_uint64, _P]),
     "zi_host_alloc": (_S, [ctypes.c_uint64, ctypes.POINTER(_P)]),
     "zi_host_free": (_S, [_P]),
     "zi_last_error": (ctypes.c_char_p, []),
@@ -544,6 +553,15 @@ def zi_embedding_bwd_bytes(T: int, V: int, D: int) -> int:
 def zi_embedding_bwd(emb: zi_embedding, ids, dX, dW, workspace, workspace_bytes: int, stream=None) -> None:
     _check(_lib.zi_embedding_bwd(ctypes.byref(emb), _ptr(ids), _ptr(dX), _ptr(dW), _ptr(workspace),
                                  int(workspace_bytes), _stream(stream)))
+
+
+def zi_orthogonalize_bytes(M: int, K: int) -> int:
+    return int(_lib.zi_orthogonalize_bytes(int(M), int(K)))
+
+
+def zi_orthogonalize(orth: zi_orth, G, O, workspace, workspace_bytes: int, stream=None) -> None:
+    _check(_lib.zi_orthogonalize(ctypes.byref(orth), _ptr(G), _ptr(O), _ptr(workspace), int(workspace_bytes),
+                                 _stream(stream)))
 
 
 def zi_host_alloc(nbytes: int) -> int:

@@ -128,6 +128,41 @@ def test_embedding_workspace(zi):
     refused(zi, "ZI_ERR_ALIGN", zi.zi_embedding_bwd, p, A, A, A, A + 128, need)
 
 
+def orth(zi, **kw):
+    d = dict(M=100, K=40, ldg=0, ldo=0, dtype=zi.ZI_BF16, steps=5, a=3.4445, b=-4.775, c=2.0315, eps=1e-7)
+    d.update(kw)
+    return zi.zi_orth(*[d[k] for k, _ in zi.zi_orth._fields_])
+
+
+ORTH_BAD = [
+    (dict(M=0), "ZI_ERR_SHAPE"), (dict(K=0), "ZI_ERR_SHAPE"), (dict(M=262145), "ZI_ERR_SHAPE"),
+    (dict(K=262145), "ZI_ERR_SHAPE"), (dict(ldg=39), "ZI_ERR_SHAPE"), (dict(ldo=-1), "ZI_ERR_SHAPE"),
+    (dict(dtype=0), "ZI_ERR_ARG"), (dict(dtype=4), "ZI_ERR_ARG"), (dict(steps=0), "ZI_ERR_ARG"),
+    (dict(steps=101), "ZI_ERR_ARG"), (dict(a=float("nan")), "ZI_ERR_ARG"), (dict(b=float("inf")), "ZI_ERR_ARG"),
+    (dict(c=float("inf")), "ZI_ERR_ARG"), (dict(eps=-1e-7), "ZI_ERR_ARG"), (dict(eps=float("nan")), "ZI_ERR_ARG"),
+]
+
+
+@pytest.mark.parametrize("bad,status", ORTH_BAD)
+def test_orth_problem(zi, bad, status):
+    refused(zi, status, zi.zi_orthogonalize, orth(zi, **bad), A, A, A, 1 << 40)
+
+
+def test_orth_pointers_and_workspace(zi):
+    o = orth(zi)
+    need = zi.zi_orthogonalize_bytes(100, 40)
+    assert need > 0 and zi.zi_orthogonalize_bytes(0, 40) == 0 and zi.zi_orthogonalize_bytes(40, 262145) == 0
+    refused(zi, "ZI_ERR_ARG", zi.zi_orthogonalize, o, None, A, A, need)
+    refused(zi, "ZI_ERR_ARG", zi.zi_orthogonalize, o, A, None, A, need)
+    refused(zi, "ZI_ERR_ALIGN", zi.zi_orthogonalize, o, A + 1, A, A, need)
+    refused(zi, "ZI_ERR_ALIGN", zi.zi_orthogonalize, o, A, A + 1, A, need)
+    refused(zi, "ZI_ERR_ALIGN", zi.zi_orthogonalize, o, A, A, A + 128, need)
+    refused(zi, "ZI_ERR_BUDGET", zi.zi_orthogonalize, o, A, A, A, need - 1)
+    refused(zi, "ZI_ERR_BUDGET", zi.zi_orthogonalize, o, A, A, None, need)
+    null = ctypes.POINTER(zi.zi_orth)()
+    assert zi._lib.zi_orthogonalize(null, A, A, A, need, None) == zi.ZI_ERR_ARG
+
+
 def test_nothing_to_do(zi):
     """No rows: no launch, so these pass without a GPU."""
     zi.zi_layer_norm_fwd(norm(zi, T=0), None, None, None, None, None, None, None, None)
@@ -157,7 +192,7 @@ def test_structs_match_the_header(zi, tmp_path):
     if shutil.which("gcc") is None:
         pytest.skip("needs gcc")
     root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
-    structs = ["zi_norm", "zi_embedding"]
+    structs = ["zi_norm", "zi_embedding", "zi_orth"]
     body = ""
     for name in structs:
         body += 'printf("%s . %%zu\\n", sizeof(%s));' % (name, name)
