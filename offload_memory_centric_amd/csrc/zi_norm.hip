@@ -40,7 +40,9 @@ struct NormArgs {
 };
 
 // Sum over the NT threads that hold a row; every one of them gets it.  `slots`:
-// LDS words of this sum alone (NT / 64 of them), so that one barrier is enough.
+// LDS words (NT / 64 of them).  One barrier is enough where two sums that take
+// turns use different words: a wave that writes one sum's words has passed the
+// other's barrier, which no wave reaches before it has read this one's last.
 template <int NT>
 __device__ __forceinline__ float row_sum(float x, float *slots) {
     if constexpr (NT <= 64) return lane_sum<NT>(x);
@@ -58,78 +60,90 @@ constexpr int kRows = NT < 256 ? 256 / NT : 1;  // rows of a workgroup at a time
 template <int NT>
 constexpr int kBlock = NT < 256 ? 256 : NT;
 
-template <typename XT, typename YT, bool RES, int NT, int V>
+// The vectors of one thread's share of a row of D >= 8 elements: vector c
+// covers elements [at, at + 8), and the row's last one is moved back to end
+// with the row, as are those past its end, so that every load and store is a
+// whole vector and none needs a branch.  Elements that a vector shares with the
+// one before it then have the same value in both threads; sums leave them out
+// (own).  The first FULL vectors lie in the row as they are, for every D that
+// takes this shape.
+template <int NT, int FULL>
+struct Share {
+    int t, D;
+    __device__ __forceinline__ int at(int c) const {
+        const int i = (c * NT + t) * 8;
+        return NT > 64 && c < FULL ? i : min(i, D - 8);
+    }
+    __device__ __forceinline__ bool own(int c, int e) const {
+        return (NT > 64 && c < FULL) || at(c) + e >= (c * NT + t) * 8;
+    }
+};
+
+template <typename XT, typename YT, bool RES, int NT, int V, int FULL>
 __global__ __launch_bounds__(kBlock<NT>) void norm_fwd_kernel(NormArgs a) {
-    __shared__ float slots[2][2][NT <= 64 ? 1 : NT / 64];
-    const int t = threadIdx.x % NT;
-    int par = 0;  // two rows in a row use different slots
-    for (int64_t at = (int64_t)blockIdx.x * kRows<NT>; at < a.T; at += (int64_t)gridDim.x * kRows<NT>, par ^= 1) {
-        const int64_t row = at + threadIdx.x / NT;
-        const int64_t D = row < a.T ? a.D : 0;  // past the last row: no elements
+    __shared__ float slots[2][NT <= 64 ? 1 : NT / 64];
+    const int sub = kRows<NT> == 1 ? 0 : threadIdx.x / NT;
+    const Share<NT, FULL> my{kRows<NT> == 1 ? (int)threadIdx.x : (int)threadIdx.x % NT, (int)a.D};
+    for (int64_t first = (int64_t)blockIdx.x * kRows<NT>; first < a.T; first += (int64_t)gridDim.x * kRows<NT>) {
+        const bool live = first + sub < a.T;
+        const int64_t row = live ? first + sub : a.T - 1;
         const XT *x = static_cast<const XT *>(a.X) + row * a.ldx;
         const YT *r = static_cast<const YT *>(a.R) + row * a.ldr;
         XT *sp = static_cast<XT *>(a.S) + row * a.lds;
         YT *y = static_cast<YT *>(a.Y) + row * a.ldy;
-        float s[V][8];
+        Raw8<XT> xr[V];
+        Raw8<YT> rr[V];
 #pragma unroll
         for (int c = 0; c < V; ++c) {
-            const int64_t i = (int64_t)(t + c * NT) * 8;
-            load_n(x + i, D - i, s[c]);
+            xr[c].load(x + my.at(c));
+            if constexpr (RES) rr[c].load(r + my.at(c));
         }
-        if constexpr (RES) {
-            float u[V][8];
-#pragma unroll
-            for (int c = 0; c < V; ++c) {
-                const int64_t i = (int64_t)(t + c * NT) * 8;
-                load_n(r + i, D - i, u[c]);
-            }
-#pragma unroll
-            for (int c = 0; c < V; ++c) {
-                const int64_t i = (int64_t)(t + c * NT) * 8;
-                // the statistics are those of the stored sum, which the backward reads
-#pragma unroll
-                for (int e = 0; e < 8; ++e) s[c][e] = (float)(XT)(s[c][e] + u[c][e]);
-                if (a.S) store_n(sp + i, D - i, s[c]);
-            }
-        }
-        float sum = 0.f;
+        float s[V][8], sum = 0.f;
 #pragma unroll
         for (int c = 0; c < V; ++c)
 #pragma unroll
-            for (int e = 0; e < 8; ++e) sum += s[c][e];
-        const float mean = row_sum<NT>(sum, slots[par][0]) / a.width;
+            for (int e = 0; e < 8; ++e) {
+                s[c][e] = xr[c][e];
+                // the statistics are those of the stored sum, which the backward reads
+                if constexpr (RES) s[c][e] = (float)(XT)(s[c][e] + rr[c][e]);
+                sum += my.own(c, e) ? s[c][e] : 0.f;
+            }
+        const float mean = row_sum<NT>(sum, slots[0]) / a.width;
+        if constexpr (RES) {  // the row has been read: S may replace X or R
+            if (a.S && live) {
+#pragma unroll
+                for (int c = 0; c < V; ++c) store8(sp + my.at(c), s[c]);
+            }
+        }
         float sq = 0.f;
 #pragma unroll
-        for (int c = 0; c < V; ++c) {
-            const int64_t i = (int64_t)(t + c * NT) * 8;
+        for (int c = 0; c < V; ++c)
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
                 s[c][e] -= mean;
-                if (i + e < D) sq += s[c][e] * s[c][e];
+                sq += my.own(c, e) ? s[c][e] * s[c][e] : 0.f;
             }
-        }
-        const float rstd = 1.0f / sqrtf(row_sum<NT>(sq, slots[par][1]) / a.width + a.eps);
-        if (t == 0 && row < a.T) {
+        const float rstd = 1.0f / sqrtf(row_sum<NT>(sq, slots[1]) / a.width + a.eps);
+        if (my.t == 0 && live) {
             if (a.mean) a.mean[row] = mean;
             if (a.rstd) a.rstd[row] = rstd;
         }
 #pragma unroll
         for (int c = 0; c < V; ++c) {
-            const int64_t i = (int64_t)(t + c * NT) * 8;
-            float g[8], b[8];
+            float g[8];
 #pragma unroll
             for (int e = 0; e < 8; ++e) s[c][e] *= rstd;
             if (a.gamma) {
-                load_n(a.gamma, a.p_dtype, i, D - i, g);
+                load8(a.gamma, a.p_dtype, my.at(c), g);
 #pragma unroll
                 for (int e = 0; e < 8; ++e) s[c][e] *= g[e];
             }
             if (a.beta) {
-                load_n(a.beta, a.p_dtype, i, D - i, b);
+                load8(a.beta, a.p_dtype, my.at(c), g);
 #pragma unroll
-                for (int e = 0; e < 8; ++e) s[c][e] += b[e];
+                for (int e = 0; e < 8; ++e) s[c][e] += g[e];
             }
-            store_n(y + i, D - i, s[c]);
+            if (live) store8(y + my.at(c), s[c]);
         }
     }
 }
@@ -139,123 +153,159 @@ template <typename XT, typename YT, bool RES>
 __global__ __launch_bounds__(1024) void norm_fwd_long_kernel(NormArgs a) {
     constexpr int NT = 1024;
     __shared__ float slots[2][NT / 64];
-    const int64_t row = blockIdx.x;
-    const XT *x = static_cast<const XT *>(a.X) + row * a.ldx;
-    const YT *r = static_cast<const YT *>(a.R) + row * a.ldr;
-    XT *sp = static_cast<XT *>(a.S) + row * a.lds;
-    YT *y = static_cast<YT *>(a.Y) + row * a.ldy;
-    // the row's sum as stored; from the first pass on it may have replaced X or R
-    auto value = [&](int64_t i, bool first, float (&s)[8]) __attribute__((always_inline)) {
-        if (RES && a.S && !first) {
-            load_n(sp + i, a.D - i, s);
-            return;
+    for (int64_t row = blockIdx.x; row < a.T; row += gridDim.x) {
+        const XT *x = static_cast<const XT *>(a.X) + row * a.ldx;
+        const YT *r = static_cast<const YT *>(a.R) + row * a.ldr;
+        XT *sp = static_cast<XT *>(a.S) + row * a.lds;
+        YT *y = static_cast<YT *>(a.Y) + row * a.ldy;
+        // the row's sum as stored; from the first pass on it may have replaced X or R
+        auto value = [&](int64_t i, bool first, float (&s)[8]) __attribute__((always_inline)) {
+            if (RES && a.S && !first) {
+                load_n(sp + i, a.D - i, s);
+                return;
+            }
+            load_n(x + i, a.D - i, s);
+            if constexpr (RES) {
+                float u[8];
+                load_n(r + i, a.D - i, u);
+#pragma unroll
+                for (int e = 0; e < 8; ++e) s[e] = (float)(XT)(s[e] + u[e]);
+            }
+        };
+        float s[8], sum = 0.f, sq = 0.f;
+        for (int64_t i = threadIdx.x * 8; i < a.D; i += NT * 8) {
+            value(i, true, s);
+            if (RES && a.S) store_n(sp + i, a.D - i, s);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) sum += s[e];
         }
-        load_n(x + i, a.D - i, s);
-        if constexpr (RES) {
-            float u[8];
-            load_n(r + i, a.D - i, u);
+        const float mean = row_sum<NT>(sum, slots[0]) / a.width;
+        for (int64_t i = threadIdx.x * 8; i < a.D; i += NT * 8) {
+            value(i, false, s);
 #pragma unroll
-            for (int e = 0; e < 8; ++e) s[e] = (float)(XT)(s[e] + u[e]);
+            for (int e = 0; e < 8; ++e)
+                if (i + e < a.D) sq += (s[e] - mean) * (s[e] - mean);
         }
-    };
-    float s[8], sum = 0.f, sq = 0.f;
-    for (int64_t i = threadIdx.x * 8; i < a.D; i += NT * 8) {
-        value(i, true, s);
-        if (RES && a.S) store_n(sp + i, a.D - i, s);
-#pragma unroll
-        for (int e = 0; e < 8; ++e) sum += s[e];
-    }
-    const float mean = row_sum<NT>(sum, slots[0]) / a.width;
-    for (int64_t i = threadIdx.x * 8; i < a.D; i += NT * 8) {
-        value(i, false, s);
-#pragma unroll
-        for (int e = 0; e < 8; ++e)
-            if (i + e < a.D) sq += (s[e] - mean) * (s[e] - mean);
-    }
-    const float rstd = 1.0f / sqrtf(row_sum<NT>(sq, slots[1]) / a.width + a.eps);
-    if (threadIdx.x == 0) {
-        if (a.mean) a.mean[row] = mean;
-        if (a.rstd) a.rstd[row] = rstd;
-    }
-    for (int64_t i = threadIdx.x * 8; i < a.D; i += NT * 8) {
-        float g[8], b[8];
-        value(i, false, s);
-#pragma unroll
-        for (int e = 0; e < 8; ++e) s[e] = (s[e] - mean) * rstd;
-        if (a.gamma) {
-            load_n(a.gamma, a.p_dtype, i, a.D - i, g);
-#pragma unroll
-            for (int e = 0; e < 8; ++e) s[e] *= g[e];
+        const float rstd = 1.0f / sqrtf(row_sum<NT>(sq, slots[1]) / a.width + a.eps);
+        if (threadIdx.x == 0) {
+            if (a.mean) a.mean[row] = mean;
+            if (a.rstd) a.rstd[row] = rstd;
         }
-        if (a.beta) {
-            load_n(a.beta, a.p_dtype, i, a.D - i, b);
+        for (int64_t i = threadIdx.x * 8; i < a.D; i += NT * 8) {
+            float g[8], b[8];
+            value(i, false, s);
 #pragma unroll
-            for (int e = 0; e < 8; ++e) s[e] += b[e];
+            for (int e = 0; e < 8; ++e) s[e] = (s[e] - mean) * rstd;
+            if (a.gamma) {
+                load_n(a.gamma, a.p_dtype, i, a.D - i, g);
+#pragma unroll
+                for (int e = 0; e < 8; ++e) s[e] *= g[e];
+            }
+            if (a.beta) {
+                load_n(a.beta, a.p_dtype, i, a.D - i, b);
+#pragma unroll
+                for (int e = 0; e < 8; ++e) s[e] += b[e];
+            }
+            store_n(y + i, a.D - i, s);
         }
-        store_n(y + i, a.D - i, s);
     }
 }
 
+__device__ __forceinline__ void pin(float (&v)[8]) {
+    asm volatile(""
+                 : "+v"(v[0]), "+v"(v[1]), "+v"(v[2]), "+v"(v[3]), "+v"(v[4]), "+v"(v[5]), "+v"(v[6]), "+v"(v[7]));
+}
+
 // A workgroup takes rows blockIdx.x, + gridDim.x, ... (kRows of them at a time)
-// and holds its sums of dY h and dY in registers over all of them.
-template <typename XT, typename YT, int NT, int V>
+// and holds its sums of dY h and dY in registers over all of them, and gamma in
+// LDS.  Between the two uses of a row it is held as it was read.
+template <typename XT, typename YT, int NT, int V, int FULL>
 __global__ __launch_bounds__(kBlock<NT>) void norm_bwd_kernel(NormArgs a) {
-    __shared__ float slots[2][2][NT <= 64 ? 1 : NT / 64];
-    __shared__ float fold[NT < 256 ? 256 * 8 : 1];
-    const int t = threadIdx.x % NT, sub = threadIdx.x / NT;
+    __shared__ float slots[2][NT <= 64 ? 1 : NT / 64];
+    extern __shared__ __attribute__((aligned(16))) float gam[];  // gamma, D elements
+    // registers of a thread's vectors: where dS too would not fit beside the
+    // sums, S and dY (256 with 512 threads), it is read after the row's sums
+    constexpr bool LATE = V * 2 * (8 + 2 * sizeof(XT) + sizeof(YT)) > 224;
+    const int sub = kRows<NT> == 1 ? 0 : threadIdx.x / NT;
+    const Share<NT, FULL> my{kRows<NT> == 1 ? (int)threadIdx.x : (int)threadIdx.x % NT, (int)a.D};
+    for (int i = threadIdx.x * 8; i < a.D; i += kBlock<NT> * 8) {
+        float g[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) g[e] = 1.f;
+        if (a.gamma) load8(a.gamma, a.p_dtype, min(i, (int)a.D - 8), g);
+        store8(gam + min(i, (int)a.D - 8), g);
+    }
+    __syncthreads();
     float ag[V][8], ab[V][8];
 #pragma unroll
     for (int c = 0; c < V; ++c)
 #pragma unroll
         for (int e = 0; e < 8; ++e) ag[c][e] = ab[c][e] = 0.f;
-    int par = 0;  // the sums of two rows in a row use different slots
-    for (int64_t first = (int64_t)blockIdx.x * kRows<NT>; first < a.T; first += (int64_t)gridDim.x * kRows<NT>, par ^= 1) {
-        const int64_t row = first + sub;
-        const int64_t D = row < a.T ? a.D : 0;
+    for (int64_t first = (int64_t)blockIdx.x * kRows<NT>; first < a.T; first += (int64_t)gridDim.x * kRows<NT>) {
+        const bool live = first + sub < a.T;
+        const int64_t row = live ? first + sub : a.T - 1;
         const XT *x = static_cast<const XT *>(a.S) + row * a.lds;
         const YT *dy = static_cast<const YT *>(a.Y) + row * a.ldy;
         const XT *ds = static_cast<const XT *>(a.dS) + row * a.ldr;
         XT *dx = static_cast<XT *>(a.dX) + row * a.ldx;
-        float h[V][8], d[V][8];
+        Raw8<XT> xr[V], ur[V];
+        Raw8<YT> dr[V];
 #pragma unroll
         for (int c = 0; c < V; ++c) {
-            const int64_t i = (int64_t)(t + c * NT) * 8;
-            load_n(x + i, D - i, h[c]);
-            load_n(dy + i, D - i, d[c]);
+            xr[c].load(x + my.at(c));
+            dr[c].load(dy + my.at(c));
         }
-        const float mean = row < a.T ? a.mean[row] : 0.f, rstd = row < a.T ? a.rstd[row] : 0.f;
+        const float mean = a.mean[row], rstd = a.rstd[row];
+        if (!LATE && a.dS) {  // on its way during the sums
+#pragma unroll
+            for (int c = 0; c < V; ++c) ur[c].load(ds + my.at(c));
+        }
         float sg = 0.f, sgh = 0.f;
 #pragma unroll
         for (int c = 0; c < V; ++c) {
-            const int64_t i = (int64_t)(t + c * NT) * 8;
             float g[8];
-            if (a.gamma) load_n(a.gamma, a.p_dtype, i, D - i, g);
+            load8(gam + my.at(c), g);
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
-                // past the row's end dY reads zero, and so do the sums
-                h[c][e] = (h[c][e] - mean) * rstd;
-                ag[c][e] += d[c][e] * h[c][e];
-                ab[c][e] += d[c][e];
-                if (a.gamma) d[c][e] *= g[e];
-                sg += d[c][e];
-                sgh += d[c][e] * h[c][e];
+                const float h = (xr[c][e] - mean) * rstd, d = kRows<NT> == 1 || live ? dr[c][e] : 0.f, w = d * g[e];
+                ag[c][e] += d * h;
+                ab[c][e] += d;
+                sg += my.own(c, e) ? w : 0.f;
+                sgh += my.own(c, e) ? w * h : 0.f;
             }
+            // all of this vector's sums are formed here: left to itself, the
+            // compiler puts some off past the row's sums and keeps what they
+            // need in registers (in scratch, for long rows)
+            pin(ag[c]);
+            pin(ab[c]);
+            asm volatile("" : "+v"(sg), "+v"(sgh));
+            xr[c].forget();
+            dr[c].forget();
         }
-        const float mg = row_sum<NT>(sg, slots[par][0]) / a.width;
-        const float mgh = row_sum<NT>(sgh, slots[par][1]) / a.width;
+        const float mg = row_sum<NT>(sg, slots[0]) / a.width;
+        const float mgh = row_sum<NT>(sgh, slots[1]) / a.width;
+        // dX may be dS, and vectors overlap at the row's end: all of dS has
+        // been read before anything is written
+        if (a.dS) {
+            if constexpr (LATE) {
+#pragma unroll
+                for (int c = 0; c < V; ++c) ur[c].load(ds + my.at(c));
+            }
+#pragma unroll
+            for (int c = 0; c < V; ++c) ur[c].forget();
+            if constexpr (LATE) __syncthreads();
+        }
 #pragma unroll
         for (int c = 0; c < V; ++c) {
-            const int64_t i = (int64_t)(t + c * NT) * 8;
-            float o[8];
+            float o[8], g[8];
+            load8(gam + my.at(c), g);
 #pragma unroll
-            for (int e = 0; e < 8; ++e) o[e] = (d[c][e] - mg - h[c][e] * mgh) * rstd;
-            if (a.dS) {
-                float u[8];
-                load_n(ds + i, D - i, u);
-#pragma unroll
-                for (int e = 0; e < 8; ++e) o[e] += u[e];
+            for (int e = 0; e < 8; ++e) {
+                const float h = (xr[c][e] - mean) * rstd;
+                o[e] = (dr[c][e] * g[e] - mg - h * mgh) * rstd;
+                if (a.dS) o[e] += ur[c][e];
             }
-            store_n(dx + i, D - i, o);
+            if (live) store8(dx + my.at(c), o);
         }
     }
     if (!a.part) return;
@@ -263,11 +313,11 @@ __global__ __launch_bounds__(kBlock<NT>) void norm_bwd_kernel(NormArgs a) {
     if constexpr (NT >= 256) {
 #pragma unroll
         for (int c = 0; c < V; ++c) {
-            const int64_t i = (int64_t)(t + c * NT) * 8;
-            store_n(pg + i, a.D - i, ag[c]);
-            store_n(pb + i, a.D - i, ab[c]);
+            store8(pg + my.at(c), ag[c]);
+            store8(pb + my.at(c), ab[c]);
         }
     } else {  // the workgroup's rows are summed here, in order
+        __shared__ float fold[256 * 8];
 #pragma unroll
         for (int c = 0; c < V; ++c)
 #pragma unroll
@@ -279,8 +329,8 @@ __global__ __launch_bounds__(kBlock<NT>) void norm_bwd_kernel(NormArgs a) {
                 for (int j = threadIdx.x; j < NT * 8; j += 256) {
                     float s = 0.f;
                     for (int k = 0; k < kRows<NT>; ++k) s += fold[k * NT * 8 + j];
-                    const int64_t i = (int64_t)c * NT * 8 + j;
-                    if (i < a.D) (w ? pb : pg)[i] = s;
+                    const int i = Share<NT, FULL>{j >> 3, (int)a.D}.at(c) + (j & 7);
+                    (w ? pb : pg)[i] = s;
                 }
             }
     }
@@ -291,44 +341,45 @@ template <typename XT, typename YT>
 __global__ __launch_bounds__(1024) void norm_bwd_long_kernel(NormArgs a) {
     constexpr int NT = 1024;
     __shared__ float slots[2][NT / 64];
-    const int64_t row = blockIdx.x;
-    const XT *x = static_cast<const XT *>(a.S) + row * a.lds;
-    const YT *dy = static_cast<const YT *>(a.Y) + row * a.ldy;
-    const XT *ds = static_cast<const XT *>(a.dS) + row * a.ldr;
-    XT *dx = static_cast<XT *>(a.dX) + row * a.ldx;
-    const float mean = a.mean[row], rstd = a.rstd[row];
-    auto value = [&](int64_t i, float (&h)[8], float (&d)[8]) __attribute__((always_inline)) {
-        float g[8];
-        load_n(x + i, a.D - i, h);
-        load_n(dy + i, a.D - i, d);
-        if (a.gamma) load_n(a.gamma, a.p_dtype, i, a.D - i, g);
+    for (int64_t row = blockIdx.x; row < a.T; row += gridDim.x) {
+        const XT *x = static_cast<const XT *>(a.S) + row * a.lds;
+        const YT *dy = static_cast<const YT *>(a.Y) + row * a.ldy;
+        const XT *ds = static_cast<const XT *>(a.dS) + row * a.ldr;
+        XT *dx = static_cast<XT *>(a.dX) + row * a.ldx;
+        const float mean = a.mean[row], rstd = a.rstd[row];
+        auto value = [&](int64_t i, float (&h)[8], float (&d)[8]) __attribute__((always_inline)) {
+            float g[8];
+            load_n(x + i, a.D - i, h);
+            load_n(dy + i, a.D - i, d);
+            if (a.gamma) load_n(a.gamma, a.p_dtype, i, a.D - i, g);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-            h[e] = (h[e] - mean) * rstd;
-            if (a.gamma) d[e] *= g[e];
-        }
-    };
-    float h[8], d[8], sg = 0.f, sgh = 0.f;
-    for (int64_t i = threadIdx.x * 8; i < a.D; i += NT * 8) {
-        value(i, h, d);
+            for (int e = 0; e < 8; ++e) {
+                h[e] = (h[e] - mean) * rstd;
+                if (a.gamma) d[e] *= g[e];
+            }
+        };
+        float h[8], d[8], sg = 0.f, sgh = 0.f;
+        for (int64_t i = threadIdx.x * 8; i < a.D; i += NT * 8) {
+            value(i, h, d);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-            sg += d[e];
-            sgh += d[e] * h[e];
+            for (int e = 0; e < 8; ++e) {
+                sg += d[e];
+                sgh += d[e] * h[e];
+            }
         }
-    }
-    const float mg = row_sum<NT>(sg, slots[0]) / a.width;
-    const float mgh = row_sum<NT>(sgh, slots[1]) / a.width;
-    for (int64_t i = threadIdx.x * 8; i < a.D; i += NT * 8) {
-        float u[8];
-        value(i, h, d);
-        if (a.dS) load_n(ds + i, a.D - i, u);
+        const float mg = row_sum<NT>(sg, slots[0]) / a.width;
+        const float mgh = row_sum<NT>(sgh, slots[1]) / a.width;
+        for (int64_t i = threadIdx.x * 8; i < a.D; i += NT * 8) {
+            float u[8];
+            value(i, h, d);
+            if (a.dS) load_n(ds + i, a.D - i, u);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-            d[e] = (d[e] - mg - h[e] * mgh) * rstd;
-            if (a.dS) d[e] += u[e];
+            for (int e = 0; e < 8; ++e) {
+                d[e] = (d[e] - mg - h[e] * mgh) * rstd;
+                if (a.dS) d[e] += u[e];
+            }
+            store_n(dx + i, a.D - i, d);
         }
-        store_n(dx + i, a.D - i, d);
     }
 }
 
@@ -381,38 +432,43 @@ __global__ __launch_bounds__(1024) void norm_fold_kernel(const float *part, int6
 
 int64_t min64(int64_t x, int64_t y) { return x < y ? x : y; }
 
-constexpr int64_t kMostGroups = 1 << 20;  // workgroups of a forward (a grid ends below 2^32 threads)
-constexpr int64_t kMostHeld = 32768;  // longest row that is held in registers
-constexpr int kParts = 512;           // most workgroups that hold partial sums
+constexpr int64_t kMostGroups = 1 << 20;  // workgroups of a launch (a grid ends below 2^32 threads)
+constexpr int64_t kLeastHeld = 8, kMostHeld = 32768;  // rows that are held in registers
 
-// f(NT, V) for the threads and vectors that hold a row of D elements.
+// Workgroups of the backward, each with its own partial sums: as many as run at
+// once where the sums take most of a compute unit's registers, and up to four
+// times as many for shorter rows.
+int64_t parts_of(int64_t D) { return D > 8192 ? 256 : D > 4096 ? 512 : 1024; }
+
+// f(NT, V, FULL) for the threads and vectors that hold a row of D elements.
 template <typename F>
 hipError_t with_shape(int64_t D, F &&f) {
-#define ZI_SHAPE(NT, V) \
-    if (D <= (int64_t)NT * V * 8) return f(std::integral_constant<int, NT>{}, std::integral_constant<int, V>{})
-    ZI_SHAPE(16, 1);
-    ZI_SHAPE(64, 1);
-    ZI_SHAPE(64, 2);
-    ZI_SHAPE(256, 1);
-    ZI_SHAPE(256, 2);
-    ZI_SHAPE(1024, 1);
-    ZI_SHAPE(1024, 2);
-    ZI_SHAPE(1024, 3);
-    ZI_SHAPE(1024, 4);
+#define ZI_SHAPE(NT, V, FULL)     \
+    if (D <= (int64_t)NT * V * 8) \
+    return f(std::integral_constant<int, NT>{}, std::integral_constant<int, V>{}, std::integral_constant<int, FULL>{})
+    ZI_SHAPE(16, 1, 0);
+    ZI_SHAPE(64, 1, 0);
+    ZI_SHAPE(64, 2, 1);
+    ZI_SHAPE(256, 1, 0);
+    ZI_SHAPE(256, 2, 1);
+    ZI_SHAPE(512, 2, 1);
+    ZI_SHAPE(512, 4, 2);
+    ZI_SHAPE(512, 7, 4);
+    ZI_SHAPE(512, 8, 7);
 #undef ZI_SHAPE
     return hipErrorInvalidValue;
 }
 
 template <typename XT, typename YT, bool RES>
 hipError_t run_fwd(const NormArgs &a, hipStream_t s) {
-    if (a.D > kMostHeld) {
-        hipLaunchKernelGGL((norm_fwd_long_kernel<XT, YT, RES>), dim3((unsigned)a.T), dim3(1024), 0, s, a);
+    if (a.D < kLeastHeld || a.D > kMostHeld) {
+        hipLaunchKernelGGL((norm_fwd_long_kernel<XT, YT, RES>), dim3((unsigned)min64(a.T, kMostGroups)), dim3(1024), 0, s, a);
         return hipGetLastError();
     }
-    return with_shape(a.D, [&](auto nt, auto v) {
-        constexpr int NT = decltype(nt)::value, V = decltype(v)::value;
+    return with_shape(a.D, [&](auto nt, auto v, auto full) {
+        constexpr int NT = decltype(nt)::value, V = decltype(v)::value, FULL = decltype(full)::value;
         const unsigned grid = (unsigned)min64((a.T + kRows<NT> - 1) / kRows<NT>, kMostGroups);
-        hipLaunchKernelGGL((norm_fwd_kernel<XT, YT, RES, NT, V>), dim3(grid), dim3(kBlock<NT>), 0, s, a);
+        hipLaunchKernelGGL((norm_fwd_kernel<XT, YT, RES, NT, V, FULL>), dim3(grid), dim3(kBlock<NT>), 0, s, a);
         return hipGetLastError();
     });
 }
@@ -421,20 +477,21 @@ template <typename XT, typename YT>
 hipError_t run_bwd(const NormArgs &a, float *dgamma, float *dbeta, hipStream_t s) {
     int parts = 0;
     hipError_t e = hipSuccess;
-    if (a.T > 0 && a.D > kMostHeld) {
+    if (a.T > 0 && (a.D < kLeastHeld || a.D > kMostHeld)) {
         if (a.part) {
-            parts = (int)min64(a.T, 64);
+            parts = (int)min64(a.T, 64);  // (at most parts_of)
             const dim3 grid((unsigned)((a.D + 2047) / 2048), (unsigned)parts);
             hipLaunchKernelGGL((norm_cols_kernel<XT, YT>), grid, dim3(256), 0, s, a);
             if ((e = hipGetLastError()) != hipSuccess) return e;
         }
-        hipLaunchKernelGGL((norm_bwd_long_kernel<XT, YT>), dim3((unsigned)a.T), dim3(1024), 0, s, a);
+        hipLaunchKernelGGL((norm_bwd_long_kernel<XT, YT>), dim3((unsigned)min64(a.T, kMostGroups)), dim3(1024), 0, s, a);
         if ((e = hipGetLastError()) != hipSuccess) return e;
     } else if (a.T > 0) {
-        e = with_shape(a.D, [&](auto nt, auto v) {
-            constexpr int NT = decltype(nt)::value, V = decltype(v)::value;
-            parts = (int)min64((a.T + kRows<NT> - 1) / kRows<NT>, kParts);
-            hipLaunchKernelGGL((norm_bwd_kernel<XT, YT, NT, V>), dim3((unsigned)parts), dim3(kBlock<NT>), 0, s, a);
+        e = with_shape(a.D, [&](auto nt, auto v, auto full) {
+            constexpr int NT = decltype(nt)::value, V = decltype(v)::value, FULL = decltype(full)::value;
+            parts = (int)min64((a.T + kRows<NT> - 1) / kRows<NT>, parts_of(a.D));
+            hipLaunchKernelGGL((norm_bwd_kernel<XT, YT, NT, V, FULL>), dim3((unsigned)parts), dim3(kBlock<NT>),
+                               (unsigned)a.D * 4, s, a);
             return hipGetLastError();
         });
         if (e != hipSuccess) return e;
@@ -522,7 +579,7 @@ extern "C" zi_status zi_layer_norm_fwd(const zi_norm *n, const void *X, const vo
 
 extern "C" uint64_t zi_layer_norm_bwd_bytes(int64_t T, int64_t D) {
     if (T < 0 || D < 1) return 0;
-    return (uint64_t)min64(T, kParts) * 2 * (uint64_t)D * 4;
+    return (uint64_t)min64(T, parts_of(D)) * 2 * (uint64_t)D * 4;
 }
 
 extern "C" zi_status zi_layer_norm_bwd(const zi_norm *n, const void *dY, const void *S, const void *gamma,

@@ -15,6 +15,7 @@ typedef __bf16 bf16_t;
 // Rows start wherever their stride puts them, so vectors are only as aligned
 // as their elements; the hardware's global loads and stores take any address.
 typedef uint16_t u16x8_u __attribute__((ext_vector_type(8), aligned(2)));
+typedef uint32_t u32x4_u __attribute__((ext_vector_type(4), aligned(2)));
 typedef float f32x4_u __attribute__((ext_vector_type(4), aligned(4)));
 
 template <typename T>
@@ -70,6 +71,45 @@ __device__ __forceinline__ void store_n(T *p, int64_t n, const float (&v)[8]) {
 #pragma unroll
         for (int e = 0; e < 8; ++e)
             if (e < n) p[e] = (T)v[e];
+    }
+}
+
+// Eight elements as they lie in memory: half the registers of their fp32
+// values where the type is 16 bits wide.
+template <typename T>
+struct Raw8 {
+    u32x4_u v;
+    __device__ __forceinline__ void load(const T *p) { v = *reinterpret_cast<const u32x4_u *>(p); }
+    __device__ __forceinline__ float operator[](int e) const { return to_f32<T>((uint16_t)(v[e >> 1] >> (16 * (e & 1)))); }
+    // Hides where the value comes from, so that what was computed from it
+    // before is computed again rather than kept in registers.
+    __device__ __forceinline__ void forget() { asm volatile("" : "+v"(v)); }
+};
+template <>
+struct Raw8<float> {
+    f32x4_u v[2];
+    __device__ __forceinline__ void load(const float *p) {
+        v[0] = *reinterpret_cast<const f32x4_u *>(p);
+        v[1] = *reinterpret_cast<const f32x4_u *>(p + 4);
+    }
+    __device__ __forceinline__ float operator[](int e) const { return v[e >> 2][e & 3]; }
+    __device__ __forceinline__ void forget() { asm volatile("" : "+v"(v[0]), "+v"(v[1])); }
+};
+
+// Eight elements of an array whose type is known at run time only (the same
+// for every lane).
+__device__ __forceinline__ void load8(const void *p, int dtype, int at, float (&v)[8]) {
+    if (dtype == ZI_F32) {
+        load8(static_cast<const float *>(p) + at, v);
+        return;
+    }
+    const u32x4_u a = *reinterpret_cast<const u32x4_u *>(static_cast<const uint16_t *>(p) + at);
+    if (dtype == ZI_F16) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) v[e] = to_f32<f16_t>((uint16_t)(a[e >> 1] >> (16 * (e & 1))));
+    } else {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) v[e] = to_f32<bf16_t>((uint16_t)(a[e >> 1] >> (16 * (e & 1))));
     }
 }
 
