@@ -66,7 +66,8 @@ __global__ __launch_bounds__(256) void embed_fwd_kernel(const void *ids, int32_t
             const int64_t i = base + c * L * 8;
 #pragma unroll
             for (int e = 0; e < 8; ++e) r[c][e] *= scale;
-            store_n(x + i, D - i, r[c]);
+            if (D - i >= 8) stream8(x + i, r[c]);
+            else store_n(x + i, D - i, r[c]);
         }
     }
 }

@@ -74,12 +74,25 @@ __device__ __forceinline__ void store_n(T *p, int64_t n, const float (&v)[8]) {
     }
 }
 
+// The same store past the caches (nontemporal), for outputs that are written
+// once.  Of fp32 values each of the two stores fills half of every line that
+// the wave touches, and the caches are left to join them.
+__device__ __forceinline__ void stream8(float *p, const float (&v)[8]) { store8(p, v); }
+template <typename T>
+__device__ __forceinline__ void stream8(T *p, const float (&v)[8]) {
+    u16x8_u a;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) a[e] = __builtin_bit_cast(uint16_t, (T)v[e]);
+    __builtin_nontemporal_store(a, reinterpret_cast<u16x8_u *>(p));
+}
+
 // Eight elements as they lie in memory: half the registers of their fp32
-// values where the type is 16 bits wide.
+// values where the type is 16 bits wide.  16-bit elements are read past the
+// caches, as they are written (stream8).
 template <typename T>
 struct Raw8 {
     u32x4_u v;
-    __device__ __forceinline__ void load(const T *p) { v = *reinterpret_cast<const u32x4_u *>(p); }
+    __device__ __forceinline__ void load(const T *p) { v = __builtin_nontemporal_load(reinterpret_cast<const u32x4_u *>(p)); }
     __device__ __forceinline__ float operator[](int e) const { return to_f32<T>((uint16_t)(v[e >> 1] >> (16 * (e & 1)))); }
     // Hides where the value comes from, so that what was computed from it
     // before is computed again rather than kept in registers.
