@@ -11,12 +11,13 @@
 // summed straight into its row of dW.  A run that crosses a chunk's border, such
 // as a frequent token's, is summed piece by piece, one piece a chunk, into the
 // workspace, and its pieces are then added in order.  Rows without a token are
-// written as zero by the same launch.  Sums are held in fp32 and rounded once.
+// written as zero.  Sums are held in fp32 and rounded once.
 //
-// The sort: a workgroup ranks 256 keys of a tile of kTile by counting the
-// tile's smaller ones; kFan sorted lists at a time are then merged, the place
-// of a key being its place in its own list plus the number of keys before it in
-// every other one (binary searches).  32768 tokens take one merge.
+// The sort: a workgroup ranks 64 keys of a tile by counting the tile's smaller
+// ones; up to 4096 tokens are one tile.  Of more, kFan sorted lists at a time
+// are then merged, the place of a key being its place in its own list plus the
+// number of keys before it in every other one (binary searches).  32768 tokens
+// take one merge.
 #include <hip/hip_runtime.h>
 #include <math.h>
 #include <stdint.h>
@@ -29,30 +30,31 @@ namespace {
 
 using namespace zi;
 
-constexpr int kChunk = 64;   // sorted tokens of a chunk
-constexpr int kTile = 1024;  // tokens that the first step sorts together
-constexpr int kFan = 32;     // lists that one merge joins
+constexpr int kChunk = 64;      // sorted tokens of a chunk, at most
+constexpr int kTile = 1024;     // tokens that the first step sorts together,
+constexpr int kOneTile = 4096;  // or all of them, if they are no more than this
+constexpr int kFan = 32;        // lists that one merge joins
 
 constexpr int64_t kMostGroups = 1 << 20;  // workgroups along one side of a grid (a side ends below 2^32 threads)
 
 int64_t min64(int64_t x, int64_t y) { return x < y ? x : y; }
+int64_t max64(int64_t x, int64_t y) { return x > y ? x : y; }
 int64_t ceil_div(int64_t x, int64_t y) { return (x + y - 1) / y; }
 uint64_t up256(uint64_t x) { return (x + 255) / 256 * 256; }
 
-// The id at position t, or V (past every row) for padding.
-__device__ __forceinline__ uint32_t key_at(const void *ids, bool wide, int64_t t, int64_t V) {
-    const int64_t id = wide ? static_cast<const int64_t *>(ids)[t] : (int64_t) static_cast<const int32_t *>(ids)[t];
-    return (uint32_t)(id < 0 || id >= V ? V : id);
-}
+// The id, or V (past every row) for padding.
+__device__ __forceinline__ uint32_t key_of(int64_t id, int64_t V) { return (uint32_t)(id < 0 || id >= V ? V : id); }
 
 // L lanes a token, 256 / L tokens a workgroup; blockIdx.y: a span of columns.
-constexpr int kSpan = 8;  // vectors a lane takes of one token
+// All of a lane's loads are in flight before its first store; X passes the
+// caches, W, whose rows come again, does not.
+constexpr int kSpan = 2;  // vectors a lane takes of one token (4: 5 % slower for long rows, 1: 15 %)
 template <typename WT, typename XT, int L>
 __global__ __launch_bounds__(256) void embed_fwd_kernel(const void *ids, int32_t wide, int64_t T, int64_t V, int64_t D,
                                                         const WT *W, int64_t ldw, float scale, XT *X, int64_t ldx) {
     const int64_t base = ((int64_t)blockIdx.y * kSpan * L + threadIdx.x % L) * 8;
     for (int64_t t = (int64_t)blockIdx.x * (256 / L) + threadIdx.x / L; t < T; t += (int64_t)gridDim.x * (256 / L)) {
-        const uint32_t v = key_at(ids, wide, t, V);
+        const uint32_t v = key_of(wide ? static_cast<const int64_t *>(ids)[t] : static_cast<const int32_t *>(ids)[t], V);
         const WT *w = W + (int64_t)v * ldw;
         XT *x = X + t * ldx;
         float r[kSpan][8];
@@ -74,24 +76,137 @@ __global__ __launch_bounds__(256) void embed_fwd_kernel(const void *ids, int32_t
 
 // ---- the sort -----------------------------------------------------------------------
 
-// The rank of 256 keys (blockIdx.y) of tile blockIdx.x among the tile's.
-__global__ __launch_bounds__(256) void sort_tile_kernel(const void *ids, int32_t wide, int64_t T, int64_t V,
-                                                        uint32_t *keys, int32_t *order) {
-    __shared__ uint32_t k[kTile];
-    const int64_t base = (int64_t)blockIdx.x * kTile;
-    const int n = (int)min((int64_t)kTile, T - base);
-    for (int j = threadIdx.x; j < kTile; j += 256) k[j] = j < n ? key_at(ids, wide, base + j, V) : 0xffffffffu;
+typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+constexpr uint32_t kNoKey = 0xffffffffu;  // past every key
+
+// Rows of dW that are written as zero, whatever their type.
+struct Fill {
+    char *base;
+    int64_t V, stride, bytes;  // rows; from one to the next, and of one, in bytes (even)
+    int32_t rows;              // that a workgroup takes at a time
+};
+constexpr int kMostRows = 64;
+
+__device__ __forceinline__ void fill_row(const Fill &f, int64_t v) {
+    char *w = f.base + v * f.stride;
+    for (int64_t i = threadIdx.x * 16; i + 16 <= f.bytes; i += blockDim.x * 16)
+        __builtin_nontemporal_store(u32x4_u{}, reinterpret_cast<u32x4_u *>(w + i));
+    const int64_t i = f.bytes / 16 * 16 + threadIdx.x * 2;
+    if (i < f.bytes) *reinterpret_cast<uint16_t *>(w + i) = 0;
+}
+
+// The place of 64 keys of a tile blockIdx.x in the sorted tile: the
+// number of keys that are smaller, or equal and before.  Each of 16 waves
+// counts over its share of the tile, four keys a read.  Workgroups from
+// `sorts` on fill all of dW, if it is filled here.
+template <int TILE, typename ID>
+__global__ __launch_bounds__(1024) void sort_tile_kernel(const ID *__restrict__ ids, int64_t T, int64_t V,
+                                                         uint32_t *__restrict__ keys, int32_t *__restrict__ order,
+                                                         int32_t sorts, int32_t per_tile, Fill fill) {
+    if ((int)blockIdx.x >= sorts) {
+        const int64_t first = (int64_t)(blockIdx.x - sorts) * fill.rows, step = (int64_t)(gridDim.x - sorts) * fill.rows;
+        for (int64_t v0 = first; v0 < fill.V; v0 += step)
+            for (int64_t v = v0; v < min(v0 + fill.rows, fill.V); ++v) fill_row(fill, v);
+        return;
+    }
+    constexpr int SHARE = TILE / 16;
+    static_assert(SHARE % 64 == 0, "the 64 keys lie in one wave's share");
+    __shared__ __attribute__((aligned(16))) uint32_t k[TILE];
+    __shared__ int count[16][64];
+    const int64_t base = (int64_t)(blockIdx.x / per_tile) * TILE;
+    const int n = (int)min((int64_t)TILE, T - base);
+#pragma unroll
+    for (int c = 0; c < TILE / 1024; ++c) {  // every load in flight at once
+        const int j = c * 1024 + threadIdx.x;
+        const uint32_t key = key_of(ids[base + min(j, n - 1)], V);
+        k[j] = j < n ? key : kNoKey;
+    }
     __syncthreads();
-    const int i = blockIdx.y * 256 + threadIdx.x;
-    const int w0 = __builtin_amdgcn_readfirstlane(i & ~63);  // the wave's own 64 positions
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int i0 = (int)(blockIdx.x % per_tile) * 64, i = i0 + lane;
     const uint32_t mine = k[i];
+    const int from = wave * SHARE;
     int rank = 0;
-    for (int j = 0; j < w0; ++j) rank += k[j] <= mine;  // equal keys before come first
-    for (int j = w0; j < w0 + 64; ++j) rank += k[j] < mine || (k[j] == mine && j < i);
-    for (int j = w0 + 64; j < kTile; ++j) rank += k[j] < mine;
-    if (i < n) {
+    auto four = [&](int j) __attribute__((always_inline)) { return *reinterpret_cast<const u32x4 *>(k + j); };
+    if (from < n) {
+#pragma unroll 16
+        for (int j = from; j < from + SHARE; j += 4) {
+            const u32x4 q = four(j);
+            if (j < i0) {  // equal keys before the 64 come first
+                rank += (q[0] <= mine) + (q[1] <= mine) + (q[2] <= mine) + (q[3] <= mine);
+            } else if (j >= i0 + 64) {
+                rank += (q[0] < mine) + (q[1] < mine) + (q[2] < mine) + (q[3] < mine);
+            } else {  // among the 64 themselves, by position
+#pragma unroll
+                for (int e = 0; e < 4; ++e) rank += q[e] < mine || (q[e] == mine && j - i0 + e < lane);
+            }
+        }
+    }
+    count[wave][lane] = rank;
+    __syncthreads();
+    if (wave == 0 && i < n) {
+        rank = 0;
+#pragma unroll
+        for (int w = 0; w < 16; ++w) rank += count[w][lane];
         keys[base + rank] = mine;
         order[base + rank] = (int32_t)(base + i);
+    }
+}
+
+// Joins up to kFan sorted lists of kTile keys: 256 keys a workgroup, which
+// holds the group's keys in LDS.  A key's place is its place in its own list
+// plus the keys before it in every other one (those equal to it too, in an
+// earlier list): a thread counts those of a quarter of the lists, by four
+// binary searches at a time.
+__global__ __launch_bounds__(1024) void merge_tiles_kernel(const uint32_t *__restrict__ keys,
+                                                           const int32_t *__restrict__ order,
+                                                           uint32_t *__restrict__ keys_out,
+                                                           int32_t *__restrict__ order_out, int64_t T) {
+    extern __shared__ __attribute__((aligned(16))) uint32_t held[];
+    __shared__ int count[4][256];
+    static_assert(kTile == 1024 && kFan % 16 == 0, "a load of the workgroup is one list");
+    const int64_t mine = blockIdx.x / (kTile / 256);             // the list of this workgroup's keys
+    const int64_t first = mine / kFan * kFan;                    // the group's first list
+    const int lists = (int)min((int64_t)kFan, (T - first * kTile + kTile - 1) / kTile);
+    const int own = (int)(mine - first);
+    for (int l = 0; l < lists; l += 4) {
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+            const int64_t j = first * kTile + (l + u) * kTile + threadIdx.x;
+            const uint32_t key = keys[min(j, T - 1)];
+            held[(l + u) * kTile + threadIdx.x] = j < T ? key : kNoKey;
+        }
+    }
+    const int slot = (int)(blockIdx.x % (kTile / 256)) * 256 + (threadIdx.x & 255);  // in its list
+    const int quarter = threadIdx.x >> 8;
+    const int64_t i = mine * kTile + slot;
+    const int32_t from = order[min(i, T - 1)];
+    __syncthreads();
+    const uint32_t key = held[own * kTile + slot];
+    int at = 0;
+    for (int l = quarter * 4; l < lists; l += 16) {
+        int pos[4] = {};
+#pragma unroll
+        for (int step = kTile / 2; step > 0; step >>= 1) {
+#pragma unroll
+            for (int u = 0; u < 4; ++u) {
+                const uint32_t q = held[(l + u) * kTile + pos[u] + step - 1];
+                pos[u] += (l + u < own ? q <= key : q < key) ? step : 0;
+            }
+        }
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {  // one key is left
+            const uint32_t q = held[(l + u) * kTile + pos[u]];
+            pos[u] += (l + u < own ? q <= key : q < key) ? 1 : 0;
+            at += l + u == own ? 0 : pos[u];
+        }
+    }
+    count[quarter][threadIdx.x & 255] = at;
+    __syncthreads();
+    if (quarter == 0 && i < T) {
+        at += slot + count[1][threadIdx.x] + count[2][threadIdx.x] + count[3][threadIdx.x];
+        keys_out[first * kTile + at] = key;
+        order_out[first * kTile + at] = from;
     }
 }
 
@@ -108,7 +223,7 @@ __device__ __forceinline__ int64_t before(const uint32_t *p, int64_t n, uint32_t
     return lo;
 }
 
-// Joins groups of kFan sorted lists of `len` keys each.
+// The same for longer lists, of `len` keys each, which stay in memory.
 __global__ __launch_bounds__(256) void merge_kernel(const uint32_t *keys, const int32_t *order, uint32_t *keys_out,
                                                     int32_t *order_out, int64_t T, int64_t len) {
     const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
@@ -131,109 +246,154 @@ __global__ __launch_bounds__(256) void merge_kernel(const uint32_t *keys, const 
 
 // ---- the sums -----------------------------------------------------------------------
 
-// Adds rows order[j] of dX, j in [from, to), columns [i, i + 8).
-template <typename DT>
-__device__ __forceinline__ void add_rows(const DT *dX, int64_t ldx, const int32_t *order, int64_t from, int64_t to,
-                                         int64_t i, int64_t n, float (&s)[8]) {
-    for (int64_t j = from; j < to; ++j) {
+// A row's sum, scaled and, with `accumulate`, added to what the row holds.
+template <typename WT>
+__device__ __forceinline__ void finish_row(WT *w, int64_t n, const float (&sum)[8], float scale, int32_t accumulate) {
+    float s[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) s[e] = sum[e] * scale;
+    if (accumulate) {
         float u[8];
-        load_n(dX + (int64_t)order[j] * ldx + i, n, u);
+        load_n(w, n, u);
 #pragma unroll
         for (int e = 0; e < 8; ++e) s[e] += u[e];
     }
+    if (n >= 8) stream8(w, s);
+    else store_n(w, n, s);
 }
 
-// Chunk blockIdx.x of the sorted tokens: notes where each run begins and ends
-// (first[v], last[v]), and sums the pieces of the runs that cross its borders:
-// of the one that comes in from the left into slot 0, of the one that goes on
-// to the right (if it begins here) into slot 1.
-template <typename DT>
-__global__ __launch_bounds__(256) void piece_kernel(const uint32_t *keys, const int32_t *order, int64_t T, int64_t V,
-                                                    const DT *dX, int64_t ldx, int64_t D, int32_t *first,
-                                                    int32_t *last, float *pieces) {
-    const int64_t a = (int64_t)blockIdx.x * kChunk, b = min(a + kChunk, T);
-    const uint32_t ka = keys[a], kb = keys[b - 1];
-    if (blockIdx.y == 0 && threadIdx.x < b - a) {
-        const int64_t j = a + threadIdx.x;
-        const uint32_t k = keys[j];
-        if (k < V) {
-            if (j == 0 || keys[j - 1] != k) first[k] = (int32_t)j;
-            if (j == T - 1 || keys[j + 1] != k) last[k] = (int32_t)j;
-        }
-    }
-    const bool in = a > 0 && keys[a - 1] == ka && ka < V;
-    const bool on = b < T && keys[b] == kb && kb < V;
-    const int64_t i = ((int64_t)blockIdx.y * 256 + threadIdx.x) * 8;
-    if (i >= D) return;
-    if (in || (on && ka == kb)) {
-        float s[8] = {};
-        int64_t to = a;
-        while (to < b && keys[to] == ka) ++to;
-        add_rows(dX, ldx, order, a, to, i, D - i, s);
-        store_n(pieces + (2 * (int64_t)blockIdx.x) * D + i, D - i, s);
-    }
-    if (on && ka != kb) {
-        float s[8] = {};
-        int64_t from = b;
-        while (keys[from - 1] == kb) --from;
-        add_rows(dX, ldx, order, from, b, i, D - i, s);
-        store_n(pieces + (2 * (int64_t)blockIdx.x + 1) * D + i, D - i, s);
-    }
-}
-
-// Row v of dW.  first[v] means something only where v has tokens; the entry of
-// any other row is whatever the workspace held, so it is checked against the
-// sorted keys, which are all written: v has tokens exactly if its entry is a
-// place in the list that holds v and is the first one to do so.
+// Chunk `c` of the sorted tokens, columns [i, i + 8) of a thread: a run of equal
+// ids that lies in the chunk is summed and written to its row of dW; one that
+// comes in from the chunk before is summed into slot 0 of the chunk's pieces;
+// one that begins here and goes on into slot 1.  The rows of eight tokens are
+// in flight at a time, whatever runs they belong to.
 template <typename DT, typename WT>
-__global__ __launch_bounds__(256) void row_kernel(const uint32_t *keys, const int32_t *order, int64_t T, int64_t V,
-                                                  const DT *dX, int64_t ldx, int64_t D, const int32_t *first,
-                                                  const int32_t *last, const float *pieces, float scale,
-                                                  int32_t accumulate, WT *dW, int64_t ldw) {
-    const int64_t i = ((int64_t)blockIdx.y * 256 + threadIdx.x) * 8;
-    if (i >= D) return;
-    for (int64_t v = blockIdx.x; v < V; v += gridDim.x) {
-        WT *w = dW + v * ldw + i;
-        const int64_t f = T > 0 ? first[v] : -1;
-        const bool has = f >= 0 && f < T && keys[f] == (uint32_t)v && (f == 0 || keys[f - 1] != (uint32_t)v);
-        float s[8] = {};
-        if (has) {
-            const int64_t l = last[v];
-            const int64_t ca = f / kChunk, cb = l / kChunk;
-            if (ca == cb) {
-                add_rows(dX, ldx, order, f, l + 1, i, D - i, s);
+__device__ __forceinline__ void sum_chunk(const uint32_t *k, int n, uint32_t V, const int32_t *__restrict__ order,
+                                          const DT *__restrict__ dX, int64_t ldx, int64_t D, int64_t i, float scale,
+                                          int32_t accumulate, WT *__restrict__ dW, int64_t ldw,
+                                          float *__restrict__ piece) {
+    constexpr int U = 8;
+    auto key = [&](int j) __attribute__((always_inline)) { return (uint32_t)__builtin_amdgcn_readfirstlane((int)k[j]); };
+    float s[8] = {};
+    bool in = key(0) == key(1);  // the run at hand came in from the left
+    for (int j0 = 0; j0 < n; j0 += U) {
+        if (key(j0 + 1) >= V) return;  // padding sorts last
+        float u[U][8];
+#pragma unroll
+        for (int q = 0; q < U; ++q) load_n(dX + (int64_t)order[min(j0 + q, n - 1)] * ldx + i, D - i, u[q]);
+#pragma unroll
+        for (int q = 0; q < U; ++q) {
+            const int j = j0 + q;
+            if (j >= n) return;
+            const uint32_t v = key(j + 1);
+            if (v >= V) return;
+#pragma unroll
+            for (int e = 0; e < 8; ++e) s[e] += u[q][e];
+            const bool on = key(j + 2) == v;
+            if (on && j + 1 < n) continue;
+            // the run, or this chunk's part of it, is complete
+            if (in) {
+                store_n(piece + i, D - i, s);
+            } else if (on) {
+                store_n(piece + D + i, D - i, s);
             } else {
-                // the first piece is slot 0 if the run begins its chunk, else slot 1
-                for (int64_t c = ca; c <= cb; ++c) {
-                    float u[8];
-                    const int64_t slot = 2 * c + (c == ca && f > c * kChunk ? 1 : 0);
-                    load_n(pieces + slot * D + i, D - i, u);
-#pragma unroll
-                    for (int e = 0; e < 8; ++e) s[e] += u[e];
-                }
+                finish_row(dW + (int64_t)v * ldw + i, D - i, s, scale, accumulate);
             }
+            in = false;
 #pragma unroll
-            for (int e = 0; e < 8; ++e) s[e] *= scale;
+            for (int e = 0; e < 8; ++e) s[e] = 0.f;
         }
-        if (accumulate) {
-            if (!has) continue;
-            float u[8];
-            load_n(w, D - i, u);
-#pragma unroll
-            for (int e = 0; e < 8; ++e) s[e] += u[e];
-        }
-        store_n(w, D - i, s);
     }
+}
+
+// Workgroups [0, sums): chunk blockIdx.x / spans, and of its columns a span of
+// 8 a thread.  The others, if dW is filled here: the rows without a token among
+// fill.rows at a time.  Sums and fill in one launch took 431 us for 32768 tokens
+// in 50257 rows of 8192, and 203 + 250 one after the other: the sums alone leave
+// most of HBM's rate unused.
+template <typename DT, typename WT>
+__global__ __launch_bounds__(256) void sums_kernel(const uint32_t *__restrict__ keys, const int32_t *__restrict__ order,
+                                                   int64_t T, int64_t V, int32_t chunk, int32_t sums, int32_t spans,
+                                                   const DT *__restrict__ dX, int64_t ldx, int64_t D, float scale,
+                                                   int32_t accumulate, WT *__restrict__ dW, int64_t ldw,
+                                                   float *__restrict__ pieces, Fill fill) {
+    __shared__ uint32_t k[kChunk + 2];  // the chunk's keys between their neighbours; or whether a row has no token
+    if ((int)blockIdx.x < sums) {
+        const int64_t c = blockIdx.x / spans, a = c * chunk;
+        const int n = (int)min((int64_t)chunk, T - a);
+        for (int j = threadIdx.x; j < n + 2; j += blockDim.x)
+            k[j] = a + j - 1 >= 0 && a + j - 1 < T ? keys[a + j - 1] : kNoKey;
+        __syncthreads();
+        const int64_t i = ((int64_t)(blockIdx.x % spans) * blockDim.x + threadIdx.x) * 8;
+        if (i < D) sum_chunk(k, n, (uint32_t)V, order + a, dX, ldx, D, i, scale, accumulate, dW, ldw, pieces + 2 * c * D);
+        return;
+    }
+    const int64_t step = (int64_t)(gridDim.x - sums) * fill.rows;
+    for (int64_t v0 = (int64_t)(blockIdx.x - sums) * fill.rows; v0 < V; v0 += step) {
+        if ((int)threadIdx.x < fill.rows) {
+            const int64_t v = v0 + threadIdx.x, at = before<false>(keys, T, (uint32_t)min(v, V));
+            k[threadIdx.x] = v < V && (at == T || keys[at] != (uint32_t)v);
+        }
+        __syncthreads();
+        for (int r = 0; r < fill.rows; ++r)
+            if (k[r]) fill_row(fill, v0 + r);
+        __syncthreads();
+    }
+}
+
+// Rows of dW whose run goes past the chunk it begins in (workgroup x: chunk):
+// its pieces, sixteen in flight at a time, added in order.
+template <typename WT>
+__global__ __launch_bounds__(256) void join_kernel(const uint32_t *__restrict__ keys, int64_t T, int64_t V,
+                                                   int32_t chunk, int64_t D, const float *__restrict__ pieces,
+                                                   float scale, int32_t accumulate, WT *__restrict__ dW, int64_t ldw) {
+    const int64_t c = blockIdx.x, a = c * chunk, b = min(a + chunk, T);
+    // its last key and the one after it, the one before the chunk and its first
+    const uint32_t v = keys[b - 1], next = keys[min(b, T - 1)], prev = keys[max(a - 1, (int64_t)0)], head = keys[a];
+    if (v >= V || b == T || next != v) return;          // it ends here
+    if (a > 0 && prev == v && head == v) return;        // it does not begin here
+    // the chunks that it goes on into begin with v
+    int64_t more = 0;
+    for (;; more += 64) {
+        const int64_t at = (c + 1 + more + (threadIdx.x & 63)) * chunk;
+        const uint64_t with = __ballot(at < T && keys[min(at, T - 1)] == v);
+        if (with != ~0ull) {
+            more += __builtin_ctzll(~with);
+            break;
+        }
+    }
+    const int64_t i = ((int64_t)blockIdx.y * blockDim.x + threadIdx.x) * 8;
+    if (i >= D) return;
+    float s[8];
+    load_n(pieces + (2 * c + 1) * D + i, D - i, s);
+    constexpr int U = 16;
+    for (int64_t m = 1; m <= more; m += U) {
+        float u[U][8];
+#pragma unroll
+        for (int q = 0; q < U; ++q) load_n(pieces + 2 * (c + min(m + q, more)) * D + i, m + q <= more ? D - i : 0, u[q]);
+#pragma unroll
+        for (int q = 0; q < U; ++q)
+#pragma unroll
+            for (int e = 0; e < 8; ++e) s[e] += u[q][e];
+    }
+    finish_row(dW + (int64_t)v * ldw + i, D - i, s, scale, accumulate);
 }
 
 // ---- host ---------------------------------------------------------------------------
 
+// Short lists take short chunks: more workgroups, each with fewer rows to add.
+int32_t chunk_of(int64_t T) { return T <= 8192 ? 16 : kChunk; }
+int64_t up4(int64_t x) { return (x + 3) / 4 * 4; }
+// Threads of a workgroup that sums rows of D elements, and workgroups a row.
+int64_t threads_of(int64_t D) { return D > 1024 ? 256 : D > 512 ? 128 : 64; }
+int64_t spans_of(int64_t D) { return ceil_div(D, threads_of(D) * 8); }
+
 // The workspace of a gradient: two sets of keys and positions (the sort goes
-// from one to the other), the runs' ends, the pieces.
+// from one to the other), the pieces.
 struct Work {
-    uint64_t keys[2], order[2], first, last, pieces, bytes;
+    uint64_t keys[2], order[2], pieces, bytes;
 };
-Work work_of(int64_t T, int64_t V, int64_t D) {
+Work work_of(int64_t T, int64_t D) {
     Work w;
     uint64_t at = 0;
     for (int k = 0; k < 2; ++k) {
@@ -242,12 +402,8 @@ Work work_of(int64_t T, int64_t V, int64_t D) {
         w.order[k] = at;
         at += up256((uint64_t)T * 4);
     }
-    w.first = at;
-    at += up256((uint64_t)V * 4);
-    w.last = at;
-    at += up256((uint64_t)V * 4);
     w.pieces = at;
-    at += up256((uint64_t)ceil_div(T, kChunk) * 2 * (uint64_t)D * 4);
+    at += up256((uint64_t)ceil_div(T, chunk_of(T)) * 2 * (uint64_t)D * 4);
     w.bytes = at;
     return w;
 }
@@ -272,36 +428,68 @@ template <typename DT, typename WT>
 hipError_t run_bwd(const zi_embedding *p, const void *ids, const void *dX, void *dW, char *work, hipStream_t s) {
     const int64_t T = p->T, V = p->V, D = p->D;
     const int64_t ldw = p->ldw ? p->ldw : D, ldx = p->ldx ? p->ldx : D;
-    const unsigned spans = (unsigned)ceil_div(D, 2048);
-    const Work w = work_of(T, V, D);
+    const int32_t chunk = chunk_of(T);
+    const Work w = work_of(T, D);
     uint32_t *keys[2] = {};
-    int32_t *order[2] = {}, *first = nullptr, *last = nullptr;
+    int32_t *order[2] = {};
     float *pieces = nullptr;
     int k = 0;
     hipError_t e;
+    // Zeros.  Where most rows stay without a token, all of dW is filled beside the
+    // sort, which leaves the device nearly idle; else the rows without a token
+    // beside the sums, which writes no row twice.  A workgroup looks at as many
+    // rows as 64 KiB hold (1 MiB: 3 % slower), fewer if there would be too few workgroups.
+    Fill fill{};
+    fill.base = reinterpret_cast<char *>(dW);
+    fill.V = V;
+    fill.stride = ldw * (int64_t)sizeof(WT);
+    fill.bytes = D * (int64_t)sizeof(WT);
+    fill.rows = (int32_t)max64(1, min64(min64((1 << 16) / fill.bytes, V / 1024), kMostRows));
+    const int64_t fills = p->accumulate ? 0 : min64(ceil_div(V, fill.rows), kMostGroups);
+    const bool at_sort = T > 0 && T <= V / 8;
     if (T > 0) {
         for (int j = 0; j < 2; ++j) {
             keys[j] = reinterpret_cast<uint32_t *>(work + w.keys[j]);
             order[j] = reinterpret_cast<int32_t *>(work + w.order[j]);
         }
-        first = reinterpret_cast<int32_t *>(work + w.first);
-        last = reinterpret_cast<int32_t *>(work + w.last);
         pieces = reinterpret_cast<float *>(work + w.pieces);
-        hipLaunchKernelGGL(sort_tile_kernel, dim3((unsigned)ceil_div(T, kTile), kTile / 256), dim3(256), 0, s, ids,
-                           p->ids64 != 0, T, V, keys[0], order[0]);
-        if ((e = hipGetLastError()) != hipSuccess) return e;
-        for (int64_t len = kTile; len < T; len *= kFan, k ^= 1) {
-            hipLaunchKernelGGL(merge_kernel, dim3((unsigned)ceil_div(T, 256)), dim3(256), 0, s, keys[k], order[k],
-                               keys[k ^ 1], order[k ^ 1], T, len);
+        const int64_t lists = T <= kOneTile ? 1 : ceil_div(T, kTile);
+        const int32_t per_tile = (int32_t)(lists > 1 ? kTile / 64 : ceil_div(T, 64));
+        const int32_t sorts = (int32_t)lists * per_tile;
+        const dim3 g((unsigned)(sorts + (at_sort ? fills : 0)));
+        auto sort = [&](auto tile) {
+            constexpr int TILE = decltype(tile)::value;
+            if (p->ids64)
+                hipLaunchKernelGGL((sort_tile_kernel<TILE, int64_t>), g, dim3(1024), 0, s, static_cast<const int64_t *>(ids),
+                                   T, V, keys[0], order[0], sorts, per_tile, fill);
+            else
+                hipLaunchKernelGGL((sort_tile_kernel<TILE, int32_t>), g, dim3(1024), 0, s, static_cast<const int32_t *>(ids),
+                                   T, V, keys[0], order[0], sorts, per_tile, fill);
+            return hipGetLastError();
+        };
+        e = T > kTile && lists == 1 ? sort(std::integral_constant<int, kOneTile>{}) : sort(std::integral_constant<int, kTile>{});
+        if (e != hipSuccess) return e;
+        if (lists > 1) {
+            hipLaunchKernelGGL(merge_tiles_kernel, dim3((unsigned)lists * (kTile / 256)), dim3(1024),
+                               (unsigned)(min64(up4(lists), kFan) * kTile * 4), s, keys[0], order[0], keys[1], order[1], T);
             if ((e = hipGetLastError()) != hipSuccess) return e;
+            k = 1;
+            for (int64_t len = (int64_t)kTile * kFan; len < T; len *= kFan, k ^= 1) {
+                hipLaunchKernelGGL(merge_kernel, dim3((unsigned)ceil_div(T, 256)), dim3(256), 0, s, keys[k], order[k],
+                                   keys[k ^ 1], order[k ^ 1], T, len);
+                if ((e = hipGetLastError()) != hipSuccess) return e;
+            }
         }
-        hipLaunchKernelGGL((piece_kernel<DT>), dim3((unsigned)ceil_div(T, kChunk), spans), dim3(256), 0, s, keys[k],
-                           order[k], T, V, static_cast<const DT *>(dX), ldx, D, first, last, pieces);
-        if ((e = hipGetLastError()) != hipSuccess) return e;
     }
-    hipLaunchKernelGGL((row_kernel<DT, WT>), dim3((unsigned)min64(V, kMostGroups), spans), dim3(256), 0, s, keys[k], order[k],
-                       T, V, static_cast<const DT *>(dX), ldx, D, first, last, pieces, p->scale, p->accumulate,
-                       static_cast<WT *>(dW), ldw);
+    const int64_t threads = threads_of(D), chunks = ceil_div(T, chunk), spans = spans_of(D);
+    const int64_t sums = chunks * spans, groups = sums + (at_sort ? 0 : fills);
+    if (groups == 0) return hipSuccess;
+    hipLaunchKernelGGL((sums_kernel<DT, WT>), dim3((unsigned)groups), dim3((unsigned)threads), 0, s, keys[k], order[k], T, V,
+                       chunk, (int32_t)sums, (int32_t)spans, static_cast<const DT *>(dX), ldx, D, p->scale, p->accumulate,
+                       static_cast<WT *>(dW), ldw, pieces, fill);
+    if ((e = hipGetLastError()) != hipSuccess || chunks < 2) return e;
+    hipLaunchKernelGGL((join_kernel<WT>), dim3((unsigned)chunks, (unsigned)spans), dim3((unsigned)threads), 0, s, keys[k], T,
+                       V, chunk, D, pieces, p->scale, p->accumulate, static_cast<WT *>(dW), ldw);
     return hipGetLastError();
 }
 
@@ -328,6 +516,9 @@ zi_status check(const zi_embedding *p, const void *ids, const void *W, const voi
     if (p->V < 1 || p->V > INT32_MAX) return fail(ZI_ERR_SHAPE, "V = %lld: 1 .. 2^31 - 1 rows", (long long)p->V);
     // spans of columns are a grid's second dimension
     if (p->D < 1 || p->D > 65535 * (int64_t)2048) return fail(ZI_ERR_SHAPE, "D = %lld is out of range", (long long)p->D);
+    // a launch's threads are a 32-bit number
+    if (ceil_div(p->T, chunk_of(p->T)) * spans_of(p->D) * threads_of(p->D) > (int64_t)UINT32_MAX - kMostGroups * 256)
+        return fail(ZI_ERR_SHAPE, "T = %lld rows of D = %lld are too many", (long long)p->T, (long long)p->D);
     if (!known(p->w_dtype) || !known(p->x_dtype))
         return fail(ZI_ERR_ARG, "unknown dtype (w %d, x %d)", p->w_dtype, p->x_dtype);
     if ((p->ldw != 0 && p->ldw < p->D) || (p->ldx != 0 && p->ldx < p->D))
@@ -357,7 +548,7 @@ extern "C" zi_status zi_embedding_fwd(const zi_embedding *p, const void *ids, co
 
 extern "C" uint64_t zi_embedding_bwd_bytes(int64_t T, int64_t V, int64_t D) {
     if (T < 1 || V < 1 || D < 1) return 0;
-    return work_of(T, V, D).bytes;
+    return work_of(T, D).bytes;
 }
 
 extern "C" zi_status zi_embedding_bwd(const zi_embedding *p, const void *ids, const void *dX, void *dW,
