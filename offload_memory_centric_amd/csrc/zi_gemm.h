@@ -356,8 +356,10 @@ struct RsOperand {
 // its LDS reads have returned, then meet the other waves.
 template <int n>
 __device__ __forceinline__ void wait_and_barrier() {
-    static_assert(n == 4 || n == 6 || n == 8 || n == 10, "the pipeline keeps one unit (n copies per wave) in flight");
-    if constexpr (n == 4)
+    static_assert(n == 2 || n == 4 || n == 6 || n == 8 || n == 10, "the pipeline keeps one unit (n copies per wave) in flight");
+    if constexpr (n == 2)
+        asm volatile("s_waitcnt vmcnt(2) lgkmcnt(0)\n\ts_barrier" ::: "memory");
+    else if constexpr (n == 4)
         asm volatile("s_waitcnt vmcnt(4) lgkmcnt(0)\n\ts_barrier" ::: "memory");
     else if constexpr (n == 6)
         asm volatile("s_waitcnt vmcnt(6) lgkmcnt(0)\n\ts_barrier" ::: "memory");
@@ -547,6 +549,94 @@ __device__ __forceinline__ void triangle_coords(int w, int n, int &tp, int &tq) 
     tq = 4 * g + c;
 }
 
+// What the epilogue of the orthogonalised update reads for four consecutive
+// elements (p, q .. q + 3) of a product; past its extents, those at its edge.
+template <int EPI>
+struct OrthIn {
+    u32x2 hi, lo;  // Apply
+    f32x4 l, dq;   // Poly
+    __device__ __forceinline__ void load(const OrthArgs &a, int64_t p, int64_t q) {
+        p = min(p, a.rows - 1);
+        q = min(q, a.cols - 4);
+        const int64_t off = p * a.ldc + q;
+        if constexpr (EPI == EPI_APPLY) {
+            hi = *reinterpret_cast<const u32x2 *>(a.hi + off);
+            lo = *reinterpret_cast<const u32x2 *>(a.lo + off);
+        }
+        if constexpr (EPI == EPI_POLY) {
+            l = *reinterpret_cast<const f32x4 *>(a.o32 + off);
+            dq = *reinterpret_cast<const f32x4 *>(a.diag + q);
+        }
+    }
+};
+// And what it reads for row p.
+template <int EPI>
+__device__ __forceinline__ float orth_row(const OrthArgs &a, int64_t p) {
+    p = min(p, a.rows - 1);
+    return EPI == EPI_APPLY ? a.bdiag[p] : EPI == EPI_POLY ? a.diag[p] : 0.f;
+}
+
+// What becomes of those elements: v their sums, d the row's value, r the scale;
+// mirror: the tile lies below the diagonal.
+template <typename T, int EPI>
+__device__ __forceinline__ void orth_store(const OrthArgs &a, int64_t p, int64_t q, const f32x4 &v,
+                                           const OrthIn<EPI> &in, float d, float r, bool mirror) {
+    const int64_t off = p * a.ldc + q;
+    if constexpr (EPI != EPI_APPLY) {
+        float o[4];  // the operand's values, zero on the diagonal
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            if constexpr (EPI == EPI_GRAM) {
+                o[e] = v[e] * r * r;
+                if (q + e == p) {
+                    a.diag[p] = o[e];
+                    o[e] = 0.f;
+                }
+            } else {
+                if (q + e == p) {
+                    a.bdiag[p] = a.ca + a.cb * d + a.cc * (v[e] + d * d);
+                    o[e] = 0.f;
+                } else {
+                    o[e] = a.cb * in.l[e] + a.cc * (v[e] + (d + in.dq[e]) * in.l[e]);
+                }
+            }
+        }
+        if constexpr (EPI == EPI_GRAM) *reinterpret_cast<f32x4 *>(a.o32 + off) = f32x4{o[0], o[1], o[2], o[3]};
+        uint16_t *c = static_cast<uint16_t *>(a.C);
+        uint32_t b[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) b[e] = bits16<T>(o[e]);
+        *reinterpret_cast<u32x2 *>(c + off) = u32x2{b[0] | (b[1] << 16), b[2] | (b[3] << 16)};
+        if (mirror) {
+#pragma unroll
+            for (int e = 0; e < 4; ++e) c[(q + e) * a.ldc + p] = (uint16_t)b[e];
+        }
+    } else {
+        float y[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            const float x = value16<T>((in.hi[e >> 1] >> (16 * (e & 1))) & 0xffffu) +
+                            value16<T>((in.lo[e >> 1] >> (16 * (e & 1))) & 0xffffu);
+            y[e] = (d * x + v[e]) * r;
+        }
+        if (a.hi_out) {
+            uint32_t h[4], l[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                h[e] = bits16<T>(y[e]);
+                l[e] = bits16<T>(y[e] - value16<T>(h[e]));
+            }
+            *reinterpret_cast<u32x2 *>(a.hi_out + off) = u32x2{h[0] | (h[1] << 16), h[2] | (h[3] << 16)};
+            *reinterpret_cast<u32x2 *>(a.lo + off) = u32x2{l[0] | (l[1] << 16), l[2] | (l[3] << 16)};
+        } else if (p < a.out_p) {
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                if (q + e < a.out_q)
+                    a.out[a.out_t ? (q + e) * a.out_ld + p : p * a.out_ld + q + e] = (uint16_t)bits16<__bf16>(y[e]);
+        }
+    }
+}
+
 // ---- the GEMM ---------------------------------------------------------------------
 
 // f(integral_constant<int, I>) for I = B .. E-1, unrolled by construction (a
@@ -581,7 +671,8 @@ __device__ constexpr int copy_at(int m) {
 //            a multiple of 320 but not of 256 (the down-projection's 1600);
 //   (6, 10)  192 x 320, gradient products whose p extent is such a width;
 //   (4, 4)   128 x 128, two workgroups per compute unit: the orthogonalised
-//            update's products where 256 x 256 tiles are too few.
+//            update's products where 256 x 256 tiles are too few;
+//   (2, 2)   64 x 64, four of them: the same for the smallest matrices.
 // PERSIST (accumulating products only): a workgroup takes the output tiles
 // of workgroup indices w, w + G, w + 2G, ... (G = the grid, a multiple of 8,
 // so all of them fall on the XCD of w and keep its tile order); between two
@@ -589,8 +680,8 @@ __device__ constexpr int copy_at(int m) {
 // the finished one's accumulators are stored.
 template <typename T, bool Q_RS, bool P_RS, int EPI, bool ALIGNED, int QB, int PB, bool PERSIST,
           typename ARGS = GemmArgs>
-__global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(QB * PB <= 16 ? 2 : 1,
-                                                                         QB * PB <= 16 ? 2 : 1)))
+__global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(QB * PB <= 4 ? 4 : QB * PB <= 16 ? 2 : 1,
+                                                                         QB * PB <= 4 ? 4 : QB * PB <= 16 ? 2 : 1)))
 void gemm_kernel(ARGS a, int tiles_p, int tiles_q) {
     constexpr int TQ = 32 * QB, TP = 32 * PB;
     static_assert(QB * PB <= 64, "accumulators beyond the 256 AGPRs of a lane");
@@ -807,6 +898,7 @@ void gemm_kernel(ARGS a, int tiles_p, int tiles_q) {
     constexpr int NC = ROW_Q ? PB : QB;  // blocks per row
     constexpr int NM = 2 * NR * NC;      // MFMAs per step
     constexpr int MH = NM / 2;
+    constexpr int CR = NM >= 8 * NC ? 4 : 2;  // MFMAs from one column read to the next
     u32x4 xr[NR - 1][2], xrl[2][2], xc[2][NC][2];
     auto qfrag = [&](const QBs &b0, const QBs &b1, int h, int f, u32x4 &out) __attribute__((always_inline)) {
         qo.frag(h ? b1 : b0, h, f, out);
@@ -835,8 +927,8 @@ void gemm_kernel(ARGS a, int tiles_p, int tiles_q) {
             (void)i;
             (void)j;
             acc[i][j] = mfma16<T>(ROW_Q ? rf : cf, ROW_Q ? cf : rf, acc[i][j]);
-            if constexpr (m % 4 == 1 && m < 8 * NC) {  // column fragment (m / 8, (m / 4) % 2) of the next step
-                constexpr int f = m / 8, hh = (m / 4) & 1;
+            if constexpr (m % CR == 1 && m < 2 * CR * NC) {  // column fragment (m / 2 CR, (m / CR) % 2) of the next step
+                constexpr int f = m / (2 * CR), hh = (m / CR) & 1;
                 cfrag(hh, f, xc[par ^ 1][f][hh]);
             }
             if constexpr ((m + 1) % (2 * NC) == 0 && m / (2 * NC) < NR - 1) {  // row m / (2 NC) of the next step
@@ -844,8 +936,8 @@ void gemm_kernel(ARGS a, int tiles_p, int tiles_q) {
                 rfrag(0, row, xr[row][0]);
                 rfrag(1, row, xr[row][1]);
             }
-            if constexpr (m == MH + 2) rfrag(0, NR - 1, xrl[par ^ 1][0]);
-            if constexpr (m == MH + 6) rfrag(1, NR - 1, xrl[par ^ 1][1]);
+            if constexpr (m == MH + CR / 2) rfrag(0, NR - 1, xrl[par ^ 1][0]);
+            if constexpr (m == MH + 3 * CR / 2) rfrag(1, NR - 1, xrl[par ^ 1][1]);
             if constexpr (m < MH) {
                 constexpr int k = copy_at<NS, MH>(m);
                 if constexpr (k >= 0) copy_a(k);
@@ -1078,23 +1170,33 @@ void gemm_kernel(ARGS a, int tiles_p, int tiles_q) {
             __syncthreads();
             if (*word != (uint32_t)(a.pieces - 1)) return;
             if (tid == 0) atomicExch(a.split_cnt + sj, 0u);
-            // sixteen blocks' loads are in flight at a time
+            // the loads of sixteen blocks are in flight at a time: of one
+            // piece, or with small tiles of NK, a divisor of `pieces`
             const __amdgpu_buffer_rsrc_t parts = __builtin_amdgcn_make_buffer_rsrc(base, 0, (int)kNumRecords, (int)kRsrcWord3);
-            static_for<0, QB * PB / 16>([&](auto C_) __attribute__((always_inline)) {
-                constexpr int c = decltype(C_)::value * 16;
-                f32x4 sum[16] = {};
-                for (int k = 0; k < a.pieces; ++k) {
-                    f32x4 o[16];
+            constexpr int NB = QB * PB < 16 ? QB * PB : 16, NK = 16 / NB;
+            static_for<0, QB * PB / NB>([&](auto C_) __attribute__((always_inline)) {
+                constexpr int c = decltype(C_)::value * NB;
+                f32x4 sum[NB] = {};
+                for (int k0 = 0; k0 < a.pieces; k0 += NK) {
+                    f32x4 o[NK][NB];
 #pragma unroll
-                    for (int b = 0; b < 16; ++b)
-                        o[b] = __builtin_bit_cast(f32x4, __builtin_amdgcn_raw_buffer_load_b128(
-                                                             parts, part_off + (c + b) * 1024, k * 4 * kWaveBytes, 16 /* sc1 */));
+                    for (int k = 0; k < NK; ++k)
 #pragma unroll
-                    for (int b = 0; b < 16; ++b)
-                        sum[b] = f32x4{sum[b][0] + o[b][0], sum[b][1] + o[b][1], sum[b][2] + o[b][2], sum[b][3] + o[b][3]};
+                        for (int b = 0; b < NB; ++b)
+                            o[k][b] = __builtin_bit_cast(
+                                f32x4, __builtin_amdgcn_raw_buffer_load_b128(
+                                           parts, part_off + (c + b) * 1024,
+                                           (k0 + k) * 4 * kWaveBytes, 16 /* sc1 */));
+#pragma unroll
+                    for (int k = 0; k < NK; ++k) {
+#pragma unroll
+                        for (int b = 0; b < NB; ++b)
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) sum[b][e] += o[k][b][e];
+                    }
                 }
 #pragma unroll
-                for (int b = 0; b < 16; ++b) acc[(c + b) / PB][(c + b) % PB] = sum[b];
+                for (int b = 0; b < NB; ++b) acc[(c + b) / PB][(c + b) % PB] = sum[b];
             });
         }
     }
@@ -1102,6 +1204,32 @@ void gemm_kernel(ARGS a, int tiles_p, int tiles_q) {
     // Epilogue.
     const int64_t pb = p0 + wp * (16 * PB) + (lane & 15);
     const int64_t qb = q0 + wq * (16 * QB) + 4 * (lane >> 4);
+    if constexpr (ORTH) {
+        // what one row of blocks reads is on its way while the one before it
+        // is stored
+        const float r = *a.scale;
+        float d[PB];
+#pragma unroll
+        for (int j = 0; j < PB; ++j) d[j] = orth_row<EPI>(a, pb + j * 16);
+        OrthIn<EPI> in[2][PB];
+#pragma unroll
+        for (int j = 0; j < PB; ++j) in[0][j].load(a, pb + j * 16, qb);
+        static_for<0, QB>([&](auto I_) __attribute__((always_inline)) {
+            constexpr int i = decltype(I_)::value;
+            const int64_t q = qb + i * 16;
+            if constexpr (i + 1 < QB) {
+#pragma unroll
+                for (int j = 0; j < PB; ++j) in[(i + 1) & 1][j].load(a, pb + j * 16, q + 16);
+            }
+#pragma unroll
+            for (int j = 0; j < PB; ++j) {
+                const int64_t p = pb + j * 16;
+                if (p < a.rows && q < a.cols)
+                    orth_store<T, EPI>(a, p, q, acc[i][j], in[i & 1][j], d[j], r, p0 != q0);
+            }
+        });
+        return;
+    }
     if constexpr (EPI == EPI_GELU || EPI == EPI_GELU_F32A) {
         // H = table[A]: the GeLU table of this type goes into the now idle LDS
         // (128 KiB: 32 one-KiB copies per wave).  Every wave's copies of the
@@ -1134,69 +1262,7 @@ void gemm_kernel(ARGS a, int tiles_p, int tiles_q) {
                 }
             }
             const int64_t off = p * a.ldc + q;
-            if constexpr (TRI) {
-                float o[4];  // the operand's values, zero on the diagonal
-                if constexpr (EPI == EPI_GRAM) {
-                    const float r = *a.scale;
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        o[e] = v[e] * r * r;
-                        if (q + e == p) {
-                            a.diag[p] = o[e];
-                            o[e] = 0.f;
-                        }
-                    }
-                    *reinterpret_cast<f32x4 *>(a.o32 + off) = f32x4{o[0], o[1], o[2], o[3]};
-                } else {
-                    const f32x4 l = *reinterpret_cast<const f32x4 *>(a.o32 + off);
-                    const f32x4 dq = *reinterpret_cast<const f32x4 *>(a.diag + q);
-                    const float dp = a.diag[p];
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        if (q + e == p) {
-                            a.bdiag[p] = a.ca + a.cb * dp + a.cc * (v[e] + dp * dp);
-                            o[e] = 0.f;
-                        } else {
-                            o[e] = a.cb * l[e] + a.cc * (v[e] + (dp + dq[e]) * l[e]);
-                        }
-                    }
-                }
-                uint16_t *c = static_cast<uint16_t *>(a.C);
-                uint32_t b[4];
-#pragma unroll
-                for (int e = 0; e < 4; ++e) b[e] = bits16<T>(o[e]);
-                *reinterpret_cast<u32x2 *>(c + off) = u32x2{b[0] | (b[1] << 16), b[2] | (b[3] << 16)};
-                if (p0 != q0) {
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) c[(q + e) * a.ldc + p] = (uint16_t)b[e];
-                }
-            } else if constexpr (EPI == EPI_APPLY) {
-                const float r = *a.scale, bd = a.bdiag[p];
-                const u32x2 hv = *reinterpret_cast<const u32x2 *>(a.hi + off);
-                const u32x2 lv = *reinterpret_cast<const u32x2 *>(a.lo + off);
-                float y[4];
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const float x = value16<T>((hv[e >> 1] >> (16 * (e & 1))) & 0xffffu) +
-                                    value16<T>((lv[e >> 1] >> (16 * (e & 1))) & 0xffffu);
-                    y[e] = (bd * x + v[e]) * r;
-                }
-                if (a.hi_out) {
-                    uint32_t h[4], l[4];
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        h[e] = bits16<T>(y[e]);
-                        l[e] = bits16<T>(y[e] - value16<T>(h[e]));
-                    }
-                    *reinterpret_cast<u32x2 *>(a.hi_out + off) = u32x2{h[0] | (h[1] << 16), h[2] | (h[3] << 16)};
-                    *reinterpret_cast<u32x2 *>(a.lo + off) = u32x2{l[0] | (l[1] << 16), l[2] | (l[3] << 16)};
-                } else if (p < a.out_p) {
-#pragma unroll
-                    for (int e = 0; e < 4; ++e)
-                        if (q + e < a.out_q)
-                            a.out[a.out_t ? (q + e) * a.out_ld + p : p * a.out_ld + q + e] = (uint16_t)bits16<__bf16>(y[e]);
-                }
-            } else if constexpr (EPI == EPI_F32 || EPI == EPI_ACC) {
+            if constexpr (EPI == EPI_F32 || EPI == EPI_ACC) {
                 *reinterpret_cast<f32x4 *>(static_cast<float *>(a.C) + off) = v;
             } else if constexpr (EPI == EPI_LP) {
                 u32x2 o = {bits16<T>(v[0]) | (bits16<T>(v[1]) << 16), bits16<T>(v[2]) | (bits16<T>(v[3]) << 16)};

@@ -79,18 +79,16 @@ struct OrthArgs : GemmArgs {
     int32_t out_t;                 // it is stored transposed: element (p, q) at out[q * out_ld + p]
 };
 
-// One of the products, on 256 x 256 tiles or (large false) 128 x 128 ones.  rows,
-// cols and red are multiples of 64.  split_part holds orth_split_bytes(large) and
-// split_cnt kOrthSplits counters, zero between launches.
-hipError_t launch_orth(OrthOp op, bool large, const OrthArgs &a, hipStream_t stream);
+// One of the products, on tiles of 256, 128 or 64 rows and columns.  rows, cols
+// and red are multiples of 64.  split_part holds kOrthSplitBytes and split_cnt
+// kOrthSplits counters, zero between launches.
+hipError_t launch_orth(OrthOp op, int tile, const OrthArgs &a, hipStream_t stream);
 
-// Tiles of a launch whose reduction is split, and their pieces: at most one
-// workgroup a compute unit with large tiles, two with small ones.
+// Workgroups that share tiles whose reduction is split: at most as many as run at
+// once, one a compute unit with tiles of 256, two with 128, four with 64.
 constexpr int kOrthUnits = 256;
-constexpr int kOrthSplits = 2 * kOrthUnits;
-constexpr uint64_t orth_split_bytes(bool large) {
-    return large ? (uint64_t)kOrthUnits * 256 * 256 * 4 : (uint64_t)kOrthSplits * 128 * 128 * 4;
-}
+constexpr int kOrthSplits = 4 * kOrthUnits;
+constexpr uint64_t kOrthSplitBytes = (uint64_t)kOrthUnits * 256 * 256 * 4;
 
 // Workgroups (one macro-tile each) that launch_gemm runs for a product with
 // `rows` output rows and `cols` output columns: the macro-tile is 256 x 256,

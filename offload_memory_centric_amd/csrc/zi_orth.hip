@@ -127,11 +127,16 @@ struct Work {
     uint64_t hi[2], lo, o16, b16, o32, diag, bdiag, sums, scale, cnt, part, bytes;
 };
 
-// 256 x 256 tiles where the triangle has at least one for each compute unit;
-// else 128 x 128, two workgroups a unit.
-bool large_tiles(int64_t mp) {
+// The side of the products' tiles: 256 where the triangle has at least one tile
+// for each compute unit; else 128, two workgroups a unit, or, for narrow
+// matrices and those whose m x k product fills no round of those, 64, four a
+// unit.  With tiles of 64 and of 128: 1024 x 1536 203 and 313 us, 1536 x 6144
+// 622 and 655, 2048 x 2048 417 and 561; 2048 x 8192 1110 and 958, 3008 x 3008
+// 1027 and 912.
+int tile_of(int64_t mp, int64_t kp) {
     const int64_t n = (mp + 255) / 256;
-    return n * (n + 1) / 2 >= kOrthUnits;
+    if (n * (n + 1) / 2 >= kOrthUnits) return 256;
+    return mp <= 1536 || ((mp + 127) / 128) * ((kp + 127) / 128) <= 2 * kOrthUnits ? 64 : 128;
 }
 
 Work work_of(int64_t M, int64_t K) {
@@ -158,7 +163,7 @@ Work work_of(int64_t M, int64_t K) {
     w.sums = take(kSums * 8);
     w.scale = take(8);
     w.cnt = take(kOrthSplits * 4);
-    w.part = take(orth_split_bytes(large_tiles(w.mp)));
+    w.part = take(kOrthSplitBytes);
     w.bytes = at;
     return w;
 }
@@ -167,7 +172,8 @@ template <typename T>
 hipError_t run(const zi_orth *o, const void *G, void *O, char *base, hipStream_t s) {
     const Work w = work_of(o->M, o->K);
     const int64_t ldg = o->ldg ? o->ldg : o->K, ldo = o->ldo ? o->ldo : o->K;
-    const bool tr = o->M > o->K, large = large_tiles(w.mp);
+    const bool tr = o->M > o->K;
+    const int tile = tile_of(w.mp, w.kp);
     double *sums = reinterpret_cast<double *>(base + w.sums);
     float *scale = reinterpret_cast<float *>(base + w.scale);
     uint16_t *hi[2] = {reinterpret_cast<uint16_t *>(base + w.hi[0]), reinterpret_cast<uint16_t *>(base + w.hi[1])};
@@ -194,17 +200,18 @@ hipError_t run(const zi_orth *o, const void *G, void *O, char *base, hipStream_t
     c.split_part = reinterpret_cast<float *>(base + w.part);
     c.split_cnt = cnt;
     c.rows = w.mp;
+    c.scale = scale + 1;  // one
     for (int step = 0; step < o->steps; ++step) {
         uint16_t *x = hi[step & 1];
         OrthArgs a = c;  // A = X X^T
-        a.scale = step == 0 ? scale : scale + 1;
+        if (step == 0) a.scale = scale;
         a.Q = a.P = x;
         a.ldq = a.ldp = w.kp;
         a.C = base + w.o16;
         a.ldc = w.mp;
         a.cols = w.mp;
         a.red = w.kp;
-        if ((e = launch_orth(OrthOp::Gram, large, a, s)) != hipSuccess) return e;
+        if ((e = launch_orth(OrthOp::Gram, tile, a, s)) != hipSuccess) return e;
         a = c;  // b A + c A^2
         a.Q = a.P = base + w.o16;
         a.ldq = a.ldp = w.mp;
@@ -212,9 +219,9 @@ hipError_t run(const zi_orth *o, const void *G, void *O, char *base, hipStream_t
         a.ldc = w.mp;
         a.cols = w.mp;
         a.red = w.mp;
-        if ((e = launch_orth(OrthOp::Poly, large, a, s)) != hipSuccess) return e;
+        if ((e = launch_orth(OrthOp::Poly, tile, a, s)) != hipSuccess) return e;
         a = c;  // a X + (b A + c A^2) X
-        a.scale = step == 0 ? scale : scale + 1;
+        if (step == 0) a.scale = scale;
         a.Q = a.hi = x;
         a.ldq = w.kp;
         a.P = base + w.b16;
@@ -232,7 +239,7 @@ hipError_t run(const zi_orth *o, const void *G, void *O, char *base, hipStream_t
             a.out_ld = ldo;
             a.out_t = tr;
         }
-        if ((e = launch_orth(OrthOp::Apply, large, a, s)) != hipSuccess) return e;
+        if ((e = launch_orth(OrthOp::Apply, tile, a, s)) != hipSuccess) return e;
     }
     return hipSuccess;
 }
