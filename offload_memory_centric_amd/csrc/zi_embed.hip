@@ -246,30 +246,88 @@ __global__ __launch_bounds__(256) void merge_kernel(const uint32_t *keys, const 
 
 // ---- the sums -----------------------------------------------------------------------
 
+// A thread's eight columns of a row of D: [at, at + 8), of which it writes those
+// from the skip-th on.  A row's last vector is moved back to end with the row,
+// so that the many rows that are read are read as whole vectors.  TINY: D < 8,
+// one thread's columns, read one by one.
+template <bool TINY>
+struct Cols {
+    int64_t at;
+    int skip, n;
+    __device__ __forceinline__ Cols(int64_t i, int64_t D) {
+        at = TINY ? 0 : min(i, D - 8);
+        skip = TINY ? 0 : (int)(i - at);
+        n = TINY ? (int)D : 8;
+    }
+    template <typename T>
+    __device__ __forceinline__ void load(const T *row, float (&v)[8]) const {
+        if constexpr (TINY) load_n(row, n, v);
+        else load8(row + at, v);
+    }
+    // Adds rows row(0) .. row(7), of which the first `many` count, in order;
+    // all eight are read at once.
+    template <typename T, typename F>
+    __device__ __forceinline__ void add8(F &&row, int64_t many, float (&s)[8]) const {
+        read8<T>(row, [&](int q, auto &&u) __attribute__((always_inline)) {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) s[e] += q < many ? u(e) : 0.f;
+        });
+    }
+    // use(q, value of element e) for q = 0 .. 7, after all eight rows are read.
+    template <typename T, typename F, typename G>
+    __device__ __forceinline__ void read8(F &&row, G &&use) const {
+        if constexpr (TINY) {
+#pragma unroll
+            for (int q = 0; q < 8; ++q) {
+                float u[8];
+                load_n(row(q), n, u);
+                use(q, [&](int e) { return u[e]; });
+            }
+        } else {
+            Raw8<T> u[8];
+#pragma unroll
+            for (int q = 0; q < 8; ++q) u[q].load(row(q) + at);
+            hold(u);
+#pragma unroll
+            for (int q = 0; q < 8; ++q) use(q, [&](int e) { return u[q][e]; });
+        }
+    }
+    template <typename T>
+    __device__ __forceinline__ void store(T *row, const float (&v)[8]) const {
+        if (!TINY && skip == 0) {
+            stream8(row + at, v);
+        } else {
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+                if (e >= skip && e < n) row[at + e] = (T)v[e];
+        }
+    }
+};
+
 // A row's sum, scaled and, with `accumulate`, added to what the row holds.
-template <typename WT>
-__device__ __forceinline__ void finish_row(WT *w, int64_t n, const float (&sum)[8], float scale, int32_t accumulate) {
+template <typename WT, bool TINY>
+__device__ __forceinline__ void finish_row(WT *row, const Cols<TINY> &my, const float (&sum)[8], float scale,
+                                           int32_t accumulate) {
     float s[8];
 #pragma unroll
     for (int e = 0; e < 8; ++e) s[e] = sum[e] * scale;
-    if (accumulate) {
+    if (accumulate) {  // (elements that it skips may be new already: they are not written)
         float u[8];
-        load_n(w, n, u);
+        my.load(row, u);
 #pragma unroll
         for (int e = 0; e < 8; ++e) s[e] += u[e];
     }
-    if (n >= 8) stream8(w, s);
-    else store_n(w, n, s);
+    my.store(row, s);
 }
 
-// Chunk `c` of the sorted tokens, columns [i, i + 8) of a thread: a run of equal
+// A chunk of the sorted tokens, a thread's columns: a run of equal
 // ids that lies in the chunk is summed and written to its row of dW; one that
 // comes in from the chunk before is summed into slot 0 of the chunk's pieces;
 // one that begins here and goes on into slot 1.  The rows of eight tokens are
 // in flight at a time, whatever runs they belong to.
-template <typename DT, typename WT>
+template <typename DT, typename WT, bool TINY>
 __device__ __forceinline__ void sum_chunk(const uint32_t *k, int n, uint32_t V, const int32_t *__restrict__ order,
-                                          const DT *__restrict__ dX, int64_t ldx, int64_t D, int64_t i, float scale,
+                                          const DT *__restrict__ dX, int64_t ldx, int64_t D, const Cols<TINY> &my, float scale,
                                           int32_t accumulate, WT *__restrict__ dW, int64_t ldw,
                                           float *__restrict__ piece) {
     constexpr int U = 8;
@@ -278,31 +336,31 @@ __device__ __forceinline__ void sum_chunk(const uint32_t *k, int n, uint32_t V, 
     bool in = key(0) == key(1);  // the run at hand came in from the left
     for (int j0 = 0; j0 < n; j0 += U) {
         if (key(j0 + 1) >= V) return;  // padding sorts last
-        float u[U][8];
+        bool done = false;
+        my.template read8<DT>(
+            [&](int q) __attribute__((always_inline)) { return dX + (int64_t)order[min(j0 + q, n - 1)] * ldx; },
+            [&](int q, auto &&u) __attribute__((always_inline)) {
+                const int j = j0 + q;
+                done = done || j >= n || key(j + 1) >= V;
+                if (done) return;
+                const uint32_t v = key(j + 1);
 #pragma unroll
-        for (int q = 0; q < U; ++q) load_n(dX + (int64_t)order[min(j0 + q, n - 1)] * ldx + i, D - i, u[q]);
+                for (int e = 0; e < 8; ++e) s[e] += u(e);
+                const bool on = key(j + 2) == v;
+                if (on && j + 1 < n) return;
+                // the run, or this chunk's part of it, is complete
+                if (in) {
+                    my.store(piece, s);
+                } else if (on) {
+                    my.store(piece + D, s);
+                } else {
+                    finish_row(dW + (int64_t)v * ldw, my, s, scale, accumulate);
+                }
+                in = false;
 #pragma unroll
-        for (int q = 0; q < U; ++q) {
-            const int j = j0 + q;
-            if (j >= n) return;
-            const uint32_t v = key(j + 1);
-            if (v >= V) return;
-#pragma unroll
-            for (int e = 0; e < 8; ++e) s[e] += u[q][e];
-            const bool on = key(j + 2) == v;
-            if (on && j + 1 < n) continue;
-            // the run, or this chunk's part of it, is complete
-            if (in) {
-                store_n(piece + i, D - i, s);
-            } else if (on) {
-                store_n(piece + D + i, D - i, s);
-            } else {
-                finish_row(dW + (int64_t)v * ldw + i, D - i, s, scale, accumulate);
-            }
-            in = false;
-#pragma unroll
-            for (int e = 0; e < 8; ++e) s[e] = 0.f;
-        }
+                for (int e = 0; e < 8; ++e) s[e] = 0.f;
+            });
+        if (done) return;
     }
 }
 
@@ -311,7 +369,7 @@ __device__ __forceinline__ void sum_chunk(const uint32_t *k, int n, uint32_t V, 
 // fill.rows at a time.  Sums and fill in one launch took 431 us for 32768 tokens
 // in 50257 rows of 8192, and 203 + 250 one after the other: the sums alone leave
 // most of HBM's rate unused.
-template <typename DT, typename WT>
+template <typename DT, typename WT, bool TINY>
 __global__ __launch_bounds__(256) void sums_kernel(const uint32_t *__restrict__ keys, const int32_t *__restrict__ order,
                                                    int64_t T, int64_t V, int32_t chunk, int32_t sums, int32_t spans,
                                                    const DT *__restrict__ dX, int64_t ldx, int64_t D, float scale,
@@ -325,7 +383,8 @@ __global__ __launch_bounds__(256) void sums_kernel(const uint32_t *__restrict__ 
             k[j] = a + j - 1 >= 0 && a + j - 1 < T ? keys[a + j - 1] : kNoKey;
         __syncthreads();
         const int64_t i = ((int64_t)(blockIdx.x % spans) * blockDim.x + threadIdx.x) * 8;
-        if (i < D) sum_chunk(k, n, (uint32_t)V, order + a, dX, ldx, D, i, scale, accumulate, dW, ldw, pieces + 2 * c * D);
+        if (i < D)
+            sum_chunk(k, n, (uint32_t)V, order + a, dX, ldx, D, Cols<TINY>(i, D), scale, accumulate, dW, ldw, pieces + 2 * c * D);
         return;
     }
     const int64_t step = (int64_t)(gridDim.x - sums) * fill.rows;
@@ -342,8 +401,8 @@ __global__ __launch_bounds__(256) void sums_kernel(const uint32_t *__restrict__ 
 }
 
 // Rows of dW whose run goes past the chunk it begins in (workgroup x: chunk):
-// its pieces, sixteen in flight at a time, added in order.
-template <typename WT>
+// its pieces, eight in flight at a time, added in order.
+template <typename WT, bool TINY>
 __global__ __launch_bounds__(256) void join_kernel(const uint32_t *__restrict__ keys, int64_t T, int64_t V,
                                                    int32_t chunk, int64_t D, const float *__restrict__ pieces,
                                                    float scale, int32_t accumulate, WT *__restrict__ dW, int64_t ldw) {
@@ -364,25 +423,20 @@ __global__ __launch_bounds__(256) void join_kernel(const uint32_t *__restrict__ 
     }
     const int64_t i = ((int64_t)blockIdx.y * blockDim.x + threadIdx.x) * 8;
     if (i >= D) return;
+    const Cols<TINY> my(i, D);
     float s[8];
-    load_n(pieces + (2 * c + 1) * D + i, D - i, s);
-    constexpr int U = 16;
-    for (int64_t m = 1; m <= more; m += U) {
-        float u[U][8];
-#pragma unroll
-        for (int q = 0; q < U; ++q) load_n(pieces + 2 * (c + min(m + q, more)) * D + i, m + q <= more ? D - i : 0, u[q]);
-#pragma unroll
-        for (int q = 0; q < U; ++q)
-#pragma unroll
-            for (int e = 0; e < 8; ++e) s[e] += u[q][e];
-    }
-    finish_row(dW + (int64_t)v * ldw + i, D - i, s, scale, accumulate);
+    my.load(pieces + (2 * c + 1) * D, s);
+    for (int64_t m = 1; m <= more; m += 8)
+        my.template add8<float>(
+            [&](int q) __attribute__((always_inline)) { return pieces + 2 * (c + min(m + q, more)) * D; }, more - m + 1, s);
+    finish_row(dW + (int64_t)v * ldw, my, s, scale, accumulate);
 }
 
 // ---- host ---------------------------------------------------------------------------
 
-// Short lists take short chunks: more workgroups, each with fewer rows to add.
-int32_t chunk_of(int64_t T) { return T <= 8192 ? 16 : kChunk; }
+// Short lists, and short rows, take short chunks: more workgroups, each with
+// fewer rows to add one after another.
+int32_t chunk_of(int64_t T, int64_t D) { return T <= 8192 ? 16 : D <= 512 ? 32 : kChunk; }
 int64_t up4(int64_t x) { return (x + 3) / 4 * 4; }
 // Threads of a workgroup that sums rows of D elements, and workgroups a row.
 int64_t threads_of(int64_t D) { return D > 1024 ? 256 : D > 512 ? 128 : 64; }
@@ -403,7 +457,7 @@ Work work_of(int64_t T, int64_t D) {
         at += up256((uint64_t)T * 4);
     }
     w.pieces = at;
-    at += up256((uint64_t)ceil_div(T, chunk_of(T)) * 2 * (uint64_t)D * 4);
+    at += up256((uint64_t)ceil_div(T, chunk_of(T, D)) * 2 * (uint64_t)D * 4);
     w.bytes = at;
     return w;
 }
@@ -424,11 +478,11 @@ hipError_t run_fwd(const zi_embedding *p, const void *ids, const void *W, void *
     return go(std::integral_constant<int, 256>{});
 }
 
-template <typename DT, typename WT>
+template <typename DT, typename WT, bool TINY>
 hipError_t run_bwd(const zi_embedding *p, const void *ids, const void *dX, void *dW, char *work, hipStream_t s) {
     const int64_t T = p->T, V = p->V, D = p->D;
     const int64_t ldw = p->ldw ? p->ldw : D, ldx = p->ldx ? p->ldx : D;
-    const int32_t chunk = chunk_of(T);
+    const int32_t chunk = chunk_of(T, D);
     const Work w = work_of(T, D);
     uint32_t *keys[2] = {};
     int32_t *order[2] = {};
@@ -484,11 +538,11 @@ hipError_t run_bwd(const zi_embedding *p, const void *ids, const void *dX, void 
     const int64_t threads = threads_of(D), chunks = ceil_div(T, chunk), spans = spans_of(D);
     const int64_t sums = chunks * spans, groups = sums + (at_sort ? 0 : fills);
     if (groups == 0) return hipSuccess;
-    hipLaunchKernelGGL((sums_kernel<DT, WT>), dim3((unsigned)groups), dim3((unsigned)threads), 0, s, keys[k], order[k], T, V,
+    hipLaunchKernelGGL((sums_kernel<DT, WT, TINY>), dim3((unsigned)groups), dim3((unsigned)threads), 0, s, keys[k], order[k], T, V,
                        chunk, (int32_t)sums, (int32_t)spans, static_cast<const DT *>(dX), ldx, D, p->scale, p->accumulate,
                        static_cast<WT *>(dW), ldw, pieces, fill);
     if ((e = hipGetLastError()) != hipSuccess || chunks < 2) return e;
-    hipLaunchKernelGGL((join_kernel<WT>), dim3((unsigned)chunks, (unsigned)spans), dim3((unsigned)threads), 0, s, keys[k], T,
+    hipLaunchKernelGGL((join_kernel<WT, TINY>), dim3((unsigned)chunks, (unsigned)spans), dim3((unsigned)threads), 0, s, keys[k], T,
                        V, chunk, D, pieces, p->scale, p->accumulate, static_cast<WT *>(dW), ldw);
     return hipGetLastError();
 }
@@ -517,7 +571,7 @@ zi_status check(const zi_embedding *p, const void *ids, const void *W, const voi
     // spans of columns are a grid's second dimension
     if (p->D < 1 || p->D > 65535 * (int64_t)2048) return fail(ZI_ERR_SHAPE, "D = %lld is out of range", (long long)p->D);
     // a launch's threads are a 32-bit number
-    if (ceil_div(p->T, chunk_of(p->T)) * spans_of(p->D) * threads_of(p->D) > (int64_t)UINT32_MAX - kMostGroups * 256)
+    if (ceil_div(p->T, chunk_of(p->T, p->D)) * spans_of(p->D) * threads_of(p->D) > (int64_t)UINT32_MAX - kMostGroups * 256)
         return fail(ZI_ERR_SHAPE, "T = %lld rows of D = %lld are too many", (long long)p->T, (long long)p->D);
     if (!known(p->w_dtype) || !known(p->x_dtype))
         return fail(ZI_ERR_ARG, "unknown dtype (w %d, x %d)", p->w_dtype, p->x_dtype);
@@ -564,7 +618,9 @@ extern "C" zi_status zi_embedding_bwd(const zi_embedding *p, const void *ids, co
     if (!aligned(workspace, 256)) return fail(ZI_ERR_ALIGN, "the workspace is not 256-byte aligned");
     hipStream_t s = static_cast<hipStream_t>(stream);
     const hipError_t e = with_types(p->w_dtype, p->x_dtype, [&](auto w, auto x) {
-        return run_bwd<decltype(x), decltype(w)>(p, ids, dX, dW, static_cast<char *>(workspace), s);
+        char *work = static_cast<char *>(workspace);
+        return p->D < 8 ? run_bwd<decltype(x), decltype(w), true>(p, ids, dX, dW, work, s)
+                        : run_bwd<decltype(x), decltype(w), false>(p, ids, dX, dW, work, s);
     });
     if (e != hipSuccess) return fail(ZI_ERR_HIP, "embedding gradient: %s", hipGetErrorString(e));
     return ZI_OK;

@@ -109,6 +109,21 @@ struct Raw8<float> {
     __device__ __forceinline__ void forget() { asm volatile("" : "+v"(v[0]), "+v"(v[1])); }
 };
 
+// All of eight vectors are loaded at this point: none of their loads is put off
+// until its value is needed.
+template <typename T>
+__device__ __forceinline__ void hold(Raw8<T> (&u)[8]) {
+    asm volatile(""
+                 : "+v"(u[0].v), "+v"(u[1].v), "+v"(u[2].v), "+v"(u[3].v), "+v"(u[4].v), "+v"(u[5].v), "+v"(u[6].v),
+                   "+v"(u[7].v));
+}
+__device__ __forceinline__ void hold(Raw8<float> (&u)[8]) {
+    asm volatile(""
+                 : "+v"(u[0].v[0]), "+v"(u[0].v[1]), "+v"(u[1].v[0]), "+v"(u[1].v[1]), "+v"(u[2].v[0]), "+v"(u[2].v[1]),
+                   "+v"(u[3].v[0]), "+v"(u[3].v[1]), "+v"(u[4].v[0]), "+v"(u[4].v[1]), "+v"(u[5].v[0]), "+v"(u[5].v[1]),
+                   "+v"(u[6].v[0]), "+v"(u[6].v[1]), "+v"(u[7].v[0]), "+v"(u[7].v[1]));
+}
+
 // Eight elements of an array whose type is known at run time only (the same
 // for every lane).
 __device__ __forceinline__ void load8(const void *p, int dtype, int at, float (&v)[8]) {
