@@ -29,30 +29,32 @@ def _code(t, name: str) -> int:
 
 
 def _here(t, name: str) -> None:
-    if t.device.type != "cuda":
+    if not t.is_cuda:
         raise ValueError("%s must be a device tensor" % name)
 
 
 def _rows(t, rows: int, cols: int, name: str, dtype=None) -> int:
     """The row stride of a [rows, cols] device tensor whose rows are contiguous."""
-    if dtype is not None and t.dtype != dtype:
+    if dtype is not None and t.dtype is not dtype:
         raise TypeError("%s has dtype %s, expected %s" % (name, t.dtype, dtype))
     _here(t, name)
-    if t.dim() != 2 or t.shape[0] != rows or t.shape[1] != cols:
+    if t.shape != (rows, cols):
         raise ValueError("%s has shape %s, expected (%d, %d)" % (name, tuple(t.shape), rows, cols))
+    if t.is_contiguous():
+        return cols
     if cols > 1 and t.stride(1) != 1:
         raise ValueError("the rows of %s must be contiguous" % name)
-    ld = t.stride(0) if rows > 1 else cols
+    ld = t.stride(0)
     if ld < cols:
         raise ValueError("the rows of %s overlap" % name)
     return ld
 
 
 def _vector(t, n: int, name: str, dtype=None) -> None:
-    if dtype is not None and t.dtype != dtype:
+    if dtype is not None and t.dtype is not dtype:
         raise TypeError("%s has dtype %s, expected %s" % (name, t.dtype, dtype))
     _here(t, name)
-    if t.dim() != 1 or t.shape[0] != n or (n > 1 and t.stride(0) != 1):
+    if t.shape != (n,) or not t.is_contiguous():
         raise ValueError("%s must be a contiguous vector of %d elements" % (name, n))
 
 
@@ -65,8 +67,17 @@ def _bytes(work) -> int:
     return work.numel() * work.element_size()
 
 
+# The handle of torch's current stream; the public call builds a stream object
+# first, which takes longer than the rest of a small call's checks.
+_current = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
 def _on(stream, t):
-    return torch.cuda.current_stream(t.device) if stream is None else stream
+    if stream is not None:
+        return stream
+    if _current is not None:
+        return _current(t.device.index)
+    return torch.cuda.current_stream(t.device)
 
 
 def _matrix(t, name: str):
@@ -76,14 +87,15 @@ def _matrix(t, name: str):
 
 
 def _params(gamma, beta, D: int) -> int:
-    code = zi.ZI_F32
-    for t, name in ((gamma, "gamma"), (beta, "beta")):
-        if t is not None:
-            _vector(t, D, name)
-            code = _code(t, name)
-    if gamma is not None and beta is not None and gamma.dtype != beta.dtype:
-        raise TypeError("gamma and beta have different dtypes")
-    return code
+    """The type of gamma and beta, of which either may be None."""
+    given = beta if gamma is None else gamma
+    if given is None:
+        return zi.ZI_F32
+    if gamma is not None:
+        _vector(gamma, D, "gamma")
+    if beta is not None:
+        _vector(beta, D, "beta", given.dtype)
+    return _code(given, "gamma" if given is gamma else "beta")
 
 
 def layer_norm_fwd(X, gamma, beta, Y, mean=None, rstd=None, eps: float = 1e-5, R=None, S=None, stream=None) -> None:
