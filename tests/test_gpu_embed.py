@@ -210,3 +210,27 @@ def test_streams_and_graph():
         graph.replay()
         torch.cuda.synchronize()
         assert torch.equal(X, X0) and torch.equal(dW, dW0), k
+
+
+def test_offsets_past_32_bits():
+    """A table of more than 2^32 bytes and 2^31 elements: its first and last rows."""
+    from offload_memory_centric_amd import layers
+    V, D, T = 270000, 8200, 300
+    g = gen(12)
+    W = torch.empty((V, D), dtype=torch.float16, device="cuda")
+    W[:100].normal_(generator=g)
+    W[-100:].normal_(generator=g)
+    ids = torch.randint(0, 100, (T,), generator=g, device="cuda")
+    ids[::2] += V - 100
+    X = torch.empty((T, D), dtype=torch.float16, device="cuda")
+    layers.embedding_fwd(ids, W, X)
+    torch.cuda.synchronize()
+    assert torch.equal(X, W[ids])
+    W.fill_(7)
+    layers.embedding_bwd(ids, X, W, layers.workspace(layers.embedding_bwd_bytes(T, V, D)))
+    low = torch.where(ids >= 100, ids - (V - 200), ids)
+    small = torch.empty((200, D), dtype=torch.float16, device="cuda")
+    layers.embedding_bwd(low, X, small, layers.workspace(layers.embedding_bwd_bytes(T, 200, D)))
+    torch.cuda.synchronize()
+    assert torch.equal(W[:100], small[:100]) and torch.equal(W[-100:], small[-100:])
+    assert not W[100:-100].any()

@@ -339,3 +339,34 @@ def test_streams_and_graph():
         graph.replay()
         torch.cuda.synchronize()
         assert all(torch.equal(a, b) for a, b in zip(outs, eager)), k
+
+
+def test_offsets_past_32_bits():
+    """More than 2^32 bytes and 2^31 elements: the last rows."""
+    from offload_memory_centric_amd import layers
+    T, D = 90000, 25000
+    g = gen(11)
+    X = torch.empty((T, D), dtype=torch.bfloat16, device="cuda")
+    X[:50].normal_(generator=g)
+    X[50:-50].fill_(1.0)
+    X[-50:].normal_(generator=g)
+    Y = torch.empty_like(X)
+    mean, rstd = torch.empty(T, device="cuda"), torch.empty(T, device="cuda")
+    gamma = torch.randn(D, generator=g, device="cuda")
+    layers.layer_norm_fwd(X, gamma, None, Y, mean, rstd, eps=EPS)
+    part = torch.cat([X[:50], X[-50:]])
+    y, m, r = torch.empty_like(part), torch.empty(100, device="cuda"), torch.empty(100, device="cuda")
+    layers.layer_norm_fwd(part, gamma, None, y, m, r, eps=EPS)
+    torch.cuda.synchronize()
+    assert torch.equal(torch.cat([Y[:50], Y[-50:]]), y) and torch.equal(torch.cat([mean[:50], mean[-50:]]), m)
+    assert not Y[1000:1010].any() and float(mean[45000]) == 1.0
+    dX = Y  # reused: the gradient of the constant rows is rstd (g - mean(g)), of the others as alone
+    dY = X
+    dg, db = torch.empty(D, device="cuda"), torch.empty(D, device="cuda")
+    layers.layer_norm_bwd(dY, X, gamma, mean, rstd, dX, dg, db, layers.workspace(layers.layer_norm_bwd_bytes(T, D)))
+    dx, dg1, db1 = torch.empty_like(part), torch.empty(D, device="cuda"), torch.empty(D, device="cuda")
+    layers.layer_norm_bwd(part, part, gamma, m, r, dx, dg1, db1, layers.workspace(layers.layer_norm_bwd_bytes(100, D)))
+    torch.cuda.synchronize()
+    assert torch.equal(torch.cat([dX[:50], dX[-50:]]), dx)
+    want = part.double().sum(0) + (T - 100)
+    close(db, want, (T / 64 + 100) * U * (part.double().abs().sum(0) + T), "dbeta")
