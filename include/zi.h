@@ -748,8 +748,8 @@ zi_status zi_embedding_bwd(const zi_embedding *emb, const void *ids, const void 
  *   X <- a X + (b A + c A^2) X (X (b A + c A^2)),
  * which acts on the singular values of X by an odd polynomial; O = RNE(X) in
  * bf16.  The products take fp16 operands and fp32 sums; what X carries over
- * from step to step is held in 22 bits.  O is within about 1e-3 |O| of the
- * exact polynomial, so that bf16 holds all of its accuracy.  With NaN or an
+ * from step to step is held in 22 bits: before its rounding to bf16, O is within
+ * about 1e-3 |O| of the exact polynomial, which is less than that rounding.  With NaN or an
  * infinity in G, O is NaN; with G zero, O is zero.  O overlaps neither G nor
  * the workspace. */
 #define ZI_ORTH_MOST 262144

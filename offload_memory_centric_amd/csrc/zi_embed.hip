@@ -18,6 +18,11 @@
 // are then merged, the place of a key being its place in its own list plus the
 // number of keys before it in every other one (binary searches).  32768 tokens
 // take one merge.
+// What it takes.  Forward, 32768 tokens of 25600 fp16 values: 474 us, 2.18 GB at
+// 4.6 TB/s.  Gradient of 32768 tokens of 8192 bf16 values in 50257 fp32 rows:
+// 466 us, of which the sums and the zeros (2.15 GB) are 405, 5.3 TB/s, and the
+// sort 20.  Of 2047 tokens of 512 fp32 values, 107 MB of them zeros: 30 us; the
+// sort, the sums and the joins wait for latencies, the fill runs beside the sort.
 #include <hip/hip_runtime.h>
 #include <math.h>
 #include <stdint.h>

@@ -67,7 +67,7 @@ hipError_t launch_gemm(GemmOp op, int dtype, const GemmArgs &a, hipStream_t stre
 enum class OrthOp : int { Gram = 0, Poly = 1, Apply = 2 };
 struct OrthArgs : GemmArgs {
     int32_t pieces;       // workgroups that share the reduction of each of the last split_tail tiles
-    const float *scale;   // Gram, Apply: true x = *scale times the planes
+    const float *scale;   // true x = *scale times the planes
     float ca, cb, cc;     // a, b, c
     float *o32;           // [rows][ldc], as O
     float *diag, *bdiag;  // D, bd
@@ -80,15 +80,15 @@ struct OrthArgs : GemmArgs {
 };
 
 // One of the products, on tiles of 256, 128 or 64 rows and columns.  rows, cols
-// and red are multiples of 64.  split_part holds kOrthSplitBytes and split_cnt
-// kOrthSplits counters, zero between launches.
+// and red are multiples of 64.  split_part holds orth_split_bytes(tile) and
+// split_cnt kOrthSplits counters, zero between launches.
 hipError_t launch_orth(OrthOp op, int tile, const OrthArgs &a, hipStream_t stream);
 
 // Workgroups that share tiles whose reduction is split: at most as many as run at
 // once, one a compute unit with tiles of 256, two with 128, four with 64.
 constexpr int kOrthUnits = 256;
 constexpr int kOrthSplits = 4 * kOrthUnits;
-constexpr uint64_t kOrthSplitBytes = (uint64_t)kOrthUnits * 256 * 256 * 4;
+constexpr uint64_t orth_split_bytes(int tile) { return (uint64_t)kOrthUnits * (256 / tile) * tile * tile * 4; }
 
 // Workgroups (one macro-tile each) that launch_gemm runs for a product with
 // `rows` output rows and `cols` output columns: the macro-tile is 256 x 256,

@@ -19,6 +19,13 @@
 // fp32.  The planes of X_0 are G times a power of two (|G| then lies in
 // [2^14, 2^15), so no element overflows and few are subnormal); the rest of the
 // normalisation is a factor of the first step, in fp32.
+//
+// What it takes.  32768 x 8192 in bf16: 28.0 ms, of which a step's A is 1.56 ms
+// (1450 TFLOP/s on the tiles formed, the matrix cores busy 0.84 of the time),
+// b A + c A^2 0.49 ms, and the product with X 3.56 ms (1235 TFLOP/s, busy 0.66:
+// each tile's planes are read and written after its last multiplication).  Small
+// matrices are bound by their seventeen launches: 512 x 512 takes 122 us, seven
+// a launch, of which four to five pass between any two launches on a stream.
 #include <hip/hip_runtime.h>
 #include <math.h>
 #include <stdint.h>
@@ -163,7 +170,7 @@ Work work_of(int64_t M, int64_t K) {
     w.sums = take(kSums * 8);
     w.scale = take(8);
     w.cnt = take(kOrthSplits * 4);
-    w.part = take(kOrthSplitBytes);
+    w.part = take(orth_split_bytes(tile_of(w.mp, w.kp)));
     w.bytes = at;
     return w;
 }
