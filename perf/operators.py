@@ -175,11 +175,15 @@ def _run_own(s):
         layers.embedding_fwd(s["ids"], s["W"], s["X"], scale=s["scale"])
         return s["X"]
     if op == "embed_bwd":
-        acc = s["before"] is not None
-        if acc:
-            s["dW"].copy_(s["before"])
-        layers.embedding_bwd(s["ids"], s["dX"], s["dW"], s["work"], scale=s["scale"], accumulate=acc)
-        return s["dW"]
+        # an fp32 gradient is accumulated where the earlier micro-batch left it, as the plain form does; one in
+        # 16 bits, which the plain form rounds into a new tensor, into a copy
+        acc, dW = s["before"] is not None, s["dW"]
+        if acc and s["before"].dtype == torch.float32:
+            dW = s["before"]
+        elif acc:
+            dW.copy_(s["before"])
+        layers.embedding_bwd(s["ids"], s["dX"], dW, s["work"], scale=s["scale"], accumulate=acc)
+        return dW
     layers.orthogonalize(s["G"], s["O"], s["work"], steps=NS_STEPS, coeffs=NS_COEFFS, eps=NS_EPS)
     return s["O"]
 
