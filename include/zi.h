@@ -720,7 +720,7 @@ zi_status zi_layer_norm_bwd(const zi_norm *norm, const void *dY, const void *S, 
 /* A table of V rows of D elements, looked up by T token ids.  An id outside
  * [0, V) marks padding: a zero row of X, and no gradient. */
 typedef struct {
-    int64_t T;           /* tokens: 0 .. 2^31 - 1025                     */
+    int64_t T;           /* tokens: 0 .. 2^27                            */
     int64_t V;           /* rows of the table: 1 .. 2^31 - 1             */
     int64_t D;           /* columns: 1 .. 65535 * 2048                   */
     int64_t ldw, ldx;    /* row strides of W and dW, of X and dX; 0 = D  */

@@ -325,10 +325,10 @@ __device__ __forceinline__ void finish_row(WT *row, const Cols<TINY> &my, const 
     my.store(row, s);
 }
 
-// A chunk of the sorted tokens, a thread's columns: a run of equal
-// ids that lies in the chunk is summed and written to its row of dW; one that
-// comes in from the chunk before is summed into slot 0 of the chunk's pieces;
-// one that begins here and goes on into slot 1.  The rows of eight tokens are
+// A chunk of the sorted tokens, a thread's columns: a run of equal ids that lies
+// in the chunk is summed and written to its row of dW; one that comes in from
+// the chunk before is summed into slot 0 of the chunk's pieces; one that begins
+// here and goes on into slot 1.  The rows of eight tokens are
 // in flight at a time, whatever runs they belong to.
 template <typename DT, typename WT, bool TINY>
 __device__ __forceinline__ void sum_chunk(const uint32_t *k, int n, uint32_t V, const int32_t *__restrict__ order,
@@ -570,12 +570,12 @@ bool aligned(const void *p, uint64_t to) { return ((uintptr_t)p & (to - 1)) == 0
 
 zi_status check(const zi_embedding *p, const void *ids, const void *W, const void *X) {
     if (!p) return fail(ZI_ERR_ARG, "embedding is NULL");
-    // a chunk's borders and a token's position are 32-bit numbers
-    if (p->T < 0 || p->T > INT32_MAX - kTile) return fail(ZI_ERR_SHAPE, "T = %lld is out of range", (long long)p->T);
+    // the sort takes sixteen threads a token, and a launch's threads are a 32-bit number
+    if (p->T < 0 || p->T > (1 << 27)) return fail(ZI_ERR_SHAPE, "T = %lld: 0 .. 2^27 tokens", (long long)p->T);
     if (p->V < 1 || p->V > INT32_MAX) return fail(ZI_ERR_SHAPE, "V = %lld: 1 .. 2^31 - 1 rows", (long long)p->V);
     // spans of columns are a grid's second dimension
     if (p->D < 1 || p->D > 65535 * (int64_t)2048) return fail(ZI_ERR_SHAPE, "D = %lld is out of range", (long long)p->D);
-    // a launch's threads are a 32-bit number
+    // so do the sums'
     if (ceil_div(p->T, chunk_of(p->T, p->D)) * spans_of(p->D) * threads_of(p->D) > (int64_t)UINT32_MAX - kMostGroups * 256)
         return fail(ZI_ERR_SHAPE, "T = %lld rows of D = %lld are too many", (long long)p->T, (long long)p->D);
     if (!known(p->w_dtype) || !known(p->x_dtype))

@@ -419,8 +419,16 @@ __global__ __launch_bounds__(1024) void norm_fold_kernel(const float *part, int6
     const int lane = threadIdx.x & 63, share = threadIdx.x >> 6;
     const int64_t col = (int64_t)blockIdx.x * 64 + lane;  // of [dgamma, dbeta]
     float s = 0.f;
-    if (col < 2 * D)
-        for (int p = share; p < parts; p += 16) s += part[p * 2 * D + col];
+    if (col < 2 * D) {
+        constexpr int U = 8;  // loads in flight
+        for (int p = share; p < parts; p += 16 * U) {
+            float v[U];
+#pragma unroll
+            for (int u = 0; u < U; ++u) v[u] = part[min(p + 16 * u, parts - 1) * 2 * D + col];
+#pragma unroll
+            for (int u = 0; u < U; ++u) s += p + 16 * u < parts ? v[u] : 0.f;
+        }
+    }
     sum[share][lane] = s;
     __syncthreads();
     if (share || col >= 2 * D) return;

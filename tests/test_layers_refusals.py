@@ -92,7 +92,7 @@ def test_null_problem(zi):
 
 
 EMB_BAD = [
-    (dict(T=-1), "ZI_ERR_SHAPE"), (dict(T=(1 << 31) - 1), "ZI_ERR_SHAPE"), (dict(V=0), "ZI_ERR_SHAPE"),
+    (dict(T=-1), "ZI_ERR_SHAPE"), (dict(T=(1 << 27) + 1), "ZI_ERR_SHAPE"), (dict(V=0), "ZI_ERR_SHAPE"),
     (dict(V=1 << 31), "ZI_ERR_SHAPE"), (dict(D=0), "ZI_ERR_SHAPE"), (dict(D=65535 * 2048 + 1), "ZI_ERR_SHAPE"),
     (dict(ldw=8), "ZI_ERR_SHAPE"), (dict(ldx=-16), "ZI_ERR_SHAPE"), (dict(w_dtype=0), "ZI_ERR_ARG"),
     (dict(x_dtype=9), "ZI_ERR_ARG"), (dict(scale=float("nan")), "ZI_ERR_ARG"), (dict(scale=float("inf")), "ZI_ERR_ARG"),
