@@ -18,8 +18,8 @@
 // are then merged, the place of a key being its place in its own list plus the
 // number of keys before it in every other one (binary searches).  32768 tokens
 // take one merge.
-// What it takes.  Forward, 32768 tokens of 25600 fp16 values: 474 us, 2.18 GB at
-// 4.6 TB/s.  Gradient of 32768 tokens of 8192 bf16 values in 50257 fp32 rows:
+// What it takes.  Forward, 32768 tokens of 25600 fp16 values: 431 us, 2.18 GB at
+// 5.1 TB/s.  Gradient of 32768 tokens of 8192 bf16 values in 50257 fp32 rows:
 // 466 us, of which the sums and the zeros (2.15 GB) are 405, 5.3 TB/s, and the
 // sort 20.  Of 2047 tokens of 512 fp32 values, 107 MB of them zeros: 30 us; the
 // sort, the sums and the joins wait for latencies, the fill runs beside the sort.
@@ -52,29 +52,37 @@ __device__ __forceinline__ uint32_t key_of(int64_t id, int64_t V) { return (uint
 
 // L lanes a token, 256 / L tokens a workgroup; blockIdx.y: a span of columns.
 // All of a lane's loads are in flight before its first store; X passes the
-// caches, W, whose rows come again, does not.
-constexpr int kSpan = 2;  // vectors a lane takes of one token (4: 5 % slower for long rows, 1: 15 %)
-template <typename WT, typename XT, int L>
+// caches, W, whose rows come again, does not.  A row's last vector is moved back
+// to end with the row: the elements that it shares with the one before it are
+// written twice, with one value.  (Rows of less than eight columns: TINY.)
+constexpr int kSpan = 4;  // vectors a lane takes of one token (3: 1 % slower for long rows, 2: 4 %)
+template <typename WT, typename XT, int L, bool TINY>
 __global__ __launch_bounds__(256) void embed_fwd_kernel(const void *ids, int32_t wide, int64_t T, int64_t V, int64_t D,
-                                                        const WT *W, int64_t ldw, float scale, XT *X, int64_t ldx) {
+                                                        const WT *__restrict__ W, int64_t ldw, float scale,
+                                                        XT *__restrict__ X, int64_t ldx) {
     const int64_t base = ((int64_t)blockIdx.y * kSpan * L + threadIdx.x % L) * 8;
     for (int64_t t = (int64_t)blockIdx.x * (256 / L) + threadIdx.x / L; t < T; t += (int64_t)gridDim.x * (256 / L)) {
         const uint32_t v = key_of(wide ? static_cast<const int64_t *>(ids)[t] : static_cast<const int32_t *>(ids)[t], V);
-        const WT *w = W + (int64_t)v * ldw;
+        const bool in = v < V;
+        const WT *w = W + (int64_t)(in ? v : 0) * ldw;
         XT *x = X + t * ldx;
         float r[kSpan][8];
 #pragma unroll
         for (int c = 0; c < kSpan; ++c) {
             const int64_t i = base + c * L * 8;
-            load_n(w + i, v < V ? D - i : 0, r[c]);
+            if constexpr (TINY) load_n(w + i, D - i, r[c]);
+            else load8(w + min(i, D - 8), r[c]);
         }
 #pragma unroll
         for (int c = 0; c < kSpan; ++c) {
             const int64_t i = base + c * L * 8;
 #pragma unroll
-            for (int e = 0; e < 8; ++e) r[c][e] *= scale;
-            if (D - i >= 8) stream8(x + i, r[c]);
-            else store_n(x + i, D - i, r[c]);
+            for (int e = 0; e < 8; ++e) r[c][e] = in ? r[c][e] * scale : 0.f;
+            if constexpr (TINY) {
+                store_n(x + i, D - i, r[c]);
+            } else {
+                if (i < D) stream8(x + min(i, D - 8), r[c]);
+            }
         }
     }
 }
@@ -474,8 +482,13 @@ hipError_t run_fwd(const zi_embedding *p, const void *ids, const void *W, void *
     auto go = [&](auto lanes) {
         constexpr int L = decltype(lanes)::value;
         const dim3 g((unsigned)min64(ceil_div(p->T, 256 / L), kMostGroups), (unsigned)ceil_div(vecs, L * kSpan));
-        hipLaunchKernelGGL((embed_fwd_kernel<WT, XT, L>), g, dim3(256), 0, s, ids, wide, p->T, p->V, p->D,
-                           static_cast<const WT *>(W), ldw, p->scale, static_cast<XT *>(X), ldx);
+        if (p->D < 8)
+            hipLaunchKernelGGL((embed_fwd_kernel<WT, XT, 16, true>), dim3((unsigned)min64(ceil_div(p->T, 16), kMostGroups)),
+                               dim3(256), 0, s, ids, wide, p->T, p->V, p->D, static_cast<const WT *>(W), ldw, p->scale,
+                               static_cast<XT *>(X), ldx);
+        else
+            hipLaunchKernelGGL((embed_fwd_kernel<WT, XT, L, false>), g, dim3(256), 0, s, ids, wide, p->T, p->V, p->D,
+                               static_cast<const WT *>(W), ldw, p->scale, static_cast<XT *>(X), ldx);
         return hipGetLastError();
     };
     if (vecs <= 16) return go(std::integral_constant<int, 16>{});
