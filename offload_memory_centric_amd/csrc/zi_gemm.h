@@ -594,7 +594,7 @@ __device__ __forceinline__ void orth_store(const OrthArgs &a, int64_t p, int64_t
                 }
             } else {
                 if (q + e == p) {
-                    a.bdiag[p] = a.ca + a.cb * d + a.cc * (v[e] + d * d);
+                    a.bdiag[p] = a.cb * d + a.cc * (v[e] + d * d);
                     o[e] = 0.f;
                 } else {
                     o[e] = a.cb * in.l[e] + a.cc * (v[e] + (d + in.dq[e]) * in.l[e]);
@@ -615,9 +615,9 @@ __device__ __forceinline__ void orth_store(const OrthArgs &a, int64_t p, int64_t
         float y[4];
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-            const float x = value16<T>((in.hi[e >> 1] >> (16 * (e & 1))) & 0xffffu) +
-                            value16<T>((in.lo[e >> 1] >> (16 * (e & 1))) & 0xffffu);
-            y[e] = (d * x + v[e]) * r;
+            const float hi = value16<T>((in.hi[e >> 1] >> (16 * (e & 1))) & 0xffffu);
+            const float x = hi + value16<T>((in.lo[e >> 1] >> (16 * (e & 1))) & 0xffffu);
+            y[e] = (a.ca * x + (d * (a.diag_x ? x : hi) + v[e])) * r;
         }
         if (a.hi_out) {
             uint32_t h[4], l[4];

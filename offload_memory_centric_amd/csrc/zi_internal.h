@@ -58,10 +58,10 @@ hipError_t launch_gemm(GemmOp op, int dtype, const GemmArgs &a, hipStream_t stre
 // A step x <- a x + (b A + c A^2) x, A = x x^T, of the orthogonalised update
 // (zi_orth.hip).  Matrices are kept with their diagonals apart: A = D + O, with
 // D in fp32 and O (zero on the diagonal) in fp16 as an operand and in fp32 for
-// the linear term; likewise a + bA + cA^2 = diag(bd) + B.
+// the linear term; likewise bA + cA^2 = diag(bd) + B.
 //   Gram   acc = x x^T        D, O (C: fp16, o32: fp32 on and below the diagonal)
 //   Poly   acc = O O          bd, B (C: fp16)
-//   Apply  acc = B x          x (hi, lo: two fp16 planes), or `out` after the last step
+//   Apply  acc = B x          a x + bd x + acc (hi, lo: two fp16 planes), or `out` after the last step
 // The first two are symmetric: tiles on and below the diagonal are formed, and
 // those below it written on both sides.
 enum class OrthOp : int { Gram = 0, Poly = 1, Apply = 2 };
@@ -73,6 +73,7 @@ struct OrthArgs : GemmArgs {
     float *diag, *bdiag;  // D, bd
     const uint16_t *hi;   // Apply: the planes of x, [rows][ldc]
     uint16_t *lo;
+    int32_t diag_x;       // bd multiplies both planes; else hi alone, as B does
     uint16_t *hi_out;     // the new planes (lo is replaced in place); null: write `out`
     uint16_t *out;        // bf16
     int64_t out_p, out_q, out_ld;  // its extents along p and q, and its row stride

@@ -16,7 +16,13 @@
 // only the products' operands are rounded to 11 bits: there a rounding meets X
 // through b A + c A^2, which vanishes where X is small.  The diagonals of A and
 // of b A + c A^2, which hold most of their norm, and A's linear term stay in
-// fp32.  The planes of X_0 are G times a power of two (|G| then lies in
+// fp32.  That is so only while all of b A + c A^2 multiplies the same values: if
+// its diagonal alone multiplied X and the rest X's high plane, what that plane
+// lacks would be left over in every direction, also in those that X does not
+// have, and be enlarged there (a rank-one 9 x 16 came out 4 % off).  Where at most one
+// step follows, that weighs less than what the diagonal gains by both planes
+// (full rank, 1001 x 1531: 6e-4 for 9e-4), so it multiplies them in the last two.
+// The planes of X_0 are G times a power of two (|G| then lies in
 // [2^14, 2^15), so no element overflows and few are subnormal); the rest of the
 // normalisation is a factor of the first step, in fp32.
 //
@@ -234,6 +240,7 @@ hipError_t run(const zi_orth *o, const void *G, void *O, char *base, hipStream_t
         a.P = base + w.b16;
         a.ldp = w.mp;
         a.lo = lo;
+        a.diag_x = step + 2 >= o->steps;
         a.ldc = w.kp;
         a.cols = w.kp;
         a.red = w.mp;
