@@ -67,7 +67,7 @@ hipError_t launch_gemm(GemmOp op, int dtype, const GemmArgs &a, hipStream_t stre
 enum class OrthOp : int { Gram = 0, Poly = 1, Apply = 2 };
 struct OrthArgs : GemmArgs {
     int32_t pieces;       // workgroups that share the reduction of each of the last split_tail tiles
-    const float *scale;   // true x = *scale times the planes
+    const float *scale;   // Gram: x = *scale times its planes; Apply: the result is *scale times what they give
     float ca, cb, cc;     // a, b, c
     float *o32;           // [rows][ldc], as O
     float *diag, *bdiag;  // D, bd

@@ -21,10 +21,16 @@
 // lacks would be left over in every direction, also in those that X does not
 // have, and be enlarged there (a rank-one 9 x 16 came out 4 % off).  Where at most one
 // step follows, that weighs less than what the diagonal gains by both planes
-// (full rank, 1001 x 1531: 6e-4 for 9e-4), so it multiplies them in the last two.
-// The planes of X_0 are G times a power of two (|G| then lies in
-// [2^14, 2^15), so no element overflows and few are subnormal); the rest of the
-// normalisation is a factor of the first step, in fp32.
+// (full rank, 1001 x 1531, the same arithmetic on the CPU: 6e-4 for 9e-4), so it
+// multiplies them in the last two.
+// fp16 has no step below 2^-24, so the low plane holds what it should only of
+// values well above 2^-13, and X's are about 1 / sqrt(M K) or, where |G| is
+// below eps, far less.  The planes are therefore X times a power of two: G's
+// own for X_0, with |G| then in [2^14, 2^15), the rest of the normalisation
+// being a factor in fp32; later the one that takes the largest singular value
+// that X can have into [2^14, 2^15) (Bound), which no element passes.  The
+// epilogues undo it; a power of two rounds nothing.  (Unscaled, a rank-one
+// 2048 x 8192 came out 1.5 % off, and |G| = 1e-12 with eps = 1e-7 as zero.)
 //
 // What it takes.  32768 x 8192 in bf16: 28.0 ms, of which a step's A is 1.56 ms
 // (1450 TFLOP/s on the tiles formed, the matrix cores busy 0.84 of the time),
@@ -71,13 +77,50 @@ __global__ __launch_bounds__(256) void squares_kernel(const T *G, int64_t M, int
     if (threadIdx.x == 0) sums[blockIdx.x] = part[0] + part[1] + part[2] + part[3];
 }
 
+// The largest |p(s)|, p(s) = a s + b s^3 + c s^5, over 0 <= s <= u: at u or where
+// p' is zero.
+struct Bound {
+    double a, b, c;
+    double at[2], peak[2];  // the positive zeros of p' (infinite: none), and |p| there
+    __host__ __device__ double p(double s) const { return fabs(s * (a + s * s * (b + s * s * c))); }
+    __device__ double operator()(double u) const {
+        double most = p(u);
+        for (int k = 0; k < 2; ++k)
+            if (at[k] <= u) most = fmax(most, peak[k]);
+        return most;
+    }
+};
+
+constexpr int kMostSteps = 100;
+
+// The factors of every step: factor[2 j], by which the planes of X_j have to be
+// multiplied to give X_j, and factor[2 j + 1], by which a step's result in terms
+// of them, to give the planes of X_{j+1} (after the last step X itself).  The
+// power of two of X_{j+1}'s planes is at least one, so that a polynomial
+// whose bound grows without end loses nothing by it.
+__device__ __forceinline__ void write_factors(const Bound &bound, int steps, double norm, double eps, int e2, float *factor) {
+    double in = 1.0 / ldexp(norm + eps, e2), most = norm / (norm + eps);
+    for (int j = 0; j < steps; ++j) {
+        most = bound(most);
+        int e = 0;  // (NaN and infinities: 0)
+        if (most < 32768) {
+            (void)frexp(most, &e);
+            e = min(15 - e, 120);
+        }
+        if (j + 1 == steps) e = 0;
+        factor[2 * j] = (float)in;
+        factor[2 * j + 1] = (float)ldexp(in, e);
+        in = ldexp(1.0, -e);
+    }
+}
+
 // The planes of X_0, 64 x 64 elements a workgroup (TR: X is G transposed), and
-// zeros up to the padded extents; workgroup (0, 0) also writes the factor that
-// is left, 1 / ((|G| + eps) 2^e), and clears the counters of split tiles.
+// zeros up to the padded extents; workgroup (0, 0) also writes the steps'
+// factors and clears the counters of split tiles.
 template <typename T, bool TR>
 __global__ __launch_bounds__(256) void planes_kernel(const T *G, int64_t M, int64_t K, int64_t ldg, const double *sums,
-                                                     float eps, uint16_t *hi, uint16_t *lo, int64_t ld, float *scale,
-                                                     uint32_t *cnt) {
+                                                     float eps, uint16_t *hi, uint16_t *lo, int64_t ld, Bound bound,
+                                                     int32_t steps, float *factor, uint32_t *cnt) {
     __shared__ double part[4];
     __shared__ float tile[64][65];
     double s = 0;
@@ -105,10 +148,7 @@ __global__ __launch_bounds__(256) void planes_kernel(const T *G, int64_t M, int6
         e2 = 15 - e2;
     }
     if (blockIdx.x == 0 && blockIdx.y == 0) {
-        if (threadIdx.x == 0) {
-            scale[0] = (float)(1.0 / ldexp(norm + (double)eps, e2));
-            scale[1] = 1.f;  // the later steps'
-        }
+        if (threadIdx.x == 0) write_factors(bound, steps, norm, (double)eps, e2, factor);
         for (int j = threadIdx.x; j < kOrthSplits; j += 256) cnt[j] = 0;
     }
 #pragma unroll
@@ -137,7 +177,7 @@ __global__ __launch_bounds__(256) void planes_kernel(const T *G, int64_t M, int6
 // Sizes and the workspace of one orthogonalisation.
 struct Work {
     int64_t m, k, mp, kp;  // the shorter and the longer side, and padded to 64
-    uint64_t hi[2], lo, o16, b16, o32, diag, bdiag, sums, scale, cnt, part, bytes;
+    uint64_t hi[2], lo, o16, b16, o32, diag, bdiag, sums, factor, cnt, part, bytes;
 };
 
 // The side of the products' tiles: 256 where the triangle has at least one tile
@@ -174,11 +214,32 @@ Work work_of(int64_t M, int64_t K) {
     w.diag = take((uint64_t)w.mp * 4);
     w.bdiag = take((uint64_t)w.mp * 4);
     w.sums = take(kSums * 8);
-    w.scale = take(8);
+    w.factor = take(kMostSteps * 8);
     w.cnt = take(kOrthSplits * 4);
     w.part = take(orth_split_bytes(tile_of(w.mp, w.kp)));
     w.bytes = at;
     return w;
+}
+
+Bound bound_of(const zi_orth &o) {
+    Bound f{o.a, o.b, o.c, {INFINITY, INFINITY}, {}};
+    // p'(s) = a + 3 b t + 5 c t^2, t = s^2
+    double t[2] = {-1, -1};
+    if (f.c != 0) {
+        const double mid = -0.3 * f.b / f.c, both = 0.2 * f.a / f.c, wide = mid * mid - both;  // both: t0 t1
+        if (wide >= 0) {
+            t[0] = mid + copysign(sqrt(wide), mid);  // the larger one: no digits cancel
+            if (t[0] != 0) t[1] = both / t[0];
+        }
+    } else if (f.b != 0) {
+        t[0] = -f.a / (3 * f.b);
+    }
+    for (int k = 0; k < 2; ++k)
+        if (t[k] > 0) {
+            f.at[k] = sqrt(t[k]);
+            f.peak[k] = f.p(f.at[k]);
+        }
+    return f;
 }
 
 template <typename T>
@@ -188,7 +249,7 @@ hipError_t run(const zi_orth *o, const void *G, void *O, char *base, hipStream_t
     const bool tr = o->M > o->K;
     const int tile = tile_of(w.mp, w.kp);
     double *sums = reinterpret_cast<double *>(base + w.sums);
-    float *scale = reinterpret_cast<float *>(base + w.scale);
+    float *factor = reinterpret_cast<float *>(base + w.factor);
     uint16_t *hi[2] = {reinterpret_cast<uint16_t *>(base + w.hi[0]), reinterpret_cast<uint16_t *>(base + w.hi[1])};
     uint16_t *lo = reinterpret_cast<uint16_t *>(base + w.lo);
     uint32_t *cnt = reinterpret_cast<uint32_t *>(base + w.cnt);
@@ -198,10 +259,10 @@ hipError_t run(const zi_orth *o, const void *G, void *O, char *base, hipStream_t
     const dim3 g((unsigned)(w.kp / 64), (unsigned)(w.mp / 64));
     if (tr)
         hipLaunchKernelGGL((planes_kernel<T, true>), g, dim3(256), 0, s, static_cast<const T *>(G), o->M, o->K, ldg, sums,
-                           o->eps, hi[0], lo, w.kp, scale, cnt);
+                           o->eps, hi[0], lo, w.kp, bound_of(*o), o->steps, factor, cnt);
     else
         hipLaunchKernelGGL((planes_kernel<T, false>), g, dim3(256), 0, s, static_cast<const T *>(G), o->M, o->K, ldg, sums,
-                           o->eps, hi[0], lo, w.kp, scale, cnt);
+                           o->eps, hi[0], lo, w.kp, bound_of(*o), o->steps, factor, cnt);
     if ((e = hipGetLastError()) != hipSuccess) return e;
     OrthArgs c{};
     c.ca = o->a;
@@ -213,11 +274,10 @@ hipError_t run(const zi_orth *o, const void *G, void *O, char *base, hipStream_t
     c.split_part = reinterpret_cast<float *>(base + w.part);
     c.split_cnt = cnt;
     c.rows = w.mp;
-    c.scale = scale + 1;  // one
     for (int step = 0; step < o->steps; ++step) {
         uint16_t *x = hi[step & 1];
         OrthArgs a = c;  // A = X X^T
-        if (step == 0) a.scale = scale;
+        a.scale = factor + 2 * step;
         a.Q = a.P = x;
         a.ldq = a.ldp = w.kp;
         a.C = base + w.o16;
@@ -234,7 +294,7 @@ hipError_t run(const zi_orth *o, const void *G, void *O, char *base, hipStream_t
         a.red = w.mp;
         if ((e = launch_orth(OrthOp::Poly, tile, a, s)) != hipSuccess) return e;
         a = c;  // a X + (b A + c A^2) X
-        if (step == 0) a.scale = scale;
+        a.scale = factor + 2 * step + 1;
         a.Q = a.hi = x;
         a.ldq = w.kp;
         a.P = base + w.b16;
@@ -277,7 +337,7 @@ extern "C" zi_status zi_orthogonalize(const zi_orth *o, const void *G, void *O, 
         return fail(ZI_ERR_SHAPE, "a row stride is less than K");
     if (o->dtype != ZI_F16 && o->dtype != ZI_BF16 && o->dtype != ZI_F32)
         return fail(ZI_ERR_ARG, "unknown dtype %d", o->dtype);
-    if (o->steps < 1 || o->steps > 100) return fail(ZI_ERR_ARG, "steps = %d: 1 .. 100", o->steps);
+    if (o->steps < 1 || o->steps > kMostSteps) return fail(ZI_ERR_ARG, "steps = %d: 1 .. %d", o->steps, kMostSteps);
     if (!isfinite(o->a) || !isfinite(o->b) || !isfinite(o->c) || !(o->eps >= 0.f) || !isfinite(o->eps))
         return fail(ZI_ERR_ARG, "a, b, c and eps must be finite, and eps not negative");
     if (!G || !O) return fail(ZI_ERR_ARG, "G and O are required");

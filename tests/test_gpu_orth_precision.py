@@ -3,7 +3,10 @@ wholly empty, or is far smaller than eps.
 
 Tolerance, relative to the result's norm.  The bf16 result is off by its rounding, at most half a step (2^-8) of
 each element, and by the error before it; what |O - exact| leaves above 2^-8 |exact|, element by element, is at most
-1 + 2^-8 times the second.  A step rounds three fp16 operands, by 2^-11 of an element at most."""
+1 + 2^-8 times the second.  A step rounds three fp16 operands, by 2^-11 of an element at most and 0.42 * 2^-11 in the
+root mean square.  Over hundreds of rows these roundings are independent and no step's polynomial enlarges what
+they leave in G's own directions by more than it shrinks it in the next, so fifteen of them add up like
+sqrt(15) * 0.42 * 2^-11, 0.8 * 2^-10: 2^-10 is taken."""
 import pytest
 import torch
 
@@ -13,6 +16,7 @@ pytestmark = pytest.mark.gpu
 
 DT = {"f16": torch.float16, "bf16": torch.bfloat16, "f32": torch.float32}
 COEFFS = (3.4445, -4.7750, 2.0315)
+MANY = 2.0 ** -10
 
 
 def gen(seed):
@@ -54,6 +58,47 @@ def low_rank(g, M, K, rank, noise=0.0, dtype="f32"):
     if noise:
         G.add_(torch.randn((M, K), generator=g, device="cuda"), alpha=noise)
     return G.to(DT[dtype])
+
+
+@pytest.mark.parametrize("M,K", [(1024, 4096), (2048, 4096), (4096, 2048), (2048, 8192), (4096, 4096), (5700, 6100)])
+@pytest.mark.parametrize("rank,noise,dtype", [(1, 0.0, "f32"), (1, 0.0, "bf16"), (16, 0.0, "f32"), (16, 0.01, "bf16"),
+                                              (4, 1e-4, "f16")])
+def test_low_rank(M, K, rank, noise, dtype):
+    """A gradient from fewer tokens than the weight has rows: what the planes of X lose in its empty directions,
+    the steps would enlarge nearly 500 times."""
+    from offload_memory_centric_amd import layers
+    G = low_rank(gen(M + rank), M, K, rank, noise, dtype)
+    e = error(orth(layers, G), polynomial(G))
+    say("orthogonalise", M, K, "rank", rank, "noise", noise, dtype, "error %.2g" % e)
+    assert e <= MANY, e
+
+
+@pytest.mark.parametrize("M,K", [(300, 1000), (1024, 4096), (2000, 700)])
+@pytest.mark.parametrize("norm", [1e-6, 1e-8, 1e-10, 1e-12, 1e-20, 1e-30])
+def test_far_below_eps(M, K, norm):
+    """X_0 is then far smaller than one, and stays so: every step takes it up by a."""
+    from offload_memory_centric_amd import layers
+    g = gen(K)
+    for rank in (1, min(M, K)):
+        G = low_rank(g, M, K, rank)
+        G.mul_(norm / float(G.double().norm()))
+        e = error(orth(layers, G), polynomial(G))
+        say("orthogonalise", M, K, "rank", rank, "norm", norm, "error %.2g" % e)
+        assert e <= MANY, e
+
+
+@pytest.mark.parametrize("coeffs,steps", [((1.5, -0.5, 0.0), 9), ((1.875, -1.25, 0.375), 7), ((3.0, -3.0, 1e-30), 3),
+                                          ((1.0, 0.0, 0.0), 4), ((2.0, 0.0, -1.0), 3), ((5.0, 0.0, 0.0), 4),
+                                          ((0.25, 0.0, 0.0), 40)])
+def test_other_polynomials(coeffs, steps):
+    """The largest singular value that X can have, by which its planes are scaled, is the polynomial's: cubic,
+    quintic, with two, one or no peak, growing or shrinking without end."""
+    from offload_memory_centric_amd import layers
+    M, K = 400, 900
+    G = low_rank(gen(steps), M, K, M)
+    e = error(orth(layers, G, steps=steps, coeffs=coeffs), polynomial(G, steps, coeffs))
+    say("orthogonalise", coeffs, steps, "error %.2g" % e)
+    assert e <= MANY, e
 
 
 # Few elements: fifteen roundings need not average out.  2^-11 each; from one step to the next the polynomial's slope
