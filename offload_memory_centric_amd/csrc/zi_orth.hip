@@ -99,7 +99,8 @@ constexpr int kMostSteps = 100;
 // power of two of X_{j+1}'s planes is at least one, so that a polynomial
 // whose bound grows without end loses nothing by it.
 __device__ __forceinline__ void write_factors(const Bound &bound, int steps, double norm, double eps, int e2, float *factor) {
-    double in = 1.0 / ldexp(norm + eps, e2), most = norm / (norm + eps);
+    // (norm 0: all planes are zero, and times zero they stay so, also without eps)
+    double in = norm == 0 ? 0 : 1.0 / ldexp(norm + eps, e2), most = norm == 0 ? 0 : norm / (norm + eps);
     for (int j = 0; j < steps; ++j) {
         most = bound(most);
         int e = 0;  // (NaN and infinities: 0)

@@ -1,5 +1,5 @@
 """The precision of the orthogonalised update (zi_orthogonalize), where its input has directions that are nearly or
-wholly empty, or is far smaller than eps.
+wholly empty, or is far smaller than eps, or zero.
 
 Tolerance, relative to the result's norm.  The bf16 result is off by its rounding, at most half a step (2^-8) of
 each element, and by the error before it; what |O - exact| leaves above 2^-8 |exact|, element by element, is at most
@@ -116,3 +116,12 @@ def test_low_rank_small(M, K, rank):
         worst = max(worst, error(orth(layers, G), polynomial(G)))
     say("orthogonalise", M, K, "rank", rank, "error %.2g" % worst)
     assert worst <= FEW, worst
+
+
+@pytest.mark.parametrize("M,K", [(70, 90), (90, 70), (1, 1)])
+@pytest.mark.parametrize("eps", [0.0, 1e-42, 1e-39])
+def test_zero_with_next_to_no_eps(M, K, eps):
+    """A zero gradient has no direction: its update is zero, whatever eps."""
+    from offload_memory_centric_amd import layers
+    Z = torch.zeros((M, K), device="cuda")
+    assert not orth(layers, Z, eps=eps).any()
