@@ -60,8 +60,10 @@ __device__ __forceinline__ float row_sum(float x, float *slots) {
     return s;
 }
 
+// Rows of a workgroup at a time.  Where fewer are left, the threads without one
+// stop: they must not read another's, which may be overwritten in place.
 template <int NT>
-constexpr int kRows = NT < 256 ? 256 / NT : 1;  // rows of a workgroup at a time
+constexpr int kRows = NT < 256 ? 256 / NT : 1;
 template <int NT>
 constexpr int kBlock = NT < 256 ? 256 : NT;
 
@@ -90,8 +92,8 @@ __global__ __launch_bounds__(kBlock<NT>) void norm_fwd_kernel(NormArgs a) {
     const int sub = kRows<NT> == 1 ? 0 : threadIdx.x / NT;
     const Share<NT, FULL> my{kRows<NT> == 1 ? (int)threadIdx.x : (int)threadIdx.x % NT, (int)a.D};
     for (int64_t first = (int64_t)blockIdx.x * kRows<NT>; first < a.T; first += (int64_t)gridDim.x * kRows<NT>) {
-        const bool live = first + sub < a.T;
-        const int64_t row = live ? first + sub : a.T - 1;
+        if (kRows<NT> > 1 && first + sub >= a.T) break;  // (row_sum: these threads share no other row's sum)
+        const int64_t row = first + sub;
         const XT *x = static_cast<const XT *>(a.X) + row * a.ldx;
         const YT *r = static_cast<const YT *>(a.R) + row * a.ldr;
         XT *sp = static_cast<XT *>(a.S) + row * a.lds;
@@ -115,7 +117,7 @@ __global__ __launch_bounds__(kBlock<NT>) void norm_fwd_kernel(NormArgs a) {
             }
         const float mean = row_sum<NT>(sum, slots[0]) / a.width;
         if constexpr (RES) {  // the row has been read: S may replace X or R
-            if (a.S && live) {
+            if (a.S) {
 #pragma unroll
                 for (int c = 0; c < V; ++c) stream8(sp + my.at(c), s[c]);
             }
@@ -129,7 +131,7 @@ __global__ __launch_bounds__(kBlock<NT>) void norm_fwd_kernel(NormArgs a) {
                 sq += my.own(c, e) ? s[c][e] * s[c][e] : 0.f;
             }
         const float rstd = 1.0f / sqrtf(row_sum<NT>(sq, slots[1]) / a.width + a.eps);
-        if (my.t == 0 && live) {
+        if (my.t == 0) {
             if (a.mean) a.mean[row] = mean;
             if (a.rstd) a.rstd[row] = rstd;
         }
@@ -148,7 +150,7 @@ __global__ __launch_bounds__(kBlock<NT>) void norm_fwd_kernel(NormArgs a) {
 #pragma unroll
                 for (int e = 0; e < 8; ++e) s[c][e] += g[e];
             }
-            if (live) stream8(y + my.at(c), s[c]);
+            stream8(y + my.at(c), s[c]);
         }
     }
 }
@@ -247,8 +249,8 @@ __global__ __launch_bounds__(kBlock<NT>) void norm_bwd_kernel(NormArgs a) {
 #pragma unroll
         for (int e = 0; e < 8; ++e) ag[c][e] = ab[c][e] = 0.f;
     for (int64_t first = (int64_t)blockIdx.x * kRows<NT>; first < a.T; first += (int64_t)gridDim.x * kRows<NT>) {
-        const bool live = first + sub < a.T;
-        const int64_t row = live ? first + sub : a.T - 1;
+        if (kRows<NT> > 1 && first + sub >= a.T) break;  // (row_sum: these threads share no other row's sum)
+        const int64_t row = first + sub;
         const XT *x = static_cast<const XT *>(a.S) + row * a.lds;
         const YT *dy = static_cast<const YT *>(a.Y) + row * a.ldy;
         const XT *ds = static_cast<const XT *>(a.dS) + row * a.ldr;
@@ -272,7 +274,7 @@ __global__ __launch_bounds__(kBlock<NT>) void norm_bwd_kernel(NormArgs a) {
             load8(gam + my.at(c), g);
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
-                const float h = (xr[c][e] - mean) * rstd, d = kRows<NT> == 1 || live ? dr[c][e] : 0.f, w = d * g[e];
+                const float h = (xr[c][e] - mean) * rstd, d = dr[c][e], w = d * g[e];
                 ag[c][e] += d * h;
                 ab[c][e] += d;
                 sg += my.own(c, e) ? w : 0.f;
@@ -310,7 +312,7 @@ __global__ __launch_bounds__(kBlock<NT>) void norm_bwd_kernel(NormArgs a) {
                 o[e] = (dr[c][e] * g[e] - mg - h * mgh) * rstd;
                 if (a.dS) o[e] += ur[c][e];
             }
-            if (live) stream8(dx + my.at(c), o);
+            stream8(dx + my.at(c), o);
         }
     }
     if (!a.part) return;
