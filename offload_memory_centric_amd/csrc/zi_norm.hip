@@ -414,32 +414,36 @@ __global__ __launch_bounds__(256) void norm_cols_kernel(NormArgs a) {
 }
 
 // dgamma and dbeta from the partial sums, in a fixed order: 64 columns and 16
-// shares of the partial sums a workgroup.
+// shares of the partial sums a workgroup at a time.
 __global__ __launch_bounds__(1024) void norm_fold_kernel(const float *part, int64_t D, int32_t parts, float *dgamma,
                                                          float *dbeta) {
     __shared__ float sum[16][64];
     const int lane = threadIdx.x & 63, share = threadIdx.x >> 6;
-    const int64_t col = (int64_t)blockIdx.x * 64 + lane;  // of [dgamma, dbeta]
-    float s = 0.f;
-    if (col < 2 * D) {
-        constexpr int U = 8;  // loads in flight
-        for (int p = share; p < parts; p += 16 * U) {
-            float v[U];
+    for (int64_t first = (int64_t)blockIdx.x * 64; first < 2 * D; first += (int64_t)gridDim.x * 64) {
+        const int64_t col = first + lane;  // of [dgamma, dbeta]
+        float s = 0.f;
+        if (col < 2 * D) {
+            constexpr int U = 8;  // loads in flight
+            for (int p = share; p < parts; p += 16 * U) {
+                float v[U];
 #pragma unroll
-            for (int u = 0; u < U; ++u) v[u] = part[min(p + 16 * u, parts - 1) * 2 * D + col];
+                for (int u = 0; u < U; ++u) v[u] = part[min(p + 16 * u, parts - 1) * 2 * D + col];
 #pragma unroll
-            for (int u = 0; u < U; ++u) s += p + 16 * u < parts ? v[u] : 0.f;
+                for (int u = 0; u < U; ++u) s += p + 16 * u < parts ? v[u] : 0.f;
+            }
         }
-    }
-    sum[share][lane] = s;
-    __syncthreads();
-    if (share || col >= 2 * D) return;
+        sum[share][lane] = s;
+        __syncthreads();
+        if (share == 0 && col < 2 * D) {
 #pragma unroll
-    for (int k = 1; k < 16; ++k) s += sum[k][lane];
-    if (col < D) {
-        if (dgamma) dgamma[col] = s;
-    } else {
-        if (dbeta) dbeta[col - D] = s;
+            for (int k = 1; k < 16; ++k) s += sum[k][lane];
+            if (col < D) {
+                if (dgamma) dgamma[col] = s;
+            } else {
+                if (dbeta) dbeta[col - D] = s;
+            }
+        }
+        __syncthreads();
     }
 }
 
@@ -523,7 +527,7 @@ hipError_t run_bwd(const NormArgs &a, float *dgamma, float *dbeta, hipStream_t s
         if (e != hipSuccess) return e;
     }
     if (!dgamma && !dbeta) return hipSuccess;
-    hipLaunchKernelGGL(norm_fold_kernel, dim3((unsigned)((2 * a.D + 63) / 64)), dim3(1024), 0, s, a.part, a.D, parts,
+    hipLaunchKernelGGL(norm_fold_kernel, dim3((unsigned)min64((2 * a.D + 63) / 64, kMostGroups)), dim3(1024), 0, s, a.part, a.D, parts,
                        dgamma, dbeta);
     return hipGetLastError();
 }
