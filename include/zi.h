@@ -737,7 +737,8 @@ zi_status zi_embedding_fwd(const zi_embedding *emb, const void *ids, const void 
 /* dW[v] (+)= scale * sum of dX[t] over the tokens with id_t = v, for every row
  * v: summed in fp32 in an order that depends on the ids alone, rounded once.
  * Without `accumulate`, rows without a token are written as zero; with it,
- * they are not touched. */
+ * they are not touched.  The workspace for T tokens of D columns also serves
+ * fewer of either; its size does not depend on V. */
 uint64_t zi_embedding_bwd_bytes(int64_t T, int64_t V, int64_t D);
 zi_status zi_embedding_bwd(const zi_embedding *emb, const void *ids, const void *dX, void *dW, void *workspace,
                            uint64_t workspace_bytes, void *stream);

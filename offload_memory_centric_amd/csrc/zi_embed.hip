@@ -449,7 +449,10 @@ __global__ __launch_bounds__(256) void join_kernel(const uint32_t *__restrict__ 
 
 // Short lists, and short rows, take short chunks: more workgroups, each with
 // fewer rows to add one after another.
-int32_t chunk_of(int64_t T, int64_t D) { return T <= 8192 ? 16 : D <= 512 ? 32 : kChunk; }
+constexpr int64_t kShortList = 8192, kShortRow = 512;
+int32_t chunk_of(int64_t T, int64_t D) { return T <= kShortList ? 16 : D <= kShortRow ? 32 : kChunk; }
+// Elements of the chunks' pieces.
+int64_t pieces_of(int64_t T, int64_t D) { return ceil_div(T, chunk_of(T, D)) * 2 * D; }
 int64_t up4(int64_t x) { return (x + 3) / 4 * 4; }
 // Threads of a workgroup that sums rows of D elements, and workgroups a row.
 int64_t threads_of(int64_t D) { return D > 1024 ? 256 : D > 512 ? 128 : 64; }
@@ -470,7 +473,11 @@ Work work_of(int64_t T, int64_t D) {
         at += up256((uint64_t)T * 4);
     }
     w.pieces = at;
-    at += up256((uint64_t)ceil_div(T, chunk_of(T, D)) * 2 * (uint64_t)D * 4);
+    // Where the chunks get longer, so where their pieces get fewer, the room
+    // stays: a workspace for T tokens of D columns holds any fewer of both.
+    const int64_t t = min64(T, kShortList), d = min64(D, kShortRow);
+    const uint64_t most = max64(pieces_of(T, D), max64(pieces_of(t, D), pieces_of(T, d)));
+    at += up256(most * 4);
     w.bytes = at;
     return w;
 }
