@@ -711,7 +711,8 @@ zi_status zi_layer_norm_fwd(const zi_norm *norm, const void *X, const void *R, c
  * stream, may be NULL (zero); so may gamma (ones), dgamma and dbeta (not
  * formed: then no workspace is needed).  dX may be dS, S or dY itself, where
  * stride and type agree.  With T = 0, dgamma and dbeta are zero.  y_dtype is
- * dY's type: ZI_F32 for the dX of zi_tiled_linear_bwd. */
+ * dY's type: ZI_F32 for the dX of zi_tiled_linear_bwd.  The workspace for T
+ * rows of D columns also serves fewer of either. */
 uint64_t zi_layer_norm_bwd_bytes(int64_t T, int64_t D);
 zi_status zi_layer_norm_bwd(const zi_norm *norm, const void *dY, const void *S, const void *gamma, const float *mean,
                             const float *rstd, const void *dS, void *dX, float *dgamma, float *dbeta,

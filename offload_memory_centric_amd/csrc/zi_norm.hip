@@ -609,7 +609,14 @@ extern "C" zi_status zi_layer_norm_fwd(const zi_norm *n, const void *X, const vo
 
 extern "C" uint64_t zi_layer_norm_bwd_bytes(int64_t T, int64_t D) {
     if (T < 0 || D < 1) return 0;
-    return (uint64_t)min64(T, parts_of(D)) * 2 * (uint64_t)D * 4;
+    // where wider rows take fewer parts, the room stays: a workspace for T rows of
+    // D columns holds any fewer of both
+    uint64_t most = 0;
+    for (int64_t d : {min64(D, 4096), min64(D, 8192), D}) {
+        const uint64_t sums = (uint64_t)min64(T, parts_of(d)) * 2 * (uint64_t)d;
+        if (sums > most) most = sums;
+    }
+    return most * 4;
 }
 
 extern "C" zi_status zi_layer_norm_bwd(const zi_norm *n, const void *dY, const void *S, const void *gamma,

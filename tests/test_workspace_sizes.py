@@ -1,4 +1,4 @@
-"""The workspace of the embedding's gradient: what holds the largest batch and the widest
+"""The workspaces of the norm's backward and of the embedding's gradient: what holds the largest batch and the widest
 rows holds every smaller one's."""
 import pytest
 
@@ -27,3 +27,13 @@ def test_embedding_in_tokens(zi, D):
 @pytest.mark.parametrize("T", TS)
 def test_embedding_in_columns(zi, T):
     assert not falls(lambda D: zi.zi_embedding_bwd_bytes(T, 1000, D), DS)
+
+
+@pytest.mark.parametrize("D", DS)
+def test_norm_in_rows(zi, D):
+    assert not falls(lambda T: zi.zi_layer_norm_bwd_bytes(T, D), TS)
+
+
+@pytest.mark.parametrize("T", TS)
+def test_norm_in_columns(zi, T):
+    assert not falls(lambda D: zi.zi_layer_norm_bwd_bytes(T, D), DS)
