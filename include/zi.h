@@ -752,8 +752,8 @@ zi_status zi_embedding_bwd(const zi_embedding *emb, const void *ids, const void 
  * bf16.  The products take operands rounded to fp16, whatever G's type, and fp32
  * sums; what X carries over from step to step is held in 22 bits, relative to its
  * largest singular value.  Before its rounding to bf16 (half a step, 2^-8, of an
- * element), O is off by 1e-4 to 1e-3 of |O| for G of any rank with more than some
- * tens of rows and columns, by up to 6e-3 for fewer, and by up to 1.3e-2 where no
+ * element), O is off by about 1e-3 of |O| or less for G of any rank with more than
+ * some tens of rows and columns, by up to 6e-3 for fewer, and by up to 1.3e-2 where no
  * rounding differs from another (G of rank one, its elements all of one magnitude).
  * Singular values that the polynomial takes past 2^7 overflow.  With NaN or an
  * infinity in G, O is NaN; with G zero, O is zero.  O overlaps neither G nor

@@ -23,6 +23,8 @@
 // 466 us, of which the sums and the zeros (2.15 GB) are 405, 5.3 TB/s, and the
 // sort 20.  Of 2047 tokens of 512 fp32 values, 107 MB of them zeros: 30 us; the
 // sort, the sums and the joins wait for latencies, the fill runs beside the sort.
+// Of 262144 tokens of 1024 bf16 values 282 us: the sort 114, of which the second
+// merge, whose searches are in memory, 30; of 65536 tokens 108: 31 and 6.
 #include <hip/hip_runtime.h>
 #include <math.h>
 #include <stdint.h>

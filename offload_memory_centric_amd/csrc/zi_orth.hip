@@ -30,9 +30,10 @@
 // being a factor in fp32; later the one that takes the largest singular value
 // that X can have into [2^14, 2^15) (Bound), which no element passes.  The
 // epilogues undo it; a power of two rounds nothing.  (Unscaled, a rank-one
-// 2048 x 8192 came out 1.5 % off, and |G| = 1e-12 with eps = 1e-7 as zero.)
+// 2048 x 8192 came out 1.3 % off past bf16's rounding, and |G| = 1e-12 with
+// eps = 1e-7 65 %; so 3e-6 and 4e-12.)
 //
-// What it takes.  32768 x 8192 in bf16: 28.0 ms, of which a step's A is 1.56 ms
+// What it takes.  32768 x 8192 in bf16: 28 to 29 ms, of which a step's A is 1.56 ms
 // (1450 TFLOP/s on the tiles formed, the matrix cores busy 0.84 of the time),
 // b A + c A^2 0.49 ms, and the product with X 3.56 ms (1235 TFLOP/s, busy 0.66:
 // each tile's planes are read and written after its last multiplication).  Small
