@@ -22,7 +22,8 @@
 // have, and be enlarged there (a rank-one 9 x 16 came out 4 % off).  Where at most one
 // step follows, that weighs less than what the diagonal gains by both planes
 // (full rank, 1001 x 1531, the same arithmetic on the CPU: 6e-4 for 9e-4), so it
-// multiplies them in the last two.
+// multiplies them in the last two, and always where X is a single row, whose
+// polynomial is a number.
 // fp16 has no step below 2^-24, so the low plane holds what it should only of
 // values well above 2^-13, and X's are about 1 / sqrt(M K) or, where |G| is
 // below eps, far less.  The planes are therefore X times a power of two: G's
@@ -302,7 +303,7 @@ hipError_t run(const zi_orth *o, const void *G, void *O, char *base, hipStream_t
         a.P = base + w.b16;
         a.ldp = w.mp;
         a.lo = lo;
-        a.diag_x = step + 2 >= o->steps;
+        a.diag_x = w.m == 1 || step + 2 >= o->steps;
         a.ldc = w.kp;
         a.cols = w.kp;
         a.red = w.mp;

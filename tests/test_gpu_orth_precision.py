@@ -125,3 +125,19 @@ def test_zero_with_next_to_no_eps(M, K, eps):
     from offload_memory_centric_amd import layers
     Z = torch.zeros((M, K), device="cuda")
     assert not orth(layers, Z, eps=eps).any()
+
+
+@pytest.mark.parametrize("K", [2000, 20000])
+@pytest.mark.parametrize("flip", [False, True])
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_one_row(K, flip, dtype):
+    """A single row is multiplied by numbers alone: no element's rounding stays with it, and in the number, a sum over
+    the row, they average out.  Fifteen of 0.42 * 2^-11, each over 2000 elements of either weight at least, come to less
+    than 2^-12: of elements a step of 2^-8 or more apart, at most one in sixteen falls to the other side."""
+    from offload_memory_centric_amd import layers
+    for seed in range(3):
+        G = torch.randn((1, K), generator=gen(seed), device="cuda").to(DT[dtype])
+        G = G.t().contiguous() if flip else G
+        off = float((orth(layers, G) != polynomial(G).to(torch.bfloat16)).float().mean())
+        say("orthogonalise one row", K, flip, dtype, "not the nearest: %.2g" % off)
+        assert off <= 1 / 16, off
