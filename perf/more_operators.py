@@ -188,7 +188,7 @@ def prepare(case, seed):
             from offload_memory_centric_amd import layers
 
             size = layers.adapters_fwd_bytes if op == "adapters_fwd" else layers.adapters_bwd_bytes
-            s["work"] = layers.workspace(size(T, K, M, N, r, S))
+            s["work"] = layers.workspace(size(T, r))
     else:
         R, E, K, M, x, y = (case[n] for n in ("R", "E", "K", "M", "x", "y"))
         s["offsets"] = _split(g, R, E)
