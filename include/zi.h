@@ -771,6 +771,129 @@ uint64_t zi_orthogonalize_bytes(int64_t M, int64_t K);
 zi_status zi_orthogonalize(const zi_orth *orth, const void *G, void *O, void *workspace, uint64_t workspace_bytes,
                            void *stream);
 
+/* A router over E experts for T tokens, each of which takes k of them. */
+#define ZI_ROUTE_EXPERTS 1024
+typedef struct {
+    int64_t T;           /* tokens: T k at most 2^30                                     */
+    int64_t ldl, ldd;    /* row strides of logits and dlogits; 0 = E                     */
+    int32_t E;           /* experts: 1 .. ZI_ROUTE_EXPERTS                               */
+    int32_t k;           /* choices: 1 .. 32, at most E                                  */
+    int32_t dtype;       /* logits, dlogits                                              */
+    int32_t normalize;   /* the weights of a token's choices sum to one (else they are
+                            probabilities over all experts)                              */
+} zi_route;
+
+/* Forward: for every token t its choices ids[t][0 .. k-1], the experts of the k
+ * largest logits in descending order (of equal ones the lowest index), and their
+ * weights[t][j], the softmax of the logits over the chosen (normalize) or over all
+ * experts.  A logit of -inf or NaN is never chosen: a token with fewer than k others
+ * has -1 and weight 0 in the places left (all of them for a masked token).  A NaN, or
+ * an infinity that is chosen, makes the token's weights NaN.
+ * The choices (t, j) are sorted by expert, each expert's by token: expert e has
+ * places [offsets[e], offsets[e + 1]) (offsets: E + 1), rows[s] is the token at place s
+ * (T k of them, -1 from offsets[E] on), and slots[t][j] the place of choice (t, j), -1
+ * without one.  rows are the ids for zi_embedding_fwd, which gathers the tokens' rows
+ * for the grouped products; slots are what zi_combine_fwd takes. */
+uint64_t zi_route_fwd_bytes(int64_t T, int32_t E, int32_t k);
+zi_status zi_route_fwd(const zi_route *route, const void *logits, int32_t *ids, float *weights, int32_t *offsets,
+                       int32_t *rows, int32_t *slots, void *workspace, uint64_t workspace_bytes, void *stream);
+
+/* Backward: with g the dweights (fp32, [T][k]) at the chosen experts and zero
+ * elsewhere, dlogits = p (g - sum p g), p the softmax over all experts, from the
+ * logits (weights may be NULL); with normalize, p the weights (logits may be NULL).
+ * dweights of choices that are -1 count as zero. */
+zi_status zi_route_bwd(const zi_route *route, const void *logits, const int32_t *ids, const float *weights,
+                       const float *dweights, void *dlogits, void *stream);
+
+/* Products of E weights, each with a share of the rows (the experts of a mixture).
+ * Group e has the rows [offsets[e], offsets[e + 1]) of X and Y (offsets: E + 1 int32
+ * in device memory, ascending; what lies outside [0, R] is left out) and the weight
+ * W_e [M x K], out-major as the tiled linear's.  Rows in no group are neither read nor
+ * written.  K, M and the strides are multiples of 8, matrices 16-byte aligned.  Sums
+ * are held in fp32 and rounded once. */
+#define ZI_GROUPS_MOST 4096
+typedef struct {
+    int64_t R;            /* rows: 0 .. 2^30                                             */
+    int64_t K, M;         /* columns of X and of Y: 8 .. 2^20                            */
+    int64_t ldx, ldy;     /* row strides: of X and dX, of Y and dY; 0 = K, M             */
+    int64_t lda;          /* of A; 0 = its columns (M in the forward, K in dX)           */
+    int64_t ldw, ldg;     /* of W's and dW's rows, and from one group's to the next;
+                             0 = K, M ldw                                                */
+    int32_t E;            /* groups: 1 .. ZI_GROUPS_MOST                                 */
+    int32_t dtype;        /* X, W, dY, A: ZI_F16 or ZI_BF16                              */
+    int32_t out_dtype;    /* Y, dX, dW: dtype or ZI_F32                                  */
+    int32_t gelu;         /* forward: Y = GeLU(X W^t)                                    */
+    int32_t accumulate;   /* dW: add to it (fp32 only; else overwrite it all)            */
+} zi_grouped;
+
+/* Y = RNE(X W_e^T); with gelu, Y = RNE(GeLU(X W_e^T)) (exact erf form, from the
+ * unrounded sum) and A, unless NULL, RNE(X W_e^T) for the backward. */
+zi_status zi_grouped_fwd(const zi_grouped *grouped, const void *X, const void *W, const int32_t *offsets, void *Y,
+                         void *A, void *stream);
+/* dX = RNE(dY W_e); with A [R x K], the input of the GeLU that made X, dX = RNE((dY W_e) GeLU'(A)). */
+zi_status zi_grouped_dx(const zi_grouped *grouped, const void *dY, const void *W, const int32_t *offsets, const void *A,
+                        void *dX, void *stream);
+/* dW_e (+)= dY_e^T X_e; without `accumulate`, a group without rows has a zero gradient. */
+zi_status zi_grouped_dw(const zi_grouped *grouped, const void *X, const void *dY, const int32_t *offsets, void *dW,
+                        void *stream);
+
+/* The sum of k rows of Z [R x D] for each of T tokens.  A slot outside [0, R) stands
+ * for no row: its weight is not read, and its dweight is zero. */
+typedef struct {
+    int64_t T;                /* tokens: T k at most 2^30                                */
+    int64_t R;                /* rows of Z: 0 .. 2^31 - 1                                */
+    int64_t D;                /* columns: 1 .. 2^31 - 1                                  */
+    int64_t ldz, ldy, lddz;   /* row strides: of Z, of Y and dY, of dZ; 0 = D            */
+    int32_t k;                /* 1 .. 1024                                               */
+    int32_t dtype;            /* Z, Y, dY, dZ                                            */
+} zi_combine;
+
+/* Y[t] = RNE(sum_j weights[t][j] Z[slots[t][j]]), summed in fp32 in the order of j. */
+zi_status zi_combine_fwd(const zi_combine *combine, const void *Z, const int32_t *slots, const float *weights, void *Y,
+                         void *stream);
+/* dZ[slots[t][j]] = RNE(weights[t][j] dY[t]), dweights[t][j] = dY[t] . Z[slots[t][j]].
+ * The slots are distinct (as the router gives them); rows of dZ that no slot names are
+ * not touched. */
+zi_status zi_combine_bwd(const zi_combine *combine, const void *dY, const void *Z, const int32_t *slots,
+                         const float *weights, void *dZ, float *dweights, void *stream);
+
+/* Low-rank adapters of many requests beside a shared projection Y0 = X W.  The rows
+ * of X lie in S segments, segment s at [offsets[s], offsets[s + 1]) (S + 1 int32 in
+ * device memory, ascending; what lies outside [0, T] is left out), each with the
+ * adapter ids[s]: A_n [r x K] and B_n [r x M], contiguous, the rank outermost.  Several
+ * segments may have one adapter.  A row in no segment, or in one whose id is outside
+ * [0, N), has no adapter.  K, M and the strides are multiples of 8, matrices 16-byte
+ * aligned. */
+typedef struct {
+    int64_t T;                       /* rows: 0 .. 2^23                                  */
+    int64_t K, M;                    /* columns of X and of Y: 8 .. 2^20                 */
+    int64_t ldx, lddx, lddx0;        /* row strides of X, dX, dX0; 0 = K                 */
+    int64_t ldy, ldy0;               /* of Y and dY, of Y0; 0 = M                        */
+    int32_t S;                       /* segments: 0 .. 2^23                              */
+    int32_t N;                       /* adapters: 1 .. 65536                             */
+    int32_t r;                       /* rank: 1 .. 256 (pad smaller ones with zeros)     */
+    int32_t dtype;                   /* X, A, B, dY: ZI_F16 or ZI_BF16                   */
+    int32_t out_dtype;               /* Y, Y0, dX, dX0: dtype or ZI_F32                  */
+    int32_t accumulate;              /* backward: add to dA and dB (else overwrite all)  */
+} zi_adapters;
+
+/* U = A_n X^T (fp32, [r x T], contiguous; zero for rows without an adapter), and
+ * Y = RNE(Y0 + scales[n] U^T B_n).  Y0 NULL: zero; it may be Y itself.  U, which the
+ * backward takes, may be NULL.  The workspace for T rows also serves fewer. */
+uint64_t zi_adapters_fwd_bytes(int64_t T, int32_t r);
+zi_status zi_adapters_fwd(const zi_adapters *adapters, const void *X, const void *A, const void *B,
+                          const int32_t *offsets, const int32_t *ids, const float *scales, const void *Y0, void *Y,
+                          float *U, void *workspace, uint64_t workspace_bytes, void *stream);
+/* From the forward's U, with dU = scales[n] B_n dY^T: dX = RNE(dX0 + dU^T A_n) (dX NULL:
+ * not formed; dX0 NULL: zero; it may be dX itself), dA_n (+)= sum dU X and
+ * dB_n (+)= scales[n] sum U dY over the rows of adapter n (fp32, the same bits every
+ * time; zero, or as they were, for adapters without rows). */
+uint64_t zi_adapters_bwd_bytes(int64_t T, int32_t r);
+zi_status zi_adapters_bwd(const zi_adapters *adapters, const void *X, const void *dY, const float *U, const void *A,
+                          const void *B, const int32_t *offsets, const int32_t *ids, const float *scales,
+                          const void *dX0, void *dX, float *dA, float *dB, void *workspace,
+                          uint64_t workspace_bytes, void *stream);
+
 /* Page-locked host memory (hipHostMalloc) for W^t / dW^t; 4096-byte aligned. */
 zi_status zi_host_alloc(uint64_t bytes, void **out);
 zi_status zi_host_free(void *ptr);

@@ -43,6 +43,11 @@ import sys
 from typing import Iterable, List, Optional, Set, Tuple
 
 RESULT_WAIT = 18
+# MFMAs that the compiler knows (builtins) are spaced by it, except that it has been
+# seen to read a result right behind the loop that made it, with no wait states at
+# all: a kernel then lost its last product now and then.  The wait states of the
+# forms used: 16-bit ones of 4 passes, fp32 ones of 8.
+BUILTIN_RESULT_WAIT = {"v_mfma_f32_16x16x32_f16": 7, "v_mfma_f32_16x16x32_bf16": 7, "v_mfma_f32_16x16x4_f32": 10}
 VALU_TO_MFMA = 2
 
 Reg = Tuple[str, int]
@@ -214,7 +219,46 @@ def check_kernel(body: List[Tuple[int, str]]) -> List[str]:
     return sorted(set(found))
 
 
-def check_file(path: str, kernel_filter: str = "") -> dict:
+def early_reads(body: List[Tuple[int, str]]) -> List[str]:
+    """Non-MFMA instructions that touch an MFMA's result before
+    its BUILTIN_RESULT_WAIT wait states, in a kernel whose MFMAs the compiler made:
+    along the listing, and along every branch of it that is taken."""
+    instrs: List[Instr] = []
+    labels = {}
+    for no, line in body:
+        m = _LABEL.match(line.strip())
+        if m:
+            labels[m.group(1)] = len(instrs)
+            continue
+        ins = _parse(line, no)
+        if ins is not None:
+            instrs.append(ins)
+    found: List[str] = []
+
+    def follow(i: int, waits: int, dst: Set[Reg], mfma: Instr, jumped: bool) -> None:
+        while i < len(instrs) and waits < BUILTIN_RESULT_WAIT.get(mfma.op, RESULT_WAIT):
+            ins = instrs[i]
+            if ins.is_mfma:
+                dst = dst - regs(ins.args[0])  # overwritten, and followed from there
+            elif ins.touched() & dst:
+                found.append("line %d: %r touches the result of MFMA %r (line %d) after %d wait states"
+                             % (ins.line, ins.text, mfma.text, mfma.line, waits))
+                return
+            b = _BRANCH.match(ins.text)
+            if b and b.group(1) in labels and not jumped:
+                follow(labels[b.group(1)], waits + 1, dst, mfma, True)
+            if ins.op == "s_branch" or ins.op == "s_endpgm":
+                return
+            waits += ins.waits
+            i += 1
+
+    for i, ins in enumerate(instrs):
+        if ins.is_mfma:
+            follow(i + 1, 0, regs(ins.args[0]), ins, False)
+    return sorted(set(found))
+
+
+def check_file(path: str, kernel_filter: str = "", check=check_kernel) -> dict:
     """{kernel symbol: [findings]} for every kernel in the file whose name
     contains `kernel_filter`."""
     lines = open(path).read().splitlines()
@@ -225,14 +269,14 @@ def check_file(path: str, kernel_filter: str = "") -> dict:
         m = _KERNEL.match(line)
         if m and not line.startswith(".") and not line.startswith(" ") and not line.startswith("\t"):
             if cur is not None:
-                out[cur] = check_kernel(body)
+                out[cur] = check(body)
             cur = m.group(1) if kernel_filter in m.group(1) else None
             body = []
             continue
         if cur is None:
             continue
         if "s_endpgm" in line:
-            out[cur] = check_kernel(body)
+            out[cur] = check(body)
             cur = None
             continue
         body.append((no, line))

@@ -18,9 +18,12 @@ OBJDIR = os.path.join(HERE, "_build")
 
 ARCH = "gfx950"
 SOURCES = ["zi_kernels.hip", "zi_api.cpp", "zi_plan.cpp", "zi_adam.cpp", "zi_source.cpp", "zi_noalloc.hip",
-           "zi_norm.hip", "zi_embed.hip", "zi_orth.hip", "zi_orth_gemm.hip"]
+           "zi_norm.hip", "zi_embed.hip", "zi_orth.hip", "zi_orth_gemm.hip", "zi_route.hip",
+           "zi_grouped.hip", "zi_grouped_fwd.hip", "zi_grouped_dx.hip", "zi_grouped_dw.hip", "zi_adapter.hip"]
 # sources with matrix-core instructions in inline assembly
-MFMA_SOURCES = ["zi_kernels.hip", "zi_orth_gemm.hip"]
+MFMA_SOURCES = ["zi_kernels.hip", "zi_orth_gemm.hip", "zi_grouped_fwd.hip", "zi_grouped_dx.hip", "zi_grouped_dw.hip"]
+# sources with matrix-core builtins
+BUILTIN_SOURCES = ["zi_grouped.hip", "zi_adapter.hip"]
 COMMON = ["-O3", "-std=c++17", "-fPIC", "-Wall", "-Wno-unused-function",
           "-I" + os.path.join(ROOT, "include")]
 # Packed fp32 VALU forms are kept out of every device code object.
@@ -62,10 +65,10 @@ def _compile(src: str) -> str:
 def check_device_asm(src: str = "zi_kernels.hip") -> None:
     """Fail unless the kernels' matrix-core instructions keep their required
     wait states (the MFMAs are inline assembly, which the compiler does not
-    pad)."""
+    pad; of builtins it misses some)."""
     from . import asm_check
     path = device_asm(src)
-    res = asm_check.check_file(path)
+    res = asm_check.check_file(path, check=asm_check.early_reads if src in BUILTIN_SOURCES else asm_check.check_kernel)
     bad = {k: v for k, v in res.items() if v}
     if not res:
         raise RuntimeError("no kernels found in %s" % path)
@@ -84,7 +87,7 @@ def build(verbose: bool = False) -> str:
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError("link failed: %s\n%s\n%s" % (" ".join(cmd), r.stdout, r.stderr))
-    for src in MFMA_SOURCES:
+    for src in MFMA_SOURCES + BUILTIN_SOURCES:
         check_device_asm(src)
     os.replace(tmp, LIB)
     if verbose:

@@ -1,0 +1,616 @@
+// zi_adapter.hip -- low-rank adapters of many requests beside a shared projection.
+//
+// The T rows of a batch lie in S segments (a request's prompt, or its one new token),
+// each with one of N adapters: A_n [r x K], B_n [r x M], the rank outermost in both.
+//   U = A_n X^T (r x T, fp32),  Y = Y0 + s_n U^T B_n
+// and backward, with dU = s_n B_n dY^T,
+//   dX = dX0 + dU^T A_n,  dA_n = sum dU X,  dB_n = s_n sum U dY  over the adapter's rows.
+// With the rank outermost everywhere these are three kernels:
+//   shrink  U from X and A, dU from dY and B      reads the wide rows once
+//   expand  Y from U and B, dX from dU and A      reads and writes the wide rows once
+//   grad    dA from dU and X, dB from U and dY    reads the wide rows once
+// All are bound by the bytes of the wide rows while r is small.  U is kept in fp32 and
+// multiplied as such: the fp32 matrix instruction (16 x 16 x 4, 157 TFLOP/s) is as fast
+// as HBM up to a rank of about 64 (expand) or 32 (grad), needs no second rounding of U,
+// and takes the other operand as it lies in memory: a lane's 16 bytes are eight
+// columns of one row, which go to eight instructions whose results are eight
+// consecutive columns again.  shrink's operands are 16-bit inputs, multiplied exactly
+// by the 16-bit instruction.
+//
+// A row's result depends on that row and its adapter alone: segments are multiplied one
+// by one, so that an infinity or a NaN in one request or adapter reaches no other.
+#include <hip/hip_runtime.h>
+#include <math.h>
+#include <stdint.h>
+
+#include "zi_host.h"
+#include "zi_stream.h"
+#include "zi_vec.h"
+
+namespace zi {
+namespace {
+
+int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
+int64_t min64(int64_t a, int64_t b) { return a < b ? a : b; }
+int64_t max64(int64_t a, int64_t b) { return a > b ? a : b; }
+
+struct Segments {
+    const int32_t *offsets;  // [count + 1]
+    const int32_t *ids;      // [count]
+    int32_t count, adapters, rows;
+};
+
+// f(n, a, b) for the runs [a, b) of rows, in order and without gaps, that cover
+// [b0, b1): n is the adapter of the run, -1 where there is none.  Whatever the offsets
+// hold, every row comes once.
+template <typename F>
+__device__ __forceinline__ void for_runs(const Segments &g, int b0, int b1, F &&f) {
+    // the first segment that ends past b0, by a search over 64 parts at a time
+    const int lane = threadIdx.x & 63;
+    int s = 0, n = g.count;
+    while (n > 0) {
+        const int step = (n + 63) / 64, at = (lane + 1) * step - 1;
+        const bool before = at < n && g.offsets[s + at + 1] <= b0;
+        const int parts = __builtin_popcountll(__ballot(before));
+        s += parts * step;
+        n = min(step - 1, n - parts * step);
+    }
+    int at = b0;
+    for (; at < b1 && s < g.count; ++s) {
+        const int lo = min(max(g.offsets[s], at), b1), hi = min(max(g.offsets[s + 1], lo), b1);
+        if (lo > at) f(-1, at, lo);
+        if (hi > lo) {
+            const int id = g.ids[s];
+            f(id >= 0 && id < g.adapters ? id : -1, lo, hi);
+        }
+        at = hi;
+    }
+    if (at < b1) f(-1, at, b1);
+}
+
+// ---- shrink --------------------------------------------------------------------------------
+
+struct ShrinkArgs {
+    const uint16_t *X, *A;  // rows [T][ldx], adapters [N][r][K]
+    int64_t ldx;
+    const float *scales;  // null: one
+    float *U;             // [parts][r][T]
+    Segments seg;
+    int32_t K, r, block, parts;  // rows a workgroup; shares of the reduction
+};
+
+// A workgroup: `block` rows (at most 16 PF) by 16 QF ranks at a time, one part of the
+// reduction, which its four waves share.
+template <typename T, int QF, int PF>
+__global__ __launch_bounds__(256) void shrink_kernel(ShrinkArgs a) {
+    __shared__ f32x4 sums[4][QF * PF][64];
+    const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int b0 = blockIdx.x * a.block, b1 = min(b0 + a.block, a.seg.rows);
+    const int steps = (a.K + 31) / 32;
+    const int from = (int)((int64_t)steps * blockIdx.y / a.parts), to = (int)((int64_t)steps * (blockIdx.y + 1) / a.parts);
+    const int share = (to - from + 3) / 4, s0 = from + wave * share, s1 = min(s0 + share, to);
+    float *U = a.U + (int64_t)blockIdx.y * a.r * a.seg.rows;
+    for_runs(a.seg, b0, b1, [&](int n, int lo, int hi) __attribute__((always_inline)) {
+        if (n < 0) {
+            const int rows = hi - lo;
+            for (int i = tid; i < a.r * rows; i += 256) U[(int64_t)(i / rows) * a.seg.rows + lo + i % rows] = 0.f;
+            return;
+        }
+        const float scale = a.scales ? a.scales[n] : 1.f;
+        uint32_t xo[PF];
+        fragment_offsets(hi - lo, a.ldx, xo);
+        for (int r0 = 0; r0 < a.r; r0 += 16 * QF) {
+            uint32_t ao[QF];
+            fragment_offsets(a.r - r0, a.K, ao);
+            f32x4 acc[QF][PF] = {};
+            stream_product<T, QF, PF, (QF * PF > 8 ? 2 : 4)>(buffer_of(a.A + ((int64_t)n * a.r + r0) * a.K), ao,
+                                                             buffer_of(a.X + lo * a.ldx), xo, s0, s1, a.K, acc);
+#pragma unroll
+            for (int i = 0; i < QF; ++i)
+#pragma unroll
+                for (int j = 0; j < PF; ++j) sums[wave][i * PF + j][lane] = acc[i][j];
+            __syncthreads();
+            for (int t = tid; t < QF * PF * 64; t += 256) {
+                const int f = t >> 6, ln = t & 63;
+                f32x4 v = sums[0][f][ln];
+#pragma unroll
+                for (int k = 1; k < 4; ++k) v += sums[k][f][ln];
+                const int rank = r0 + 16 * (f / PF) + 4 * (ln >> 4), row = lo + 16 * (f % PF) + (ln & 15);
+                if (row < hi) {
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        if (rank + e < a.r) U[(int64_t)(rank + e) * a.seg.rows + row] = v[e] * scale;
+                }
+            }
+            __syncthreads();
+        }
+    });
+}
+
+// ---- expand --------------------------------------------------------------------------------
+
+struct ExpandArgs {
+    const float *U;       // [parts][r][T]
+    float *U_out;         // the parts' sum, or null
+    const uint16_t *B;    // [N][r][M]
+    const float *scales;  // null: one
+    const void *Y0;       // null: zero
+    void *Y;
+    int64_t ldy0, ldy;
+    Segments seg;
+    int32_t M, r, parts;
+    int32_t same;  // Y is Y0: rows without an adapter are left
+};
+
+template <typename YT>
+__device__ __forceinline__ void load_y(const ExpandArgs &a, int64_t row, int64_t m, float (&v)[8]) {
+    if (a.Y0) {
+        load8(static_cast<const YT *>(a.Y0) + row * a.ldy0 + m, v);
+    } else {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) v[e] = 0.f;
+    }
+}
+
+// U[rank][row] as the sum of its parts, in order.
+__device__ __forceinline__ float u_at(const ExpandArgs &a, int rank, int row) {
+    const float *p = a.U + (int64_t)rank * a.seg.rows + row;
+    float u = *p;
+    for (int k = 1; k < a.parts; ++k) u += p[(int64_t)k * a.r * a.seg.rows];
+    return u;
+}
+
+constexpr int kExpandRows = 64, kExpandCols = 512;
+
+// 64 rows by 128 columns a wave: per step of four ranks a lane reads eight columns of
+// one row of B_n and one value of U for each of four fragments of 16 rows; instruction
+// (i, j) gives rows 16 i + 4 (lane / 16) .. +3 of column 8 (lane % 16) + j.
+template <typename T, typename YT>
+__global__ __launch_bounds__(256) void expand_kernel(ExpandArgs a) {
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, c = lane & 15, g = lane >> 4;
+    const int b0 = blockIdx.x * kExpandRows, b1 = min(b0 + kExpandRows, a.seg.rows);
+    const int m = blockIdx.y * kExpandCols + wave * 128 + 8 * c;
+    const bool in = m < a.M;
+    for_runs(a.seg, b0, b1, [&](int n, int lo, int hi) __attribute__((always_inline)) {
+        if (n < 0 && a.same) return;
+        f32x4 acc[4][8] = {};
+        if (n >= 0) {
+            const uint16_t *B = a.B + (int64_t)n * a.r * a.M + m;
+            const float scale = a.scales ? a.scales[n] : 1.f;
+            for (int r0 = 0; r0 < a.r; r0 += 4) {
+                const int rank = r0 + g;
+                float b[8], u[4];
+#pragma unroll
+                for (int j = 0; j < 8; ++j) b[j] = 0.f;
+                if (in && rank < a.r) load8(reinterpret_cast<const T *>(B + (int64_t)rank * a.M), b);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const int row = b0 + 16 * i + c;
+                    u[i] = rank < a.r && row >= lo && row < hi ? u_at(a, rank, row) : 0.f;
+                    if (a.U_out && blockIdx.y == 0 && wave == 0 && rank < a.r && row >= lo && row < hi)
+                        a.U_out[(int64_t)rank * a.seg.rows + row] = u[i];
+                    u[i] *= scale;
+                }
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x4f32(u[i], b[j], acc[i][j], 0, 0, 0);
+            }
+        } else if (a.U_out && blockIdx.y == 0) {
+            for (int i = threadIdx.x; i < a.r * (hi - lo); i += 256)
+                a.U_out[(int64_t)(i / (hi - lo)) * a.seg.rows + lo + i % (hi - lo)] = 0.f;
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const int row = b0 + 16 * i + 4 * g + e;
+                if (in && row >= lo && row < hi) {
+                    float y[8];
+                    load_y<YT>(a, row, m, y);
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) y[j] += acc[i][j][e];
+                    store8(static_cast<YT *>(a.Y) + row * a.ldy + m, y);
+                }
+            }
+        }
+    });
+}
+
+// One row by 2048 columns, for segments of a token or so: the multiplications are few,
+// and B_n is read once, eight columns a thread, sixteen ranks in flight.
+constexpr int kMostRank = 256;
+template <typename T, typename YT>
+__global__ __launch_bounds__(256) void expand_row_kernel(ExpandArgs a) {
+    __shared__ float u[kMostRank];
+    const int row = blockIdx.x;
+    const int m = (blockIdx.y * 256 + threadIdx.x) * 8;
+    for_runs(a.seg, row, row + 1, [&](int n, int lo, int hi) __attribute__((always_inline)) {
+        (void)lo;
+        (void)hi;
+        if (n < 0 && a.same && !a.U_out) return;
+        const float scale = n >= 0 && a.scales ? a.scales[n] : 1.f;
+        for (int i = threadIdx.x; i < a.r; i += 256) {
+            const float v = n >= 0 ? u_at(a, i, row) : 0.f;
+            if (a.U_out && blockIdx.y == 0) a.U_out[(int64_t)i * a.seg.rows + row] = v;
+            u[i] = v * scale;
+        }
+        __syncthreads();
+        if (m >= a.M || (n < 0 && a.same)) return;
+        float y[8], d[8] = {};
+        load_y<YT>(a, row, m, y);
+        if (n >= 0) {
+            const T *B = reinterpret_cast<const T *>(a.B + (int64_t)n * a.r * a.M + m);
+            int k = 0;
+            for (; k + 16 <= a.r; k += 16) {
+                u32x4 raw[16];
+#pragma unroll
+                for (int q = 0; q < 16; ++q) raw[q] = *reinterpret_cast<const u32x4 *>(B + (int64_t)(k + q) * a.M);
+#pragma unroll
+                for (int q = 0; q < 16; ++q)
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) d[e] += u[k + q] * value16<T>((raw[q][e >> 1] >> (16 * (e & 1))) & 0xffffu);
+            }
+            for (; k < a.r; ++k) {
+                float b[8];
+                load8(B + (int64_t)k * a.M, b);
+#pragma unroll
+                for (int e = 0; e < 8; ++e) d[e] += u[k] * b[e];
+            }
+        }
+#pragma unroll
+        for (int e = 0; e < 8; ++e) y[e] += d[e];
+        store8(static_cast<YT *>(a.Y) + row * a.ldy + m, y);
+    });
+}
+
+// ---- grad ----------------------------------------------------------------------------------
+
+struct GradArgs {
+    const float *V;     // [r][T]
+    const uint16_t *X;  // [T][ldx]
+    int64_t ldx;
+    const float *scales;  // null: one
+    float *G;             // [N][r][K]
+    float *part;          // [splits][N][r][K] where splits > 1
+    Segments seg;
+    int32_t K, r, splits, accumulate;
+};
+
+// One adapter by 128 columns by 16 F ranks a workgroup, over one split of the adapter's
+// rows; its four waves take chunks of 16 rows in turn.  Of a chunk a lane reads V at
+// rank lane % 16 of four rows and, of each of those, eight columns.
+template <typename T, int F>
+__global__ __launch_bounds__(256) void grad_kernel(GradArgs a) {
+    __shared__ f32x4 sums[4][8][64];
+    const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int c = lane & 15, g = lane >> 4;
+    const int n = blockIdx.x / a.splits, split = blockIdx.x % a.splits;
+    const int k0 = blockIdx.y * 128, r0 = blockIdx.z * (16 * F);
+    const bool in = k0 + 8 * c < a.K;
+    const uint16_t *X = a.X + k0 + 8 * c;
+    f32x4 acc[F][8] = {};
+    for (int s0 = 0; s0 < a.seg.count; s0 += 64) {
+        uint64_t mine = __ballot(s0 + lane < a.seg.count && a.seg.ids[min(s0 + lane, a.seg.count - 1)] == n);
+        while (mine) {
+            const int s = s0 + __builtin_ctzll(mine);
+            mine &= mine - 1;
+            const int lo = min(max(a.seg.offsets[s], 0), a.seg.rows), hi = min(max(a.seg.offsets[s + 1], lo), a.seg.rows);
+            for (int t0 = lo + 16 * (split * 4 + wave); t0 < hi; t0 += 64 * a.splits) {
+                u32x4 x[4];
+                float v[F][4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const int t = t0 + 4 * g + i;
+                    x[i] = u32x4{0, 0, 0, 0};
+                    if (in && t < hi) x[i] = *reinterpret_cast<const u32x4 *>(X + t * a.ldx);
+#pragma unroll
+                    for (int f = 0; f < F; ++f) {
+                        const int rank = r0 + 16 * f + c;
+                        v[f][i] = t < hi && rank < a.r ? a.V[(int64_t)rank * a.seg.rows + t] : 0.f;
+                    }
+                }
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) {
+                        const float b = value16<T>((x[i][j >> 1] >> (16 * (j & 1))) & 0xffffu);
+#pragma unroll
+                        for (int f = 0; f < F; ++f)
+                            acc[f][j] = __builtin_amdgcn_mfma_f32_16x16x4f32(v[f][i], b, acc[f][j], 0, 0, 0);
+                    }
+                }
+            }
+        }
+    }
+    const float scale = a.scales ? a.scales[n] : 1.f;
+    const bool whole = a.splits == 1;
+    float *out = (whole ? a.G : a.part + (int64_t)split * a.seg.adapters * a.r * a.K) + (int64_t)n * a.r * a.K;
+#pragma unroll
+    for (int f = 0; f < F; ++f) {
+        __syncthreads();
+#pragma unroll
+        for (int j = 0; j < 8; ++j) sums[wave][j][lane] = acc[f][j];
+        __syncthreads();
+        // thread (lane, wave): row 4 (lane / 16) + wave of the fragment, eight columns
+        float v[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            v[j] = sums[0][j][lane][wave];
+#pragma unroll
+            for (int k = 1; k < 4; ++k) v[j] += sums[k][j][lane][wave];
+            v[j] *= scale;
+        }
+        const int rank = r0 + 16 * f + 4 * g + wave;
+        if (in && rank < a.r) {
+            float *p = out + (int64_t)rank * a.K + k0 + 8 * c;
+            if (whole && a.accumulate) {
+                float old[8];
+                load8(p, old);
+#pragma unroll
+                for (int j = 0; j < 8; ++j) v[j] += old[j];
+            }
+            store8(p, v);
+        }
+    }
+}
+
+// out[i] (+)= the sum of part[p][i] over the parts, in order.
+__global__ __launch_bounds__(256) void sum_parts_kernel(const float *part, int parts, int64_t n, float *out, int accumulate) {
+    for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < n; i += (int64_t)gridDim.x * 256) {
+        float v = part[i];
+        for (int p = 1; p < parts; ++p) v += part[p * n + i];
+        out[i] = accumulate ? out[i] + v : v;
+    }
+}
+
+// ---- launches ------------------------------------------------------------------------------
+
+// Rows a workgroup of shrink: one where segments are of a token or so, as many as fit
+// otherwise.
+int block_of(int64_t T, int64_t S) {
+    const int64_t mean = T / S;
+    return mean < 4 ? 1 : mean <= 32 ? 16 : 64;
+}
+// Shares of the reduction, so that a few rows still occupy the chip: at least 512
+// columns each.
+constexpr int64_t kShrinkGroups = 512, kMostParts = 16;
+int64_t parts_of(int64_t T, int64_t S, int64_t K) {
+    const int64_t blocks = ceil_div(T, block_of(T, S));
+    return max64(1, min64(min64(kShrinkGroups / blocks, kMostParts), K / 512));
+}
+// What any T' <= T rows take: blocks * 64 >= T.
+uint64_t u_bytes(int64_t T, int64_t r) { return (uint64_t)max64(T, min64(kMostParts * T, 64 * kShrinkGroups)) * (uint64_t)r * 4; }
+uint64_t round_up(uint64_t n) { return (n + 255) / 256 * 256; }
+
+// Splits of the adapters' rows, so that a few adapters still occupy the chip.
+constexpr int64_t kGradGroups = 512;
+int64_t splits_of(int64_t T, int64_t N, int64_t K) {
+    return max64(1, min64(kGradGroups / (N * ceil_div(K, 128)), ceil_div(T, 256)));
+}
+uint64_t part_bytes(int64_t r) { return (uint64_t)kGradGroups * 128 * (uint64_t)r * 4; }
+
+template <typename T, int QF>
+hipError_t shrink_blocks(const ShrinkArgs &a, hipStream_t s) {
+    const dim3 grid((unsigned)ceil_div(a.seg.rows, a.block), (unsigned)a.parts);
+    if (a.block <= 16)
+        hipLaunchKernelGGL((shrink_kernel<T, QF, 1>), grid, dim3(256), 0, s, a);
+    else
+        hipLaunchKernelGGL((shrink_kernel<T, QF, 4>), grid, dim3(256), 0, s, a);
+    return hipGetLastError();
+}
+hipError_t shrink(int dtype, const ShrinkArgs &a, hipStream_t s) {
+    auto go = [&](auto type) {
+        using T = decltype(type);
+        return a.r <= 16 ? shrink_blocks<T, 1>(a, s) : a.r <= 32 ? shrink_blocks<T, 2>(a, s) : shrink_blocks<T, 4>(a, s);
+    };
+    return dtype == ZI_F16 ? go(f16_t{}) : go(bf16_t{});
+}
+
+template <typename T, typename YT>
+hipError_t expand_typed(const ExpandArgs &a, bool rows, hipStream_t s) {
+    if (rows)
+        hipLaunchKernelGGL((expand_row_kernel<T, YT>), dim3((unsigned)a.seg.rows, (unsigned)ceil_div(a.M, 2048)), dim3(256), 0, s, a);
+    else
+        hipLaunchKernelGGL((expand_kernel<T, YT>),
+                           dim3((unsigned)ceil_div(a.seg.rows, kExpandRows), (unsigned)ceil_div(a.M, kExpandCols)), dim3(256), 0, s,
+                           a);
+    return hipGetLastError();
+}
+hipError_t expand(int dtype, int out_dtype, const ExpandArgs &a, bool rows, hipStream_t s) {
+    if (dtype == ZI_F16) return out_dtype == ZI_F32 ? expand_typed<f16_t, float>(a, rows, s) : expand_typed<f16_t, f16_t>(a, rows, s);
+    return out_dtype == ZI_F32 ? expand_typed<bf16_t, float>(a, rows, s) : expand_typed<bf16_t, bf16_t>(a, rows, s);
+}
+
+hipError_t sum_parts(const float *part, int64_t parts, int64_t n, float *out, int accumulate, hipStream_t s) {
+    hipLaunchKernelGGL(sum_parts_kernel, dim3((unsigned)min64(ceil_div(n, 256), 4096)), dim3(256), 0, s, part, (int)parts, n, out,
+                       accumulate);
+    return hipGetLastError();
+}
+
+hipError_t grad(int dtype, GradArgs a, hipStream_t s) {
+    a.splits = (int32_t)splits_of(a.seg.rows, a.seg.adapters, a.K);
+    auto go = [&](auto type, auto frags) {
+        constexpr int F = decltype(frags)::value;
+        hipLaunchKernelGGL((grad_kernel<decltype(type), F>),
+                           dim3((unsigned)(a.seg.adapters * a.splits), (unsigned)ceil_div(a.K, 128), (unsigned)ceil_div(a.r, 16 * F)),
+                           dim3(256), 0, s, a);
+        return hipGetLastError();
+    };
+    auto sized = [&](auto type) {
+        return a.r <= 16 ? go(type, std::integral_constant<int, 1>{})
+                         : a.r <= 32 ? go(type, std::integral_constant<int, 2>{}) : go(type, std::integral_constant<int, 4>{});
+    };
+    const hipError_t e = dtype == ZI_F16 ? sized(f16_t{}) : sized(bf16_t{});
+    if (e != hipSuccess || a.splits == 1) return e;
+    return sum_parts(a.part, a.splits, (int64_t)a.seg.adapters * a.r * a.K, a.G, a.accumulate, s);
+}
+
+bool aligned(const void *p, uint64_t to) { return ((uintptr_t)p & (to - 1)) == 0; }
+
+zi_status check(const zi_adapters *p) {
+    if (!p) return fail(ZI_ERR_ARG, "adapters is NULL");
+    // a workgroup a row, and a launch's threads are a 32-bit number
+    if (p->T < 0 || p->T > (1 << 23)) return fail(ZI_ERR_SHAPE, "T = %lld: 0 .. 2^23 rows", (long long)p->T);
+    if (p->K < 8 || p->M < 8 || p->K % 8 || p->M % 8 || p->K > kGroupLd || p->M > kGroupLd)
+        return fail(ZI_ERR_SHAPE, "K = %lld, M = %lld: multiples of 8 up to 2^20", (long long)p->K, (long long)p->M);
+    if (p->N < 1 || p->N > 65536) return fail(ZI_ERR_SHAPE, "N = %d: 1 .. 65536 adapters", p->N);
+    if (p->r < 1 || p->r > kMostRank) return fail(ZI_ERR_SHAPE, "r = %d: 1 .. %d", p->r, kMostRank);
+    if (p->S < 0 || p->S > (1 << 23)) return fail(ZI_ERR_SHAPE, "S = %d: 0 .. 2^23 segments", p->S);
+    const int64_t lds[5] = {p->ldx, p->lddx, p->lddx0, p->ldy, p->ldy0};
+    for (int i = 0; i < 5; ++i)
+        if (lds[i] < 0 || lds[i] % 8 || lds[i] > kGroupLd || (lds[i] && lds[i] < (i < 3 ? p->K : p->M)))
+            return fail(ZI_ERR_SHAPE, "row strides are multiples of 8, at least a row and up to 2^20");
+    if (p->dtype != ZI_F16 && p->dtype != ZI_BF16) return fail(ZI_ERR_ARG, "dtype %d: fp16 or bf16", p->dtype);
+    if (p->out_dtype != p->dtype && p->out_dtype != ZI_F32) return fail(ZI_ERR_ARG, "out_dtype %d: dtype or fp32", p->out_dtype);
+    return ZI_OK;
+}
+
+zi_status check_work(uint64_t need, const void *workspace, uint64_t bytes) {
+    if (!workspace || bytes < need)
+        return fail(ZI_ERR_BUDGET, "the workspace holds %llu B, the adapters need %llu", (unsigned long long)(workspace ? bytes : 0),
+                    (unsigned long long)need);
+    if (!aligned(workspace, 256)) return fail(ZI_ERR_ALIGN, "the workspace is not 256-byte aligned");
+    return ZI_OK;
+}
+
+Segments segments_of(const zi_adapters *p, const int32_t *offsets, const int32_t *ids) {
+    return {offsets, ids, p->S, p->N, (int32_t)p->T};
+}
+
+}  // namespace
+}  // namespace zi
+
+using namespace zi;
+
+extern "C" uint64_t zi_adapters_fwd_bytes(int64_t T, int32_t r) { return T < 1 || r < 1 ? 0 : round_up(u_bytes(T, r)); }
+
+extern "C" zi_status zi_adapters_fwd(const zi_adapters *p, const void *X, const void *A, const void *B, const int32_t *offsets,
+                                     const int32_t *ids, const float *scales, const void *Y0, void *Y, float *U, void *workspace,
+                                     uint64_t workspace_bytes, void *stream) {
+    clear_error();
+    zi_status st = check(p);
+    if (st != ZI_OK || p->T == 0) return st;
+    if (!X || !A || !B || !offsets || !scales || !Y || (p->S > 0 && !ids))
+        return fail(ZI_ERR_ARG, "X, A, B, offsets, ids, scales and Y are required");
+    if (!aligned(X, 16) || !aligned(A, 16) || !aligned(B, 16) || !aligned(Y0, 16) || !aligned(Y, 16) || !aligned(offsets, 4) ||
+        !aligned(ids, 4) || !aligned(scales, 4) || !aligned(U, 4))
+        return fail(ZI_ERR_ALIGN, "a matrix is not 16-byte aligned, or a vector not to its element");
+    if (Y0 == Y && (p->ldy0 ? p->ldy0 : p->M) != (p->ldy ? p->ldy : p->M)) return fail(ZI_ERR_SHAPE, "Y is Y0, with another row stride");
+    if ((st = check_work(zi_adapters_fwd_bytes(p->T, p->r), workspace, workspace_bytes)) != ZI_OK) return st;
+    hipStream_t s = static_cast<hipStream_t>(stream);
+    const int64_t S = max64(p->S, 1), parts = parts_of(p->T, S, p->K);
+    float *u = parts == 1 && U ? U : static_cast<float *>(workspace);
+    const int block = block_of(p->T, S);
+    ShrinkArgs a = {};
+    a.X = static_cast<const uint16_t *>(X);
+    a.A = static_cast<const uint16_t *>(A);
+    a.ldx = p->ldx ? p->ldx : p->K;
+    a.U = u;
+    a.seg = segments_of(p, offsets, ids);
+    a.K = (int32_t)p->K;
+    a.r = p->r;
+    a.block = block;
+    a.parts = (int32_t)parts;
+    hipError_t e = shrink(p->dtype, a, s);
+    if (e == hipSuccess) {
+        ExpandArgs b = {};
+        b.U = u;
+        b.U_out = parts > 1 ? U : nullptr;
+        b.B = static_cast<const uint16_t *>(B);
+        b.scales = scales;
+        b.Y0 = Y0;
+        b.Y = Y;
+        b.ldy = p->ldy ? p->ldy : p->M;
+        b.ldy0 = p->ldy0 ? p->ldy0 : p->M;
+        b.seg = a.seg;
+        b.M = (int32_t)p->M;
+        b.r = p->r;
+        b.parts = (int32_t)parts;
+        b.same = Y0 == Y;
+        e = expand(p->dtype, p->out_dtype, b, block == 1, s);
+    }
+    if (e != hipSuccess) return fail(ZI_ERR_HIP, "adapters forward: %s", hipGetErrorString(e));
+    return ZI_OK;
+}
+
+extern "C" uint64_t zi_adapters_bwd_bytes(int64_t T, int32_t r) {
+    return T < 1 || r < 1 ? 0 : round_up(u_bytes(T, r)) + round_up((uint64_t)T * r * 4) + part_bytes(r);
+}
+
+extern "C" zi_status zi_adapters_bwd(const zi_adapters *p, const void *X, const void *dY, const float *U, const void *A, const void *B,
+                                     const int32_t *offsets, const int32_t *ids, const float *scales, const void *dX0, void *dX,
+                                     float *dA, float *dB, void *workspace, uint64_t workspace_bytes, void *stream) {
+    clear_error();
+    zi_status st = check(p);
+    if (st != ZI_OK) return st;
+    if (!dA || !dB) return fail(ZI_ERR_ARG, "dA and dB are required");
+    if (p->T > 0 && (!X || !dY || !U || !A || !B || !offsets || !scales || (p->S > 0 && !ids)))
+        return fail(ZI_ERR_ARG, "X, dY, U, A, B, offsets, ids and scales are required");
+    if (dX0 && !dX) return fail(ZI_ERR_ARG, "dX0 without dX");
+    if (!aligned(X, 16) || !aligned(dY, 16) || !aligned(A, 16) || !aligned(B, 16) || !aligned(dX0, 16) || !aligned(dX, 16) ||
+        !aligned(dA, 16) || !aligned(dB, 16) || !aligned(offsets, 4) || !aligned(ids, 4) || !aligned(scales, 4) || !aligned(U, 4))
+        return fail(ZI_ERR_ALIGN, "a matrix is not 16-byte aligned, or a vector not to its element");
+    if (dX && dX0 == dX && (p->lddx0 ? p->lddx0 : p->K) != (p->lddx ? p->lddx : p->K))
+        return fail(ZI_ERR_SHAPE, "dX is dX0, with another row stride");
+    if (p->T > 0 && (st = check_work(zi_adapters_bwd_bytes(p->T, p->r), workspace, workspace_bytes)) != ZI_OK) return st;
+    hipStream_t s = static_cast<hipStream_t>(stream);
+    const int64_t S = max64(p->S, 1);
+    char *work = static_cast<char *>(workspace);
+    float *parted = reinterpret_cast<float *>(work), *dU = reinterpret_cast<float *>(work + round_up(u_bytes(p->T, p->r)));
+    float *part = reinterpret_cast<float *>(work + round_up(u_bytes(p->T, p->r)) + round_up((uint64_t)p->T * p->r * 4));
+    const Segments seg = segments_of(p, offsets, ids);
+    hipError_t e = hipSuccess;
+    if (p->T > 0) {
+        const int64_t parts = parts_of(p->T, S, p->M);
+        ShrinkArgs a = {};
+        a.X = static_cast<const uint16_t *>(dY);
+        a.A = static_cast<const uint16_t *>(B);
+        a.ldx = p->ldy ? p->ldy : p->M;
+        a.scales = scales;
+        a.U = parts == 1 ? dU : parted;
+        a.seg = seg;
+        a.K = (int32_t)p->M;
+        a.r = p->r;
+        a.block = block_of(p->T, S);
+        a.parts = (int32_t)parts;
+        e = shrink(p->dtype, a, s);
+        if (e == hipSuccess && parts > 1) e = sum_parts(parted, parts, p->T * p->r, dU, 0, s);
+        if (e == hipSuccess && dX) {
+            ExpandArgs b = {};
+            b.U = dU;
+            b.B = static_cast<const uint16_t *>(A);
+            b.Y0 = dX0;
+            b.Y = dX;
+            b.ldy = p->lddx ? p->lddx : p->K;
+            b.ldy0 = p->lddx0 ? p->lddx0 : p->K;
+            b.seg = seg;
+            b.M = (int32_t)p->K;
+            b.r = p->r;
+            b.parts = 1;
+            b.same = dX0 == dX;
+            e = expand(p->dtype, p->out_dtype, b, a.block == 1, s);
+        }
+    }
+    auto one = [&](const float *V, const void *rows, int64_t ld, int64_t cols, const float *by, float *out) {
+        GradArgs a = {};
+        a.V = V;
+        a.X = static_cast<const uint16_t *>(rows);
+        a.ldx = ld;
+        a.scales = by;
+        a.G = out;
+        a.part = part;
+        a.seg = seg;
+        a.K = (int32_t)cols;
+        a.r = p->r;
+        a.accumulate = p->accumulate;
+        if (p->T == 0) a.seg.count = 0;  // zeros, or nothing added
+        return grad(p->dtype, a, s);
+    };
+    if (e == hipSuccess && !(p->T == 0 && p->accumulate)) {
+        e = one(dU, X, p->ldx ? p->ldx : p->K, p->K, nullptr, dA);
+        if (e == hipSuccess) e = one(U, dY, p->ldy ? p->ldy : p->M, p->M, p->T == 0 ? nullptr : scales, dB);
+    }
+    if (e != hipSuccess) return fail(ZI_ERR_HIP, "adapters backward: %s", hipGetErrorString(e));
+    return ZI_OK;
+}

@@ -66,8 +66,12 @@ constexpr int BK = kGemmStep;                        // reduction elements per s
 
 // Epilogues: RNE to 16 bits; fp32; GeLU (A and H = GeLU(A) in 16 bits);
 // accumulate into fp32 C; GeLU with A kept in fp32 (H still from the 16-bit A);
-// the three products of a step of the orthogonalised update (OrthArgs).
-enum Epi { EPI_LP = 0, EPI_F32 = 1, EPI_GELU = 2, EPI_ACC = 3, EPI_GELU_F32A = 4, EPI_GRAM = 5, EPI_POLY = 6, EPI_APPLY = 7 };
+// the three products of a step of the orthogonalised update (OrthArgs);
+// the grouped products' GeLU (C = GeLU(acc), C2 = acc) and its gradient (GroupArgs).
+enum Epi {
+    EPI_LP = 0, EPI_F32 = 1, EPI_GELU = 2, EPI_ACC = 3, EPI_GELU_F32A = 4, EPI_GRAM = 5, EPI_POLY = 6, EPI_APPLY = 7,
+    EPI_ACT = 8, EPI_DACT = 9
+};
 
 __device__ __forceinline__ uint32_t lds_addr(const char *p) { return (uint32_t)(uintptr_t)p; }
 
@@ -549,6 +553,114 @@ __device__ __forceinline__ void triangle_coords(int w, int n, int &tp, int &tq) 
     tq = 4 * g + c;
 }
 
+// The tile of workgroup w among nt, for the grouped products: 256 consecutive tiles
+// at a time (512 where two workgroups share a compute unit, per = 64), of which each
+// XCD takes 32 consecutive ones; the last, partial round is shared out evenly.
+// Negative: no tile.
+__device__ __forceinline__ int64_t grouped_order(int w, int64_t nt, int per) {
+    const int x = w & 7, k = w >> 3;
+    const int64_t full = nt / (8 * per);
+    if (k < full * per) return (int64_t)(k / per) * (8 * per) + x * per + k % per;
+    const int rest = (int)(nt - full * (8 * per));
+    const int at = (int)(k - full * per);
+    if (at >= (rest >> 3) + (x < (rest & 7) ? 1 : 0)) return -1;
+    return full * (8 * per) + x * (rest >> 3) + min(x, rest & 7) + at;
+}
+// Position r among tiles_p x tiles_q tiles: groups of 8 rows in column-major order,
+// so that 32 consecutive tiles read 12 panels and 256 read 40.
+__device__ __forceinline__ void grouped_coords(int64_t r, int tiles_p, int tiles_q, int &tp, int &tq) {
+    const int64_t per_group = 8 * (int64_t)tiles_q;
+    const int g = (int)(r / per_group);
+    const int rows = min(tiles_p - 8 * g, 8);
+    const int pos = (int)(r - g * per_group);
+    tp = 8 * g + pos % rows;
+    tq = pos / rows;
+}
+
+// A group's rows [lo, hi), clipped to [0, total) whatever the offsets hold.
+__device__ __forceinline__ void group_rows(const int32_t *offsets, int64_t total, int g, int64_t &lo, int64_t &hi) {
+    lo = min(max((int64_t)offsets[g], (int64_t)0), total);
+    hi = min(max((int64_t)offsets[g + 1], lo), total);
+}
+
+// Row tiles of 2^shift... rows each: the tile of workgroup w among those of all
+// groups, tiles_q columns of tiles wide.  Every wave finds it by itself: a lane takes
+// a group, and a scan over the wave counts the row tiles before it.  False: no tile.
+struct GroupTile {
+    int group, tp, tq;
+    int64_t lo, hi;
+};
+template <int TP>
+__device__ __forceinline__ bool find_group_tile(const int32_t *offsets, int groups, int64_t total, int w, int tiles_q, int per,
+                                                GroupTile &out) {
+    const int lane = threadIdx.x & 63;
+    int64_t row_tiles = 0;
+    for (int g0 = 0; g0 < groups; g0 += 64) {
+        int64_t lo = 0, hi = 0;
+        if (g0 + lane < groups) group_rows(offsets, total, g0 + lane, lo, hi);
+        int n = (int)((hi - lo + TP - 1) / TP);
+#pragma unroll
+        for (int d = 1; d < 64; d <<= 1) n += __shfl_xor(n, d, 64);
+        row_tiles += n;
+    }
+    const int64_t t = grouped_order(w, row_tiles * tiles_q, per);
+    if (t < 0) return false;
+    const int64_t row = t / tiles_q;
+    int64_t before = 0;
+    for (int g0 = 0; g0 < groups; g0 += 64) {
+        int64_t lo = 0, hi = 0;
+        if (g0 + lane < groups) group_rows(offsets, total, g0 + lane, lo, hi);
+        const int n = (int)((hi - lo + TP - 1) / TP);
+        int scan = n;
+#pragma unroll
+        for (int d = 1; d < 64; d <<= 1) {
+            const int y = __shfl_up(scan, d, 64);
+            scan += lane >= d ? y : 0;
+        }
+        const uint64_t past = __ballot(before + scan > row);
+        if (past) {
+            const int at = __builtin_ctzll(past);
+            const int tiles = __builtin_amdgcn_readlane(n, at);
+            const int64_t start = before + __builtin_amdgcn_readlane(scan, at) - tiles;
+            out.group = g0 + at;
+            out.lo = __builtin_amdgcn_readlane((int)lo, at);
+            out.hi = __builtin_amdgcn_readlane((int)hi, at);
+            grouped_coords(t - start * tiles_q, tiles, tiles_q, out.tp, out.tq);
+            return true;
+        }
+        before += __builtin_amdgcn_readlane(scan, 63);
+    }
+    return false;
+}
+
+// GeLU and its gradient in fp32, for epilogues that evaluate them: 20 instructions,
+// where erff and expf take 60 and 1 + erf loses the negative side to cancellation.
+// For x >= 0, Phi(-x) = exp(-x^2 / 2) R(t), t = 1 / (1 + 0.36 x), R(t) a polynomial
+// without a constant term fitted to erfcx(x / sqrt 2) / 2 on [0, 14] (past which the
+// exponential is below fp32), off by at most 9e-7 of the value.
+struct GeluTerms {
+    float cdf, e;  // Phi(a) and exp(-a^2 / 2)
+};
+__device__ __forceinline__ GeluTerms gelu_terms(float a) {
+    const float e = __builtin_amdgcn_exp2f(a * a * -0.72134752f);
+    const float t = __builtin_amdgcn_rcpf(fmaf(fabsf(a), 0.36f, 1.f));
+    float r = 0.047062017f;
+    r = fmaf(r, t, -0.179784372f);
+    r = fmaf(r, t, 0.180980921f);
+    r = fmaf(r, t, 0.026530694f);
+    r = fmaf(r, t, 0.139726102f);
+    r = fmaf(r, t, 0.141771197f);
+    r = fmaf(r, t, 0.143713132f);
+    const float q = e * (r * t);
+    return {a > 0.f ? 1.f - q : q, e};
+}
+__device__ __forceinline__ float gelu_f32(float a) { return a * gelu_terms(a).cdf; }
+// Phi(a) + a phi(a); the second term is zero where the exponential is, also of an infinite a.
+__device__ __forceinline__ float gelu_slope_f32(float a) {
+    const GeluTerms g = gelu_terms(a);
+    return g.cdf + (g.e > 0.f ? a * g.e * 0.39894228f : 0.f);
+}
+
 // What the epilogue of the orthogonalised update reads for four consecutive
 // elements (p, q .. q + 3) of a product; past its extents, those at its edge.
 template <int EPI>
@@ -722,6 +834,25 @@ void gemm_kernel(ARGS a, int tiles_p, int tiles_q) {
     // the reduction each.
     constexpr bool TRI = EPI == EPI_GRAM || EPI == EPI_POLY;
     constexpr bool ORTH = TRI || EPI == EPI_APPLY;
+    constexpr bool GROUPED = std::is_same<ARGS, GroupArgs>::value;
+    constexpr bool G_RED = GROUPED && Q_RS && P_RS;  // the group's rows are the reduction
+    constexpr int kPer = QB * PB <= 4 ? 128 : QB * PB <= 16 ? 64 : 32;  // workgroups an XCD runs at once
+    [[maybe_unused]] GroupTile gt;
+    if constexpr (GROUPED) {
+        if constexpr (G_RED) {
+            const int64_t each = (int64_t)tiles_p * tiles_q;
+            const int64_t t = grouped_order(w, each * a.groups, kPer);
+            if (t < 0) return;
+            gt.group = (int)(t / each);
+            grouped_coords(t - gt.group * each, tiles_p, tiles_q, gt.tp, gt.tq);
+            group_rows(a.offsets, a.total, gt.group, gt.lo, gt.hi);
+        } else {
+            if (!find_group_tile<TP>(a.offsets, a.groups, a.total, w, tiles_q, kPer, gt)) return;
+            a.rows = gt.hi;
+        }
+        gt.group = __builtin_amdgcn_readfirstlane(gt.group);
+        if constexpr (G_RED) a.C = static_cast<char *>(a.C) + gt.group * a.c_group * (EPI == EPI_LP ? 2 : 4);
+    }
     int half = -1, sj = 0;
     [[maybe_unused]] int32_t first_step = 0, steps = 0;
     if constexpr (ORTH) {
@@ -752,12 +883,30 @@ void gemm_kernel(ARGS a, int tiles_p, int tiles_q) {
     // across the main loop.)
     auto setup = [&](int wi, int ln) __attribute__((always_inline)) {
         int tp, tq;
-        if constexpr (TRI)
+        if constexpr (GROUPED) {
+            tp = gt.tp;
+            tq = gt.tq;
+        } else if constexpr (TRI)
             triangle_coords(wi, tiles_p, tp, tq);
         else
             tile_coords<(Q_RS && P_RS) ? 8 : (QB == 10 ? 1 : 4)>(wi, tiles_p, tiles_q, tp, tq);
         p0 = (int64_t)tp * TP;
         q0 = (int64_t)tq * TQ;
+        if constexpr (GROUPED) {
+            const uint16_t *q = static_cast<const uint16_t *>(a.Q), *p = static_cast<const uint16_t *>(a.P);
+            if constexpr (G_RED) {
+                q += gt.lo * a.ldq;
+                p += gt.lo * a.ldp;
+            } else {
+                q += gt.group * a.q_group;
+                p0 += gt.lo;
+            }
+            qo.init(q, a.ldq, q0, a.cols, wave, ln);
+            po.init(p, a.ldp, p0, a.rows, wave, ln);
+            qo.init_cursor();
+            po.init_cursor();
+            return;
+        }
         if constexpr (Q_RS) {
             qo.init(static_cast<const uint16_t *>(a.Q), a.ldq, q0, a.cols, wave, ln);
             qo.set_split(a.Q2, a.qsplit, q0);
@@ -803,7 +952,7 @@ void gemm_kernel(ARGS a, int tiles_p, int tiles_q) {
     // unit idles.
     // below 2^30 (the host checks); a split half runs half of it, a whole
     // number of steps (the host checks)
-    const int32_t red = ORTH ? steps * BK : (int32_t)(half >= 0 ? a.red >> 1 : a.red);
+    const int32_t red = ORTH ? steps * BK : G_RED ? (int32_t)(gt.hi - gt.lo) : (int32_t)(half >= 0 ? a.red >> 1 : a.red);
     const int64_t ksteps = (red + BK - 1) / BK;
     // slot of unit u (used for the first five units; the ring below rotates
     // from there)
@@ -1243,6 +1392,41 @@ void gemm_kernel(ARGS a, int tiles_p, int tiles_q) {
             copy16(rs, lds_addr(lds + blk * 1024), (uint32_t)(blk * 1024 + lane * 16));
         }
         asm volatile("s_waitcnt vmcnt(0)\n\ts_barrier" ::: "memory");
+    }
+    if constexpr (EPI == EPI_ACT || EPI == EPI_DACT) {
+        static_for<0, QB>([&](auto I_) __attribute__((always_inline)) {
+            constexpr int i = decltype(I_)::value;
+            const int64_t q = qb + i * 16;
+            u32x2 pre[PB];
+            if constexpr (EPI == EPI_DACT) {
+#pragma unroll
+                for (int j = 0; j < PB; ++j)  // past the edges, what lies at them
+                    pre[j] = *reinterpret_cast<const u32x2 *>(a.pre + min(pb + j * 16, a.rows - 1) * a.ldpre + min(q, a.cols - 4));
+            }
+#pragma unroll
+            for (int j = 0; j < PB; ++j) {
+                const int64_t p = pb + j * 16;
+                const f32x4 v = acc[i][j];
+                uint32_t b[4];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    if constexpr (EPI == EPI_ACT)
+                        b[e] = bits16<T>(gelu_f32(v[e]));
+                    else
+                        b[e] = bits16<T>(v[e] * gelu_slope_f32(value16<T>((pre[j][e >> 1] >> (16 * (e & 1))) & 0xffffu)));
+                }
+                if (p < a.rows && q < a.cols) {
+                    *reinterpret_cast<u32x2 *>(static_cast<uint16_t *>(a.C) + p * a.ldc + q) =
+                        u32x2{b[0] | (b[1] << 16), b[2] | (b[3] << 16)};
+                    if constexpr (EPI == EPI_ACT) {
+                        if (a.C2)
+                            *reinterpret_cast<u32x2 *>(static_cast<uint16_t *>(a.C2) + p * a.ldpre + q) =
+                                u32x2{bits16<T>(v[0]) | (bits16<T>(v[1]) << 16), bits16<T>(v[2]) | (bits16<T>(v[3]) << 16)};
+                    }
+                }
+            }
+        });
+        return;
     }
     [[maybe_unused]] const __attribute__((address_space(3))) uint16_t *gtab =
         (const __attribute__((address_space(3))) uint16_t *)(uintptr_t)lds_addr(lds);

@@ -91,6 +91,28 @@ constexpr int kOrthUnits = 256;
 constexpr int kOrthSplits = 4 * kOrthUnits;
 constexpr uint64_t orth_split_bytes(int tile) { return (uint64_t)kOrthUnits * (256 / tile) * tile * tile * 4; }
 
+// Products of many weights, each with a share of the rows (zi_grouped.hip): group g
+// has the rows [offsets[g], offsets[g + 1]) of the ragged operands.  offsets are in
+// device memory; what lies outside [0, total) is left out.
+//   Fwd   Y[r][m] = sum_k X[r][k] W_g[m][k]     (Q = W_g, P = X)
+//   Dx    dX[r][k] = sum_m dY[r][m] W_g[m][k]   (Q = W_g^T, P = dY)
+//   Dw    dW_g[m][k] = sum_r dY[r][m] X[r][k]   (Q = X^T, P = dY^T, over the group's rows)
+// In GemmArgs rows is total for Fwd and Dx, red is total for Dw.
+struct GroupArgs : GemmArgs {
+    const int32_t *offsets;  // [groups + 1]
+    int64_t total;
+    int64_t q_group;         // Fwd, Dx: elements from a group's Q to the next one's
+    int64_t c_group;         // Dw: the same of C
+    int32_t groups;
+    int32_t act;             // Fwd: C = RNE(GeLU(acc)), and C2, if any, RNE(acc)
+    const uint16_t *pre;     // Dx: C = RNE(acc GeLU'(pre)); null: without
+    int64_t ldpre;
+};
+// On macro-tiles of `tile` (256, 128, 64) rows and columns; an accumulating Dw on 256.
+hipError_t launch_grouped_fwd(int dtype, int tile, const GroupArgs &a, hipStream_t stream);
+hipError_t launch_grouped_dx(int dtype, int tile, const GroupArgs &a, hipStream_t stream);
+hipError_t launch_grouped_dw(int dtype, int tile, const GroupArgs &a, hipStream_t stream);
+
 // Workgroups (one macro-tile each) that launch_gemm runs for a product with
 // `rows` output rows and `cols` output columns: the macro-tile is 256 x 256,
 // or 192 x 320 / 320 x 192 (rows x columns) where that tile covers a forward's
@@ -116,5 +138,9 @@ constexpr int kGemmStep = 64;
 constexpr int kSplitTiles = 128;
 constexpr uint64_t kSplitPartBytes = (uint64_t)kSplitTiles * 2 * 256 * 256 * 4;
 constexpr uint64_t kSplitBytes = kSplitPartBytes + 512;
+
+
+// Largest row stride, in elements, of the 16-bit operands of the grouped products.
+constexpr int64_t kGroupLd = (int64_t)1 << 20;
 
 }  // namespace zi

@@ -117,7 +117,33 @@ class zi_orth(ctypes.Structure):
                 ("c", ctypes.c_float), ("eps", ctypes.c_float)]
 
 
+class zi_route(ctypes.Structure):
+    _fields_ = [("T", ctypes.c_int64), ("ldl", ctypes.c_int64), ("ldd", ctypes.c_int64), ("E", ctypes.c_int32),
+                ("k", ctypes.c_int32), ("dtype", ctypes.c_int32), ("normalize", ctypes.c_int32)]
+
+
+class zi_grouped(ctypes.Structure):
+    _fields_ = [("R", ctypes.c_int64), ("K", ctypes.c_int64), ("M", ctypes.c_int64), ("ldx", ctypes.c_int64),
+                ("ldy", ctypes.c_int64), ("lda", ctypes.c_int64), ("ldw", ctypes.c_int64), ("ldg", ctypes.c_int64),
+                ("E", ctypes.c_int32), ("dtype", ctypes.c_int32), ("out_dtype", ctypes.c_int32),
+                ("gelu", ctypes.c_int32), ("accumulate", ctypes.c_int32)]
+
+
+class zi_combine(ctypes.Structure):
+    _fields_ = [("T", ctypes.c_int64), ("R", ctypes.c_int64), ("D", ctypes.c_int64), ("ldz", ctypes.c_int64),
+                ("ldy", ctypes.c_int64), ("lddz", ctypes.c_int64), ("k", ctypes.c_int32), ("dtype", ctypes.c_int32)]
+
+
+class zi_adapters(ctypes.Structure):
+    _fields_ = [("T", ctypes.c_int64), ("K", ctypes.c_int64), ("M", ctypes.c_int64), ("ldx", ctypes.c_int64),
+                ("lddx", ctypes.c_int64), ("lddx0", ctypes.c_int64), ("ldy", ctypes.c_int64), ("ldy0", ctypes.c_int64),
+                ("S", ctypes.c_int32), ("N", ctypes.c_int32), ("r", ctypes.c_int32), ("dtype", ctypes.c_int32),
+                ("out_dtype", ctypes.c_int32), ("accumulate", ctypes.c_int32)]
+
+
 ZI_ORTH_MOST = 262144
+ZI_ROUTE_EXPERTS = 1024
+ZI_GROUPS_MOST = 4096
 ZI_STATS_KERNELS = 16
 
 
@@ -231,6 +257,18 @@ _sigs = {
     "zi_embedding_bwd": (_S, [ctypes.POINTER(zi_embedding), _P, _P, _P, _P, ctypes.c_uint64, _P]),
     "zi_orthogonalize_bytes": (ctypes.c_uint64, [ctypes.c_int64, ctypes.c_int64]),
     "zi_orthogonalize": (_S, [ctypes.POINTER(zi_orth), _P, _P, _P, ctypes.c_uint64, _P]),
+    "zi_route_fwd_bytes": (ctypes.c_uint64, [ctypes.c_int64, ctypes.c_int32, ctypes.c_int32]),
+    "zi_route_fwd": (_S, [ctypes.POINTER(zi_route)] + [_P] * 7 + [ctypes.c_uint64, _P]),
+    "zi_route_bwd": (_S, [ctypes.POINTER(zi_route)] + [_P] * 6),
+    "zi_grouped_fwd": (_S, [ctypes.POINTER(zi_grouped)] + [_P] * 6),
+    "zi_grouped_dx": (_S, [ctypes.POINTER(zi_grouped)] + [_P] * 6),
+    "zi_grouped_dw": (_S, [ctypes.POINTER(zi_grouped)] + [_P] * 5),
+    "zi_combine_fwd": (_S, [ctypes.POINTER(zi_combine)] + [_P] * 5),
+    "zi_combine_bwd": (_S, [ctypes.POINTER(zi_combine)] + [_P] * 7),
+    "zi_adapters_fwd_bytes": (ctypes.c_uint64, [ctypes.c_int64, ctypes.c_int32]),
+    "zi_adapters_fwd": (_S, [ctypes.POINTER(zi_adapters)] + [_P] * 10 + [ctypes.c_uint64, _P]),
+    "zi_adapters_bwd_bytes": (ctypes.c_uint64, [ctypes.c_int64, ctypes.c_int32]),
+    "zi_adapters_bwd": (_S, [ctypes.POINTER(zi_adapters)] + [_P] * 13 + [ctypes.c_uint64, _P]),
     "zi_host_alloc": (_S, [ctypes.c_uint64, ctypes.POINTER(_P)]),
     "zi_host_free": (_S, [_P]),
     "zi_last_error": (ctypes.c_char_p, []),
@@ -562,6 +600,66 @@ def zi_orthogonalize_bytes(M: int, K: int) -> int:
 def zi_orthogonalize(orth: zi_orth, G, O, workspace, workspace_bytes: int, stream=None) -> None:
     _check(_lib.zi_orthogonalize(ctypes.byref(orth), _ptr(G), _ptr(O), _ptr(workspace), int(workspace_bytes),
                                  _stream(stream)))
+
+
+def zi_route_fwd_bytes(T: int, E: int, k: int) -> int:
+    return int(_lib.zi_route_fwd_bytes(int(T), int(E), int(k)))
+
+
+def zi_route_fwd(route: zi_route, logits, ids, weights, offsets, rows, slots, workspace, workspace_bytes: int,
+                 stream=None) -> None:
+    _check(_lib.zi_route_fwd(ctypes.byref(route), _ptr(logits), _ptr(ids), _ptr(weights), _ptr(offsets), _ptr(rows),
+                             _ptr(slots), _ptr(workspace), int(workspace_bytes), _stream(stream)))
+
+
+def zi_route_bwd(route: zi_route, logits, ids, weights, dweights, dlogits, stream=None) -> None:
+    _check(_lib.zi_route_bwd(ctypes.byref(route), _ptr(logits), _ptr(ids), _ptr(weights), _ptr(dweights),
+                             _ptr(dlogits), _stream(stream)))
+
+
+def zi_grouped_fwd(grouped: zi_grouped, X, W, offsets, Y, A, stream=None) -> None:
+    _check(_lib.zi_grouped_fwd(ctypes.byref(grouped), _ptr(X), _ptr(W), _ptr(offsets), _ptr(Y), _ptr(A),
+                               _stream(stream)))
+
+
+def zi_grouped_dx(grouped: zi_grouped, dY, W, offsets, A, dX, stream=None) -> None:
+    _check(_lib.zi_grouped_dx(ctypes.byref(grouped), _ptr(dY), _ptr(W), _ptr(offsets), _ptr(A), _ptr(dX),
+                              _stream(stream)))
+
+
+def zi_grouped_dw(grouped: zi_grouped, X, dY, offsets, dW, stream=None) -> None:
+    _check(_lib.zi_grouped_dw(ctypes.byref(grouped), _ptr(X), _ptr(dY), _ptr(offsets), _ptr(dW), _stream(stream)))
+
+
+def zi_combine_fwd(combine: zi_combine, Z, slots, weights, Y, stream=None) -> None:
+    _check(_lib.zi_combine_fwd(ctypes.byref(combine), _ptr(Z), _ptr(slots), _ptr(weights), _ptr(Y), _stream(stream)))
+
+
+def zi_combine_bwd(combine: zi_combine, dY, Z, slots, weights, dZ, dweights, stream=None) -> None:
+    _check(_lib.zi_combine_bwd(ctypes.byref(combine), _ptr(dY), _ptr(Z), _ptr(slots), _ptr(weights), _ptr(dZ),
+                               _ptr(dweights), _stream(stream)))
+
+
+def zi_adapters_fwd_bytes(T: int, r: int) -> int:
+    return int(_lib.zi_adapters_fwd_bytes(int(T), int(r)))
+
+
+def zi_adapters_fwd(adapters: zi_adapters, X, A, B, offsets, ids, scales, Y0, Y, U, workspace, workspace_bytes: int,
+                    stream=None) -> None:
+    _check(_lib.zi_adapters_fwd(ctypes.byref(adapters), _ptr(X), _ptr(A), _ptr(B), _ptr(offsets), _ptr(ids),
+                                _ptr(scales), _ptr(Y0), _ptr(Y), _ptr(U), _ptr(workspace), int(workspace_bytes),
+                                _stream(stream)))
+
+
+def zi_adapters_bwd_bytes(T: int, r: int) -> int:
+    return int(_lib.zi_adapters_bwd_bytes(int(T), int(r)))
+
+
+def zi_adapters_bwd(adapters: zi_adapters, X, dY, U, A, B, offsets, ids, scales, dX0, dX, dA, dB, workspace,
+                    workspace_bytes: int, stream=None) -> None:
+    _check(_lib.zi_adapters_bwd(ctypes.byref(adapters), _ptr(X), _ptr(dY), _ptr(U), _ptr(A), _ptr(B), _ptr(offsets),
+                                _ptr(ids), _ptr(scales), _ptr(dX0), _ptr(dX), _ptr(dA), _ptr(dB), _ptr(workspace),
+                                int(workspace_bytes), _stream(stream)))
 
 
 def zi_host_alloc(nbytes: int) -> int:
