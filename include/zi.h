@@ -870,7 +870,7 @@ typedef struct {
     int64_t ldx, lddx, lddx0;        /* row strides of X, dX, dX0; 0 = K                 */
     int64_t ldy, ldy0;               /* of Y and dY, of Y0; 0 = M                        */
     int32_t S;                       /* segments: 0 .. 2^23                              */
-    int32_t N;                       /* adapters: 1 .. 65536                             */
+    int32_t N;                       /* adapters: 1 .. 65535                             */
     int32_t r;                       /* rank: 1 .. 256 (pad smaller ones with zeros)     */
     int32_t dtype;                   /* X, A, B, dY: ZI_F16 or ZI_BF16                   */
     int32_t out_dtype;               /* Y, Y0, dX, dX0: dtype or ZI_F32                  */

@@ -45,25 +45,33 @@ struct Segments {
 // hold, every row comes once.
 template <typename F>
 __device__ __forceinline__ void for_runs(const Segments &g, int b0, int b1, F &&f) {
-    // the first segment that ends past b0, by a search over 64 parts at a time
     const int lane = threadIdx.x & 63;
-    int s = 0, n = g.count;
-    while (n > 0) {
-        const int step = (n + 63) / 64, at = (lane + 1) * step - 1;
-        const bool before = at < n && g.offsets[s + at + 1] <= b0;
-        const int parts = __builtin_popcountll(__ballot(before));
-        s += parts * step;
-        n = min(step - 1, n - parts * step);
-    }
     int at = b0;
-    for (; at < b1 && s < g.count; ++s) {
-        const int lo = min(max(g.offsets[s], at), b1), hi = min(max(g.offsets[s + 1], lo), b1);
+    auto run = [&](int start, int end, int id) __attribute__((always_inline)) {
+        const int lo = min(max(start, at), b1), hi = min(max(end, lo), b1);
         if (lo > at) f(-1, at, lo);
-        if (hi > lo) {
-            const int id = g.ids[s];
-            f(id >= 0 && id < g.adapters ? id : -1, lo, hi);
-        }
+        if (hi > lo) f(id >= 0 && id < g.adapters ? id : -1, lo, hi);
         at = hi;
+    };
+    int s = 0, n = g.count;
+    if (n <= 64) {
+        // a lane a segment: one access to memory before the first run
+        const bool mine = lane < n;
+        const int start = mine ? g.offsets[lane] : 0, end = mine ? g.offsets[lane + 1] : 0, id = mine ? g.ids[lane] : -1;
+        for (uint64_t rest = __ballot(mine && end > b0 && start < b1); rest && at < b1; rest &= rest - 1) {
+            const int k = __builtin_ctzll(rest);
+            run(__builtin_amdgcn_readlane(start, k), __builtin_amdgcn_readlane(end, k), __builtin_amdgcn_readlane(id, k));
+        }
+    } else {
+        // the first segment that ends past b0, by a search over 64 parts at a time
+        while (n > 0) {
+            const int step = (n + 63) / 64, probe = (lane + 1) * step - 1;
+            const bool before = probe < n && g.offsets[s + probe + 1] <= b0;
+            const int parts = __builtin_popcountll(__ballot(before));
+            s += parts * step;
+            n = min(step - 1, n - parts * step);
+        }
+        for (; at < b1 && s < g.count; ++s) run(g.offsets[s], g.offsets[s + 1], g.ids[s]);
     }
     if (at < b1) f(-1, at, b1);
 }
@@ -160,59 +168,103 @@ __device__ __forceinline__ float u_at(const ExpandArgs &a, int rank, int row) {
     return u;
 }
 
-constexpr int kExpandRows = 64, kExpandCols = 512;
-
-// 64 rows by 128 columns a wave: per step of four ranks a lane reads eight columns of
-// one row of B_n and one value of U for each of four fragments of 16 rows; instruction
-// (i, j) gives rows 16 i + 4 (lane / 16) .. +3 of column 8 (lane % 16) + j.
-template <typename T, typename YT>
-__global__ __launch_bounds__(256) void expand_kernel(ExpandArgs a) {
+// A wave: 128 columns of a run of rows, 16 rows at a time.  Per step of four ranks a
+// lane has eight columns of one row of B_n, held in registers over the run (r <= 64:
+// HOLD of 4, 8 or 16 steps; more ranks are read again for every 16 rows), and one value
+// of U; instruction j gives rows 4 (lane / 16) .. +3 of column 8 (lane % 16) + j.  U and
+// Y0 of the next 16 rows are on their way while these are multiplied and stored.
+constexpr int kExpandCols = 512;
+template <typename T, typename YT, int HOLD>
+__global__ __launch_bounds__(256) void expand_kernel(ExpandArgs a, int block) {
+    constexpr int STEPS = HOLD > 0 ? HOLD : 16;
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, c = lane & 15, g = lane >> 4;
-    const int b0 = blockIdx.x * kExpandRows, b1 = min(b0 + kExpandRows, a.seg.rows);
+    const int b0 = blockIdx.x * block, b1 = min(b0 + block, a.seg.rows);
     const int m = blockIdx.y * kExpandCols + wave * 128 + 8 * c;
     const bool in = m < a.M;
+    const bool keeps = a.U_out && blockIdx.y == 0 && wave == 0;
     for_runs(a.seg, b0, b1, [&](int n, int lo, int hi) __attribute__((always_inline)) {
-        if (n < 0 && a.same) return;
-        f32x4 acc[4][8] = {};
-        if (n >= 0) {
-            const uint16_t *B = a.B + (int64_t)n * a.r * a.M + m;
-            const float scale = a.scales ? a.scales[n] : 1.f;
-            for (int r0 = 0; r0 < a.r; r0 += 4) {
-                const int rank = r0 + g;
-                float b[8], u[4];
+        if (n < 0) {
+            if (a.U_out && blockIdx.y == 0)
+                for (int i = threadIdx.x; i < a.r * (hi - lo); i += 256)
+                    a.U_out[(int64_t)(i / (hi - lo)) * a.seg.rows + lo + i % (hi - lo)] = 0.f;
+            if (a.same || !in) return;
+            for (int row = lo + g; row < hi; row += 4) {
+                float y[8];
+                load_y<YT>(a, row, m, y);
+                store8(static_cast<YT *>(a.Y) + row * a.ldy + m, y);
+            }
+            return;
+        }
+        const float scale = a.scales ? a.scales[n] : 1.f;
+        const uint16_t *B = a.B + (int64_t)n * a.r * a.M + m;
+        u32x4 b[STEPS];
+        auto load_b = [&](int r0) __attribute__((always_inline)) {
 #pragma unroll
-                for (int j = 0; j < 8; ++j) b[j] = 0.f;
-                if (in && rank < a.r) load8(reinterpret_cast<const T *>(B + (int64_t)rank * a.M), b);
+            for (int s = 0; s < STEPS; ++s) {
+                const int rank = r0 + 4 * s + g;
+                b[s] = u32x4{0, 0, 0, 0};
+                if (in && rank < a.r) b[s] = *reinterpret_cast<const u32x4 *>(B + (int64_t)rank * a.M);
+            }
+        };
+        auto load_u = [&](int row0, int r0, float (&u)[STEPS]) __attribute__((always_inline)) {
+            const int row = row0 + c;
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const int row = b0 + 16 * i + c;
-                    u[i] = rank < a.r && row >= lo && row < hi ? u_at(a, rank, row) : 0.f;
-                    if (a.U_out && blockIdx.y == 0 && wave == 0 && rank < a.r && row >= lo && row < hi)
-                        a.U_out[(int64_t)rank * a.seg.rows + row] = u[i];
-                    u[i] *= scale;
+            for (int s = 0; s < STEPS; ++s) {
+                const int rank = r0 + 4 * s + g;
+                u[s] = row < hi && rank < a.r ? u_at(a, rank, row) : 0.f;
+            }
+        };
+        Raw8<YT> y[2][4];
+        auto load_y0 = [&](int row0, Raw8<YT> (&out)[4]) __attribute__((always_inline)) {
+            if (!a.Y0 || !in) return;
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                out[e].load(static_cast<const YT *>(a.Y0) + min(row0 + 4 * g + e, hi - 1) * a.ldy0 + m);
+        };
+        auto rows16 = [&](int row0, float (&u)[STEPS], Raw8<YT> (&y0)[4]) __attribute__((always_inline)) {
+            f32x4 acc[8] = {};
+            for (int r0 = 0;; r0 += 4 * STEPS) {
+                if constexpr (HOLD == 0) {
+                    load_b(r0);
+                    load_u(row0, r0, u);
                 }
 #pragma unroll
-                for (int i = 0; i < 4; ++i)
+                for (int s = 0; s < STEPS; ++s) {
+                    asm volatile("" : "+v"(b[s]));  // converted anew for every 16 rows: all of B_n in fp32 would spill
+                    if (keeps && row0 + c < hi && r0 + 4 * s + g < a.r)
+                        a.U_out[(int64_t)(r0 + 4 * s + g) * a.seg.rows + row0 + c] = u[s];
+                    const float v = u[s] * scale;
 #pragma unroll
-                    for (int j = 0; j < 8; ++j) acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x4f32(u[i], b[j], acc[i][j], 0, 0, 0);
+                    for (int j = 0; j < 8; ++j)
+                        acc[j] = __builtin_amdgcn_mfma_f32_16x16x4f32(v, value16<T>((b[s][j >> 1] >> (16 * (j & 1))) & 0xffffu),
+                                                                     acc[j], 0, 0, 0);
+                }
+                if (HOLD > 0 || r0 + 4 * STEPS >= a.r) break;
             }
-        } else if (a.U_out && blockIdx.y == 0) {
-            for (int i = threadIdx.x; i < a.r * (hi - lo); i += 256)
-                a.U_out[(int64_t)(i / (hi - lo)) * a.seg.rows + lo + i % (hi - lo)] = 0.f;
-        }
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
+            if (!in) return;
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
-                const int row = b0 + 16 * i + 4 * g + e;
-                if (in && row >= lo && row < hi) {
-                    float y[8];
-                    load_y<YT>(a, row, m, y);
+                const int row = row0 + 4 * g + e;
+                float o[8];
 #pragma unroll
-                    for (int j = 0; j < 8; ++j) y[j] += acc[i][j][e];
-                    store8(static_cast<YT *>(a.Y) + row * a.ldy + m, y);
-                }
+                for (int j = 0; j < 8; ++j) o[j] = acc[j][e] + (a.Y0 ? y0[e][j] : 0.f);
+                if (row < hi) stream8(static_cast<YT *>(a.Y) + row * a.ldy + m, o);
             }
+        };
+        float u[2][STEPS];
+        if constexpr (HOLD > 0) {
+            load_b(0);
+            load_u(lo, 0, u[0]);
+        }
+        load_y0(lo, y[0]);
+        for (int row = lo; row < hi; row += 32) {
+            if constexpr (HOLD > 0) load_u(row + 16, 0, u[1]);
+            load_y0(row + 16, y[1]);
+            rows16(row, u[0], y[0]);
+            if (row + 16 >= hi) break;
+            if constexpr (HOLD > 0) load_u(row + 32, 0, u[0]);
+            load_y0(row + 32, y[0]);
+            rows16(row + 16, u[1], y[1]);
         }
     });
 }
@@ -278,17 +330,22 @@ struct GradArgs {
 };
 
 // One adapter by 128 columns by 16 F ranks a workgroup, over one split of the adapter's
-// rows; its four waves take chunks of 16 rows in turn.  Of a chunk a lane reads V at
-// rank lane % 16 of four rows and, of each of those, eight columns.
+// rows (columns first in the grid, so that every XCD gets its share of each adapter); its four waves take chunks of 16 rows in turn, the next one on its way while
+// one is multiplied.  Of a chunk a lane reads V at rank lane % 16 of four rows and, of
+// each of those, eight columns.
 template <typename T, int F>
 __global__ __launch_bounds__(256) void grad_kernel(GradArgs a) {
     __shared__ f32x4 sums[4][8][64];
     const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int c = lane & 15, g = lane >> 4;
-    const int n = blockIdx.x / a.splits, split = blockIdx.x % a.splits;
-    const int k0 = blockIdx.y * 128, r0 = blockIdx.z * (16 * F);
+    const int n = blockIdx.y / a.splits, split = blockIdx.y % a.splits;
+    const int k0 = blockIdx.x * 128, r0 = blockIdx.z * (16 * F);
     const bool in = k0 + 8 * c < a.K;
-    const uint16_t *X = a.X + k0 + 8 * c;
+    // ranks and columns past the last read the last one's values and are not stored
+    const uint16_t *X = a.X + min(k0 + 8 * c, a.K - 8);
+    const float *V[F];
+#pragma unroll
+    for (int f = 0; f < F; ++f) V[f] = a.V + (int64_t)min(r0 + 16 * f + c, a.r - 1) * a.seg.rows;
     f32x4 acc[F][8] = {};
     for (int s0 = 0; s0 < a.seg.count; s0 += 64) {
         uint64_t mine = __ballot(s0 + lane < a.seg.count && a.seg.ids[min(s0 + lane, a.seg.count - 1)] == n);
@@ -296,30 +353,46 @@ __global__ __launch_bounds__(256) void grad_kernel(GradArgs a) {
             const int s = s0 + __builtin_ctzll(mine);
             mine &= mine - 1;
             const int lo = min(max(a.seg.offsets[s], 0), a.seg.rows), hi = min(max(a.seg.offsets[s + 1], lo), a.seg.rows);
-            for (int t0 = lo + 16 * (split * 4 + wave); t0 < hi; t0 += 64 * a.splits) {
-                u32x4 x[4];
-                float v[F][4];
+            const int first = lo + 16 * (split * 4 + wave), step = 64 * a.splits;
+            u32x4 x[2][4];
+            f32x4_u v[2][F];
+            auto load = [&](int t0, u32x4 (&xs)[4], f32x4_u (&vs)[F]) __attribute__((always_inline)) {
+                const int t = t0 + 4 * g;  // this lane's four rows
+                if (t0 + 16 <= hi) {
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const int t = t0 + 4 * g + i;
-                    x[i] = u32x4{0, 0, 0, 0};
-                    if (in && t < hi) x[i] = *reinterpret_cast<const u32x4 *>(X + t * a.ldx);
+                    for (int i = 0; i < 4; ++i) xs[i] = *reinterpret_cast<const u32x4 *>(X + (t + i) * a.ldx);
 #pragma unroll
-                    for (int f = 0; f < F; ++f) {
-                        const int rank = r0 + 16 * f + c;
-                        v[f][i] = t < hi && rank < a.r ? a.V[(int64_t)rank * a.seg.rows + t] : 0.f;
+                    for (int f = 0; f < F; ++f) vs[f] = *reinterpret_cast<const f32x4_u *>(V[f] + t);
+                } else {
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        xs[i] = u32x4{0, 0, 0, 0};
+                        if (t + i < hi) xs[i] = *reinterpret_cast<const u32x4 *>(X + (t + i) * a.ldx);
+#pragma unroll
+                        for (int f = 0; f < F; ++f) vs[f][i] = t + i < hi ? V[f][t + i] : 0.f;
                     }
                 }
+            };
+            auto multiply = [&](u32x4 (&xs)[4], f32x4_u (&vs)[F]) __attribute__((always_inline)) {
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
 #pragma unroll
                     for (int j = 0; j < 8; ++j) {
-                        const float b = value16<T>((x[i][j >> 1] >> (16 * (j & 1))) & 0xffffu);
+                        const float b = value16<T>((xs[i][j >> 1] >> (16 * (j & 1))) & 0xffffu);
 #pragma unroll
                         for (int f = 0; f < F; ++f)
-                            acc[f][j] = __builtin_amdgcn_mfma_f32_16x16x4f32(v[f][i], b, acc[f][j], 0, 0, 0);
+                            acc[f][j] = __builtin_amdgcn_mfma_f32_16x16x4f32(vs[f][i], b, acc[f][j], 0, 0, 0);
                     }
                 }
+            };
+            if (first >= hi) continue;
+            load(first, x[0], v[0]);
+            for (int t0 = first; t0 < hi; t0 += 2 * step) {
+                if (t0 + step < hi) load(t0 + step, x[1], v[1]);
+                multiply(x[0], v[0]);
+                if (t0 + step >= hi) break;
+                if (t0 + 2 * step < hi) load(t0 + 2 * step, x[0], v[0]);
+                multiply(x[1], v[1]);
             }
         }
     }
@@ -366,11 +439,16 @@ __global__ __launch_bounds__(256) void sum_parts_kernel(const float *part, int p
 
 // ---- launches ------------------------------------------------------------------------------
 
-// Rows a workgroup of shrink: one where segments are of a token or so, as many as fit
-// otherwise.
+// Rows a workgroup of shrink: one where segments are of a token or so, otherwise up to
+// 64, a number of which every compute unit gets as many (20011 rows of 8192 with
+// r = 16: 135 us in blocks of 64, which leave a fifth of the second round; 32768 rows
+// with r = 32: 144 us in blocks of 64, 180 in blocks of 32, which read A_n twice as
+// often).
 int block_of(int64_t T, int64_t S) {
     const int64_t mean = T / S;
-    return mean < 4 ? 1 : mean <= 32 ? 16 : 64;
+    if (mean <= 32) return mean < 4 ? 1 : 16;
+    const int64_t rounds = ceil_div(T, 256 * 64);
+    return (int)max64(16, ceil_div(T, 256 * rounds));
 }
 // Shares of the reduction, so that a few rows still occupy the chip: at least 512
 // columns each.
@@ -379,12 +457,12 @@ int64_t parts_of(int64_t T, int64_t S, int64_t K) {
     const int64_t blocks = ceil_div(T, block_of(T, S));
     return max64(1, min64(min64(kShrinkGroups / blocks, kMostParts), K / 512));
 }
-// What any T' <= T rows take: blocks * 64 >= T.
+// What any T' <= T rows take: parts <= kShrinkGroups / blocks, and blocks * 64 >= T.
 uint64_t u_bytes(int64_t T, int64_t r) { return (uint64_t)max64(T, min64(kMostParts * T, 64 * kShrinkGroups)) * (uint64_t)r * 4; }
 uint64_t round_up(uint64_t n) { return (n + 255) / 256 * 256; }
 
 // Splits of the adapters' rows, so that a few adapters still occupy the chip.
-constexpr int64_t kGradGroups = 512;
+constexpr int64_t kGradGroups = 1024;
 int64_t splits_of(int64_t T, int64_t N, int64_t K) {
     return max64(1, min64(kGradGroups / (N * ceil_div(K, 128)), ceil_div(T, 256)));
 }
@@ -395,6 +473,10 @@ hipError_t shrink_blocks(const ShrinkArgs &a, hipStream_t s) {
     const dim3 grid((unsigned)ceil_div(a.seg.rows, a.block), (unsigned)a.parts);
     if (a.block <= 16)
         hipLaunchKernelGGL((shrink_kernel<T, QF, 1>), grid, dim3(256), 0, s, a);
+    else if (a.block <= 32)
+        hipLaunchKernelGGL((shrink_kernel<T, QF, 2>), grid, dim3(256), 0, s, a);
+    else if (a.block <= 48)
+        hipLaunchKernelGGL((shrink_kernel<T, QF, 3>), grid, dim3(256), 0, s, a);
     else
         hipLaunchKernelGGL((shrink_kernel<T, QF, 4>), grid, dim3(256), 0, s, a);
     return hipGetLastError();
@@ -407,14 +489,24 @@ hipError_t shrink(int dtype, const ShrinkArgs &a, hipStream_t s) {
     return dtype == ZI_F16 ? go(f16_t{}) : go(bf16_t{});
 }
 
+constexpr int64_t kExpandGroups = 1024;
 template <typename T, typename YT>
 hipError_t expand_typed(const ExpandArgs &a, bool rows, hipStream_t s) {
     if (rows)
         hipLaunchKernelGGL((expand_row_kernel<T, YT>), dim3((unsigned)a.seg.rows, (unsigned)ceil_div(a.M, 2048)), dim3(256), 0, s, a);
-    else
-        hipLaunchKernelGGL((expand_kernel<T, YT>),
-                           dim3((unsigned)ceil_div(a.seg.rows, kExpandRows), (unsigned)ceil_div(a.M, kExpandCols)), dim3(256), 0, s,
-                           a);
+    else {
+        const int64_t wide = ceil_div(a.M, kExpandCols);
+        int block = 128;  // rows a workgroup: fewer where the chip would not be full
+        while (block > 16 && ceil_div(a.seg.rows, block) * wide < kExpandGroups) block /= 2;
+        const dim3 grid((unsigned)ceil_div(a.seg.rows, block), (unsigned)wide);
+        auto go = [&](auto hold) {
+            hipLaunchKernelGGL((expand_kernel<T, YT, decltype(hold)::value>), grid, dim3(256), 0, s, a, block);
+        };
+        if (a.r <= 16) go(std::integral_constant<int, 4>{});
+        else if (a.r <= 32) go(std::integral_constant<int, 8>{});
+        else if (a.r <= 64) go(std::integral_constant<int, 16>{});
+        else go(std::integral_constant<int, 0>{});
+    }
     return hipGetLastError();
 }
 hipError_t expand(int dtype, int out_dtype, const ExpandArgs &a, bool rows, hipStream_t s) {
@@ -433,7 +525,7 @@ hipError_t grad(int dtype, GradArgs a, hipStream_t s) {
     auto go = [&](auto type, auto frags) {
         constexpr int F = decltype(frags)::value;
         hipLaunchKernelGGL((grad_kernel<decltype(type), F>),
-                           dim3((unsigned)(a.seg.adapters * a.splits), (unsigned)ceil_div(a.K, 128), (unsigned)ceil_div(a.r, 16 * F)),
+                           dim3((unsigned)ceil_div(a.K, 128), (unsigned)(a.seg.adapters * a.splits), (unsigned)ceil_div(a.r, 16 * F)),
                            dim3(256), 0, s, a);
         return hipGetLastError();
     };
@@ -454,7 +546,7 @@ zi_status check(const zi_adapters *p) {
     if (p->T < 0 || p->T > (1 << 23)) return fail(ZI_ERR_SHAPE, "T = %lld: 0 .. 2^23 rows", (long long)p->T);
     if (p->K < 8 || p->M < 8 || p->K % 8 || p->M % 8 || p->K > kGroupLd || p->M > kGroupLd)
         return fail(ZI_ERR_SHAPE, "K = %lld, M = %lld: multiples of 8 up to 2^20", (long long)p->K, (long long)p->M);
-    if (p->N < 1 || p->N > 65536) return fail(ZI_ERR_SHAPE, "N = %d: 1 .. 65536 adapters", p->N);
+    if (p->N < 1 || p->N > 65535) return fail(ZI_ERR_SHAPE, "N = %d: 1 .. 65535 adapters", p->N);
     if (p->r < 1 || p->r > kMostRank) return fail(ZI_ERR_SHAPE, "r = %d: 1 .. %d", p->r, kMostRank);
     if (p->S < 0 || p->S > (1 << 23)) return fail(ZI_ERR_SHAPE, "S = %d: 0 .. 2^23 segments", p->S);
     const int64_t lds[5] = {p->ldx, p->lddx, p->lddx0, p->ldy, p->ldy0};

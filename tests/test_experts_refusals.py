@@ -70,7 +70,7 @@ BAD = [
     ("zi_combine", dict(k=1025), "ZI_ERR_SHAPE"), ("zi_combine", dict(ldz=23), "ZI_ERR_SHAPE"), ("zi_combine", dict(dtype=9), "ZI_ERR_ARG"),
     ("zi_adapters", dict(T=-1), "ZI_ERR_SHAPE"), ("zi_adapters", dict(T=(1 << 23) + 1), "ZI_ERR_SHAPE"),
     ("zi_adapters", dict(K=4), "ZI_ERR_SHAPE"), ("zi_adapters", dict(M=50), "ZI_ERR_SHAPE"), ("zi_adapters", dict(N=0), "ZI_ERR_SHAPE"),
-    ("zi_adapters", dict(N=65537), "ZI_ERR_SHAPE"), ("zi_adapters", dict(r=0), "ZI_ERR_SHAPE"), ("zi_adapters", dict(r=257), "ZI_ERR_SHAPE"),
+    ("zi_adapters", dict(N=65536), "ZI_ERR_SHAPE"), ("zi_adapters", dict(r=0), "ZI_ERR_SHAPE"), ("zi_adapters", dict(r=257), "ZI_ERR_SHAPE"),
     ("zi_adapters", dict(S=-1), "ZI_ERR_SHAPE"), ("zi_adapters", dict(ldx=24), "ZI_ERR_SHAPE"), ("zi_adapters", dict(ldy=52), "ZI_ERR_SHAPE"),
     ("zi_adapters", dict(lddx=24), "ZI_ERR_SHAPE"), ("zi_adapters", dict(lddx0=-8), "ZI_ERR_SHAPE"),
     ("zi_adapters", dict(dtype=3, out_dtype=3), "ZI_ERR_ARG"), ("zi_adapters", dict(dtype=1, out_dtype=2), "ZI_ERR_ARG"),
