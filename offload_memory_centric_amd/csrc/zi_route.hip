@@ -5,10 +5,8 @@
 // few instructions a logit, so what counts is that the selection takes few
 // of them and that there are few launches:
 //   choose  L lanes share a token (8 for up to 128 experts, 64 for 1024), so a
-//           wave takes 64 / L tokens side by side; a round of the selection is a
-//           maximum over a lane's own logits, one over the L lanes, and a ballot
-//           for the lowest index.  Logits are compared as ordered integers, in
-//           which 0 stands for an expert that cannot be chosen.
+//           wave takes 64 / L tokens side by side.  Logits are compared as ordered
+//           integers, in which 0 stands for an expert that cannot be chosen.
 //   place   a stable counting sort.  A token has an expert once, so the rank of a
 //           pair among its expert's is a count of tokens: a bit mask of 128 tokens
 //           for every expert, whose bits are set in any order and counted below
@@ -34,7 +32,7 @@
 namespace zi {
 namespace {
 
-constexpr int kChooseThreads = 256, kPlaceThreads = 1024;
+constexpr int kOneThreads = 256, kThreads = 1024;  // of a workgroup that does everything; of the others
 constexpr int kMostChoices = 32;
 constexpr int kMaskTokens = 128;          // tokens of a mask: four words an expert
 constexpr int kMostBlocks = 512;
@@ -97,72 +95,148 @@ __device__ __forceinline__ void load_logits(const LT *p, int n, float (&x)[V]) {
 
 // ---- choice ------------------------------------------------------------------------------
 
-struct Chosen {
-    int32_t id[kChooseThreads / 8][kMostChoices];
-    float e[kChooseThreads / 8][kMostChoices];
+// Of each group of L lanes, which are of one wave: its lanes' maxima, how many
+// candidates it has, and those; then its choices.
+struct Pick {
+    uint32_t lo, hi;  // a candidate: ~index, key (one number, of its order); a choice: index, logit
 };
+template <int GROUPS, int L>
+struct Chosen {
+    uint32_t most[GROUPS][L];
+    uint32_t count[GROUPS];
+    __attribute__((aligned(16))) Pick pick[GROUPS][kMostChoices];
+};
+// The lanes of a wave access LDS in order; this keeps the compiler to it.
+__device__ __forceinline__ void lds_order() { __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront"); }
 
 // The choices of tokens [t0, t1), counted in hist (shared, E counts).
-template <typename LT, int L, int V>
+//
+// Of the lanes' maxima the k-th largest is a bound that at least k logits reach.  Those
+// that do, some 12 of 256 for k = 8, are gathered in LDS and ranked by counting, all
+// lanes at once.  Where there are more than kMostChoices (many equal logits), or k is
+// more than there are lanes, the choices are found one after another.  (32768 tokens,
+// 256 experts, k = 8: 19.7 us one after another, bound by instructions.)
+template <int THREADS, typename LT, int L, int V>
 __device__ __forceinline__ void choose(const LT *logits, int64_t ldl, int64_t t0, int64_t t1, int E, int k, int normalize,
-                                       int32_t *ids, float *weights, uint32_t *hist, Chosen &out) {
+                                       int32_t *ids, float *weights, uint32_t *hist, Chosen<THREADS / L, L> &lds) {
     const int lane = threadIdx.x & (L - 1), group = threadIdx.x / L;
     const int first = lane * V;  // this lane's first expert
     const int shift = (threadIdx.x & 63) & ~(L - 1);
-    for (int64_t base = t0; base < t1; base += kChooseThreads / L) {
+    Pick *pick = lds.pick[group];
+    for (int64_t base = t0; base < t1; base += THREADS / L) {
         const int64_t t = base + group;
         const int n = t < t1 ? E - first : 0;
         float x[V];
         load_logits<V>(logits + (t < t1 ? t : t0) * ldl + first, n, x);
-        uint32_t key[V], bad = 0;
+        uint32_t key[V], bad = 0, most = 0;
 #pragma unroll
         for (int v = 0; v < V; ++v) {
             key[v] = key_of(x[v]);
             bad |= x[v] != x[v] ? 1u : 0u;
+            most = key[v] > most ? key[v] : most;
         }
-        float top = 0.f, total = 0.f;
         int found = 0;
-        for (int j = 0; j < k; ++j) {
-            uint32_t m = key[0];
+        bool slow = k > L;
+        if (!slow) {
+            constexpr int PER = kMostChoices > L ? kMostChoices / L : 1;
+            lds.most[group][lane] = most;
+            if (lane == 0) lds.count[group] = 0;
 #pragma unroll
-            for (int v = 1; v < V; ++v) m = key[v] > m ? key[v] : m;
-            const uint32_t best = lanes_max<L>(m);
-            if (j == 0) top = logit_of(best);
-            const uint64_t having = __ballot(m == best) >> shift;
-            if (__ballot(best != 0) == 0) break;  // no token of the wave has another expert
-            if (best == 0) continue;
-            ++found;
-            const float e = expf(logit_of(best) - top);
-            total += e;
-            if (lane == __builtin_ctzll(having)) {
-                int at = V - 1;
+            for (int q = 0; q < PER; ++q)
+                if (lane + q * L < kMostChoices) pick[lane + q * L] = Pick{0, 0};
+            lds_order();
+            uint32_t above = 0;  // lanes with a larger maximum
 #pragma unroll
-                for (int v = V - 2; v >= 0; --v) at = key[v] == best ? v : at;
+            for (int i = 0; i < L; ++i) above += lds.most[group][i] > most ? 1u : 0u;
+            const uint32_t least = lanes<L>(above < (uint32_t)k ? most : ~0u, [](uint32_t a, uint32_t b) { return a < b ? a : b; });
+            const uint32_t bound = least > 1u ? least : 1u;
+            uint32_t mine = 0;
 #pragma unroll
-                for (int v = 0; v < V; ++v) key[v] = v == at ? 0u : key[v];
-                out.id[group][j] = first + at;
-                out.e[group][j] = e;
-                atomicAdd(hist + first + at, 1u);
+            for (int v = 0; v < V; ++v) mine += key[v] >= bound ? 1u : 0u;
+            uint32_t at = mine ? atomicAdd(&lds.count[group], mine) : 0u;
+            lds_order();
+            const uint32_t all = lds.count[group];
+            slow = __ballot(all > (uint32_t)kMostChoices) != 0;
+            if (!slow) {
+#pragma unroll
+                for (int v = 0; v < V; ++v)
+                    if (key[v] >= bound) pick[at++] = Pick{~(uint32_t)(first + v), key[v]};
+                lds_order();
+                uint64_t own[PER];
+                uint32_t rank[PER] = {};
+#pragma unroll
+                for (int q = 0; q < PER; ++q) {
+                    const Pick p = pick[(lane + q * L) & (kMostChoices - 1)];
+                    own[q] = (uint64_t)p.hi << 32 | p.lo;
+                }
+                // (entries past the last are zeros, which no candidate is below)
+                for (uint32_t j = 0; __ballot(j < all) != 0; j += 2) {
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        const Pick p = pick[j + h];
+                        const uint64_t other = (uint64_t)p.hi << 32 | p.lo;
+#pragma unroll
+                        for (int q = 0; q < PER; ++q) rank[q] += other > own[q] ? 1u : 0u;
+                    }
+                }
+                lds_order();
+#pragma unroll
+                for (int q = 0; q < PER; ++q)
+                    if (own[q] && rank[q] < (uint32_t)k && lane + q * L < kMostChoices)
+                        pick[rank[q]] = Pick{~(uint32_t)own[q], __builtin_bit_cast(uint32_t, logit_of((uint32_t)(own[q] >> 32)))};
+                found = (int)(all < (uint32_t)k ? all : (uint32_t)k);
             }
         }
-        if (!normalize) {  // over all experts
-            total = 0.f;
+        if (slow) {
+            for (int j = 0; j < k; ++j) {
+                uint32_t m = key[0];
+#pragma unroll
+                for (int v = 1; v < V; ++v) m = key[v] > m ? key[v] : m;
+                const uint32_t best = lanes_max<L>(m);
+                const uint64_t having = __ballot(m == best) >> shift;
+                if (__ballot(best != 0) == 0) break;  // no token of the wave has another expert
+                if (best == 0) continue;
+                ++found;
+                // the lowest lane that has it gives it up, its first one
+                const bool wins = lane == __builtin_ctzll(having);
+                bool still = wins;
+                int at = 0;
+#pragma unroll
+                for (int v = 0; v < V; ++v) {
+                    const bool hit = still & (key[v] == best);
+                    still = still & !hit;
+                    key[v] = hit ? 0u : key[v];
+                    at = hit ? v : at;
+                }
+                if (wins) pick[j] = Pick{(uint32_t)(first + at), __builtin_bit_cast(uint32_t, logit_of(best))};
+            }
+        }
+        lds_order();
+        const float top = found ? __builtin_bit_cast(float, pick[0].hi) : 0.f;
+        float total = 0.f;
+        if (normalize) {
+            for (int j = lane; j < found; j += L) total += expf(__builtin_bit_cast(float, pick[j].hi) - top);
+        } else {  // over all experts
 #pragma unroll
             for (int v = 0; v < V; ++v) total += v < n ? expf(x[v] - top) : 0.f;
-            total = lanes_sum<L>(total);
         }
+        total = lanes_sum<L>(total);
         if (lanes_max<L>(bad)) total = NAN;
-        // the lanes of a token are of one wave, whose LDS accesses come in order
-        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "workgroup");
         if (t < t1) {
             for (int j = lane; j < k; j += L) {
-                ids[t * k + j] = j < found ? out.id[group][j] : -1;
-                weights[t * k + j] = j < found ? out.e[group][j] / total : 0.f;
+                const bool is = j < found;
+                const int id = is ? (int)pick[j].lo : -1;
+                ids[t * k + j] = id;
+                weights[t * k + j] = is ? expf(__builtin_bit_cast(float, pick[j].hi) - top) / total : 0.f;
+                if (is) atomicAdd(hist + id, 1u);
             }
         }
-        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "workgroup");
+        lds_order();
     }
 }
+
+// Counts a row holds: a whole number of words of bytes.
+__host__ __device__ constexpr int row_of(int E) { return (E + 3) / 4 * 4; }
 
 // ---- placement ---------------------------------------------------------------------------
 
@@ -244,61 +318,95 @@ __device__ __forceinline__ void place(const int32_t *ids, int64_t t0, int64_t t1
 
 // Everything in one workgroup.
 template <typename LT, int L, int V>
-__global__ __launch_bounds__(kChooseThreads) void route_kernel(const LT *logits, int64_t ldl, int T, int E, int k, int normalize,
+__global__ __launch_bounds__(kOneThreads) void route_kernel(const LT *logits, int64_t ldl, int T, int E, int k, int normalize,
                                                                int32_t *ids, float *weights, int32_t *offsets, int32_t *rows,
                                                                int32_t *slots) {
-    __shared__ Chosen out;
-    __shared__ uint32_t hist[L * V], base[L * V], mask[4 * L * V], part[kChooseThreads / 64];
-    for (int e = threadIdx.x; e < E; e += kChooseThreads) hist[e] = 0;
+    __shared__ Chosen<kOneThreads / L, L> out;
+    __shared__ uint32_t hist[L * V], base[L * V], mask[4 * L * V], part[kOneThreads / 64];
+    for (int e = threadIdx.x; e < E; e += kOneThreads) hist[e] = 0;
     __syncthreads();
-    choose<LT, L, V>(logits, ldl, 0, T, E, k, normalize, ids, weights, hist, out);
+    choose<kOneThreads, LT, L, V>(logits, ldl, 0, T, E, k, normalize, ids, weights, hist, out);
     __threadfence_block();  // the ids are read again
     __syncthreads();
-    const int total = (int)bases_of<kChooseThreads>(hist, nullptr, E, base, offsets, part);
-    place<kChooseThreads>(ids, 0, T, E, k, base, mask, rows, slots);
-    for (int i = total + threadIdx.x; i < T * k; i += kChooseThreads) rows[i] = -1;
+    const int total = (int)bases_of<kOneThreads>(hist, nullptr, E, base, offsets, part);
+    place<kOneThreads>(ids, 0, T, E, k, base, mask, rows, slots);
+    for (int i = total + threadIdx.x; i < T * k; i += kOneThreads) rows[i] = -1;
 }
 
-// Block b: tokens [b step, (b + 1) step), its counts in counts[b][E].
+// Block b: tokens [b step, (b + 1) step), its counts in row b of counts: bytes where a
+// block has 128 tokens (every other block reads them: 256 blocks and experts in 32 bits
+// took 10.3 us, most of it for the 64 MB).
 template <typename LT, int L, int V>
-__global__ __launch_bounds__(kChooseThreads) void choose_kernel(const LT *logits, int64_t ldl, int64_t T, int64_t step, int E,
+__global__ __launch_bounds__(kThreads) void choose_kernel(const LT *logits, int64_t ldl, int64_t T, int64_t step, int E,
                                                                 int k, int normalize, int32_t *ids, float *weights,
-                                                                uint32_t *counts) {
-    __shared__ Chosen out;
+                                                                void *counts) {
+    __shared__ Chosen<kThreads / L, L> out;
     __shared__ uint32_t hist[L * V];
-    for (int e = threadIdx.x; e < E; e += kChooseThreads) hist[e] = 0;
+    for (int e = threadIdx.x; e < E; e += kThreads) hist[e] = 0;
     __syncthreads();
     const int64_t t0 = blockIdx.x * step, t1 = t0 + step < T ? t0 + step : T;
-    choose<LT, L, V>(logits, ldl, t0, t1, E, k, normalize, ids, weights, hist, out);
+    choose<kThreads, LT, L, V>(logits, ldl, t0, t1, E, k, normalize, ids, weights, hist, out);
     __syncthreads();
-    for (int e = threadIdx.x; e < E; e += kChooseThreads) counts[(int64_t)blockIdx.x * E + e] = hist[e];
+    const int64_t row = (int64_t)blockIdx.x * row_of(E);
+    for (int e = threadIdx.x; e < row_of(E); e += kThreads) {
+        const uint32_t n = e < E ? hist[e] : 0;
+        if (step == kMaskTokens) static_cast<uint8_t *>(counts)[row + e] = (uint8_t)n;
+        else static_cast<uint32_t *>(counts)[row + e] = n;
+    }
 }
 
-__global__ __launch_bounds__(kPlaceThreads) void place_kernel(const int32_t *ids, int64_t T, int64_t step, int E, int k,
-                                                              const uint32_t *counts, int32_t *offsets, int32_t *rows,
+__global__ __launch_bounds__(kThreads) void place_kernel(const int32_t *ids, int64_t T, int64_t step, int E, int k,
+                                                              const void *counts, int32_t *offsets, int32_t *rows,
                                                               int32_t *slots) {
-    __shared__ uint32_t all[1024], before[1024], base[1024], mask[4 * 1024], part[kPlaceThreads / 64];
+    __shared__ uint32_t all[1024], before[1024], base[1024], mask[4 * 1024], part[kThreads / 64];
     const int b = blockIdx.x, blocks = gridDim.x;
-    for (int e = threadIdx.x; e < E; e += kPlaceThreads) all[e] = before[e] = 0;
+    for (int e = threadIdx.x; e < E; e += kThreads) all[e] = before[e] = 0;
     __syncthreads();
-    // the threads left over by one an expert share the blocks
-    const int shares = kPlaceThreads / E, share = threadIdx.x / E, e = threadIdx.x - share * E;
+    // four experts a thread; the threads left over share the blocks
+    const int words = row_of(E) / 4, shares = kThreads / words, share = threadIdx.x / words, w = threadIdx.x - share * words;
     if (share < shares) {
-        uint32_t sum = 0, low = 0;
+        uint32_t sum[4] = {}, low[4] = {};
+        if (step == kMaskTokens) {
+            // sums of two bytes a word: a share has at most 128 of the 512 blocks (256 words
+            // at most), so they stay below 2^16
+            static_assert(kMostBlocks / (kThreads / (ZI_ROUTE_EXPERTS / 4)) * kMaskTokens < 65536, "16-bit sums");
+            uint32_t s0 = 0, s1 = 0, l0 = 0, l1 = 0;
+            const uint32_t *row = static_cast<const uint32_t *>(counts) + w;
 #pragma unroll 8
-        for (int c = share; c < blocks; c += shares) {
-            const uint32_t n = counts[(int64_t)c * E + e];
-            sum += n;
-            low += c < b ? n : 0u;
+            for (int c = share; c < blocks; c += shares) {
+                const uint32_t n = row[(int64_t)c * words], n0 = n & 0x00ff00ffu, n1 = (n >> 8) & 0x00ff00ffu;
+                s0 += n0;
+                s1 += n1;
+                l0 += c < b ? n0 : 0u;
+                l1 += c < b ? n1 : 0u;
+            }
+            sum[0] = s0 & 0xffffu, sum[1] = s1 & 0xffffu, sum[2] = s0 >> 16, sum[3] = s1 >> 16;
+            low[0] = l0 & 0xffffu, low[1] = l1 & 0xffffu, low[2] = l0 >> 16, low[3] = l1 >> 16;
+        } else {
+            const u32x4_u *row = static_cast<const u32x4_u *>(counts) + w;
+#pragma unroll 4
+            for (int c = share; c < blocks; c += shares) {
+                const u32x4_u n = row[(int64_t)c * words];
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
+                    sum[q] += n[q];
+                    low[q] += c < b ? n[q] : 0u;
+                }
+            }
         }
-        atomicAdd(all + e, sum);
-        atomicAdd(before + e, low);
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+            if (4 * w + q < E) {
+                atomicAdd(all + 4 * w + q, sum[q]);
+                atomicAdd(before + 4 * w + q, low[q]);
+            }
+        }
     }
     __syncthreads();
-    const int64_t total = bases_of<kPlaceThreads>(all, before, E, base, b == 0 ? offsets : nullptr, part);
+    const int64_t total = bases_of<kThreads>(all, before, E, base, b == 0 ? offsets : nullptr, part);
     const int64_t t0 = b * step, t1 = t0 + step < T ? t0 + step : T;
-    place<kPlaceThreads>(ids, t0, t1, E, k, base, mask, rows, slots);
-    for (int64_t i = total + (int64_t)b * kPlaceThreads + threadIdx.x; i < T * k; i += (int64_t)blocks * kPlaceThreads) rows[i] = -1;
+    place<kThreads>(ids, t0, t1, E, k, base, mask, rows, slots);
+    for (int64_t i = total + (int64_t)b * kThreads + threadIdx.x; i < T * k; i += (int64_t)blocks * kThreads) rows[i] = -1;
 }
 
 // ---- backward ----------------------------------------------------------------------------
@@ -332,16 +440,25 @@ __global__ __launch_bounds__(256) void route_bwd_kernel(const LT *logits, int64_
             scale = sum == 0.f ? 0.f : 1.f / sum;
         }
         float along = 0.f;
-        for (int j = 0; j < k; ++j) {
-            const int id = ids[t * k + j];
-            if (id < 0) continue;
-            const float d = dweights[t * k + j];
-            if constexpr (NORM) along += weights[t * k + j] * d;
+        for (int j0 = 0; j0 < k; j0 += 8) {
+            int id[8];
+            float d[8], w[8];
 #pragma unroll
-            for (int v = 0; v < V; ++v) {
-                if (id == first + v) {
-                    g[v] += d;
-                    if constexpr (NORM) p[v] = weights[t * k + j];
+            for (int j = 0; j < 8; ++j) {
+                const bool is = j0 + j < k;
+                id[j] = is ? ids[t * k + j0 + j] : -1;
+                d[j] = is ? dweights[t * k + j0 + j] : 0.f;
+                w[j] = NORM && is ? weights[t * k + j0 + j] : 0.f;
+            }
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                if (id[j] < 0) continue;
+                if constexpr (NORM) along += w[j] * d[j];
+#pragma unroll
+                for (int v = 0; v < V; ++v) {
+                    const bool hit = id[j] == first + v;
+                    g[v] += hit ? d[j] : 0.f;
+                    if constexpr (NORM) p[v] = hit ? w[j] : p[v];
                 }
             }
         }
@@ -448,23 +565,30 @@ __global__ __launch_bounds__(256) void combine_bwd_kernel(const ZT *dY, int64_t 
             if (t < T) {
                 for (int64_t v = lane; v < vecs; v += row_threads) {
                     const Vec at = D >= 8 ? vec_of(v, D) : Vec{0, 0};
-                    float d[8], z[KP][8];
+                    float d[8];
+                    Raw8<ZT> z[KP];
                     load_row(dY + t * ldy, D, at.at, d);
+                    if (D >= 8) {
 #pragma unroll
-                    for (int j = 0; j < KP; ++j) {
-#pragma unroll
-                        for (int e = 0; e < 8; ++e) z[j][e] = 0.f;
-                        if (slot[j] >= 0) load_row(Z + slot[j] * ldz, D, at.at, z[j]);
+                        for (int j = 0; j < KP; ++j)
+                            if (slot[j] >= 0) z[j].load(Z + slot[j] * ldz + at.at);
                     }
 #pragma unroll
                     for (int j = 0; j < KP; ++j) {
-                        float o[8];
+                        if (slot[j] < 0) continue;
+                        float zf[8], o[8];
+                        if (D >= 8) {
+#pragma unroll
+                            for (int e = 0; e < 8; ++e) zf[e] = z[j][e];
+                        } else {
+                            load_n(Z + slot[j] * ldz, D, zf);
+                        }
 #pragma unroll
                         for (int e = 0; e < 8; ++e) {
-                            sum[j] += e >= at.from && slot[j] >= 0 ? d[e] * z[j][e] : 0.f;
+                            sum[j] += e >= at.from ? d[e] * zf[e] : 0.f;
                             o[e] = w[j] * d[e];
                         }
-                        if (slot[j] >= 0) store_row(dZ + slot[j] * lddz, D, at.at, o);
+                        store_row(dZ + slot[j] * lddz, D, at.at, o);
                     }
                 }
             }
@@ -542,10 +666,14 @@ zi_status check(const zi_combine *c) {
     return ZI_OK;
 }
 
-// Threads that share a row: one a vector, at most a workgroup.
+// Threads that share a row: one a vector, at most a workgroup, half or a quarter of one
+// where the last turn would be emptier.
 int row_threads_of(int64_t D) {
     int n = 8;
     while (n < 256 && n * 8 < D) n *= 2;
+    const int64_t vecs = ceil_div(D, 8);
+    for (int less = 128; n == 256 && less >= 64; less /= 2)
+        if (ceil_div(vecs, less) * less * 10 < ceil_div(vecs, 256) * 256 * 9) n = less;
     return n;
 }
 
@@ -559,7 +687,7 @@ extern "C" uint64_t zi_route_fwd_bytes(int64_t T, int32_t E, int32_t k) {
     if (T <= kOneTokens || E < 1) return 0;
     // as many blocks as any smaller T has, so that what serves T serves those too
     const int64_t blocks = ceil_div(T, kMaskTokens);
-    return (uint64_t)(blocks < kMostBlocks ? blocks : kMostBlocks) * (uint64_t)E * 4;
+    return (uint64_t)(blocks < kMostBlocks ? blocks : kMostBlocks) * (uint64_t)row_of(E) * 4;
 }
 
 extern "C" zi_status zi_route_fwd(const zi_route *r, const void *logits, int32_t *ids, float *weights, int32_t *offsets,
@@ -586,18 +714,17 @@ extern "C" zi_status zi_route_fwd(const zi_route *r, const void *logits, int32_t
         return with_lanes(r->E, [&](auto lanes, auto values) {
             constexpr int L = decltype(lanes)::value, V = decltype(values)::value;
             if (r->T <= kOneTokens) {
-                hipLaunchKernelGGL((route_kernel<LT, L, V>), dim3(1), dim3(kChooseThreads), 0, s, l, ldl, (int)r->T, r->E, r->k,
+                hipLaunchKernelGGL((route_kernel<LT, L, V>), dim3(1), dim3(kOneThreads), 0, s, l, ldl, (int)r->T, r->E, r->k,
                                    r->normalize, ids, weights, offsets, rows, slots);
                 return hipGetLastError();
             }
             const int64_t step = step_of(r->T);
             const dim3 blocks((unsigned)ceil_div(r->T, step));
-            uint32_t *counts = static_cast<uint32_t *>(workspace);
-            hipLaunchKernelGGL((choose_kernel<LT, L, V>), blocks, dim3(kChooseThreads), 0, s, l, ldl, r->T, step, r->E, r->k,
-                               r->normalize, ids, weights, counts);
+            hipLaunchKernelGGL((choose_kernel<LT, L, V>), blocks, dim3(kThreads), 0, s, l, ldl, r->T, step, r->E, r->k,
+                               r->normalize, ids, weights, workspace);
             const hipError_t st = hipGetLastError();
             if (st != hipSuccess) return st;
-            hipLaunchKernelGGL(place_kernel, blocks, dim3(kPlaceThreads), 0, s, ids, r->T, step, r->E, r->k, counts, offsets, rows,
+            hipLaunchKernelGGL(place_kernel, blocks, dim3(kThreads), 0, s, ids, r->T, step, r->E, r->k, workspace, offsets, rows,
                                slots);
             return hipGetLastError();
         });
@@ -683,7 +810,8 @@ extern "C" zi_status zi_combine_bwd(const zi_combine *c, const void *dY, const v
             return hipGetLastError();
         };
         if (c->k <= 2) return go(std::integral_constant<int, 2>{});
-        return go(std::integral_constant<int, 4>{});
+        if (c->k <= 4) return go(std::integral_constant<int, 4>{});
+        return go(std::integral_constant<int, 8>{});
     });
     if (e != hipSuccess) return fail(ZI_ERR_HIP, "combination gradient: %s", hipGetErrorString(e));
     return ZI_OK;
