@@ -542,7 +542,12 @@ __global__ __launch_bounds__(256) void combine_fwd_kernel(const ZT *Z, int64_t l
     }
 }
 
-template <typename ZT, int KP>
+// KP rows of Z at a time, dY's vectors again from the caches for each pair: with rows
+// read and written side by side memory does worse (4099 tokens of 6 x 5003 fp16: 133 us
+// with two rows, 152 with four, 162 with eight; one barrier a token in place of two a
+// pair, which keep the four waves on the same rows, 146).
+constexpr int KP = 2;
+template <typename ZT>
 __global__ __launch_bounds__(256) void combine_bwd_kernel(const ZT *dY, int64_t ldy, const ZT *Z, int64_t ldz, int64_t R,
                                                           const int32_t *slots, const float *weights, int64_t T, int64_t D, int k,
                                                           int row_threads, ZT *dZ, int64_t lddz, float *dweights) {
@@ -666,14 +671,11 @@ zi_status check(const zi_combine *c) {
     return ZI_OK;
 }
 
-// Threads that share a row: one a vector, at most a workgroup, half or a quarter of one
-// where the last turn would be emptier.
+// Threads that share a row: one a vector, at most a workgroup.  (Rows of 5003 fp16 on
+// 128 threads, whose last turn is fuller, took a fifth longer in both directions.)
 int row_threads_of(int64_t D) {
     int n = 8;
     while (n < 256 && n * 8 < D) n *= 2;
-    const int64_t vecs = ceil_div(D, 8);
-    for (int less = 128; n == 256 && less >= 64; less /= 2)
-        if (ceil_div(vecs, less) * less * 10 < ceil_div(vecs, 256) * 256 * 9) n = less;
     return n;
 }
 
@@ -803,15 +805,10 @@ extern "C" zi_status zi_combine_bwd(const zi_combine *c, const void *dY, const v
     const dim3 grid((unsigned)(groups < (1 << 20) ? groups : (1 << 20)));
     const hipError_t e = with_type(c->dtype, [&](auto type) {
         using ZT = decltype(type);
-        auto go = [&](auto rows) {
-            hipLaunchKernelGGL((combine_bwd_kernel<ZT, decltype(rows)::value>), grid, dim3(256), 0, s, static_cast<const ZT *>(dY),
-                               c->ldy ? c->ldy : c->D, static_cast<const ZT *>(Z), c->ldz ? c->ldz : c->D, c->R, slots, weights, c->T,
-                               c->D, c->k, row, static_cast<ZT *>(dZ), c->lddz ? c->lddz : c->D, dweights);
-            return hipGetLastError();
-        };
-        if (c->k <= 2) return go(std::integral_constant<int, 2>{});
-        if (c->k <= 4) return go(std::integral_constant<int, 4>{});
-        return go(std::integral_constant<int, 8>{});
+        hipLaunchKernelGGL((combine_bwd_kernel<ZT>), grid, dim3(256), 0, s, static_cast<const ZT *>(dY), c->ldy ? c->ldy : c->D,
+                           static_cast<const ZT *>(Z), c->ldz ? c->ldz : c->D, c->R, slots, weights, c->T, c->D, c->k, row,
+                           static_cast<ZT *>(dZ), c->lddz ? c->lddz : c->D, dweights);
+        return hipGetLastError();
     });
     if (e != hipSuccess) return fail(ZI_ERR_HIP, "combination gradient: %s", hipGetErrorString(e));
     return ZI_OK;
