@@ -11,6 +11,7 @@
 // memory into the matrix cores' registers, past LDS.
 #include <hip/hip_runtime.h>
 #include <math.h>
+#include <stdlib.h>
 #include <stdint.h>
 
 #include "zi_gemm.h"
@@ -99,6 +100,7 @@ hipError_t few(const GroupArgs &a, int pf, hipStream_t s) {
 // round of tiles of 256 (one a unit) counts 1, of 128 (two a unit) 0.71, of 64 (four)
 // 0.62, from what a unit multiplies in each.  `groups` of the row tiles are half full.
 int tile_of(int64_t rows, int64_t cols, int64_t groups, bool ragged) {
+    if (getenv("GT")) return atoi(getenv("GT"));
     int best = 256;
     double least = 0;
     for (int tile = 256, each = 1; tile >= 64; tile /= 2, each *= 2) {
@@ -180,8 +182,8 @@ extern "C" zi_status zi_grouped_fwd(const zi_grouped *g, const void *X, const vo
     // rows of an average group with any: up to 32 the weights' bytes are what counts
     const int64_t mean = ceil_div(g->R, live);
     hipError_t e;
-    if (mean <= 32) {
-        const int pf = mean <= 8 ? 1 : mean <= 16 ? 2 : 4;
+    if (getenv("PF") ? atoi(getenv("PF")) > 0 : mean <= 32) {
+        const int pf = getenv("PF") ? atoi(getenv("PF")) : mean <= 8 ? 1 : mean <= 16 ? 2 : 4;
         e = g->dtype == ZI_F16 ? few<_Float16>(a, pf, s) : few<__bf16>(a, pf, s);
     } else {
         e = launch_grouped_fwd(g->dtype, tile_of(g->R, g->M, live, true), a, s);
