@@ -5,108 +5,48 @@
 //   dX       dX = dY W_g, with GeLU times GeLU'(A)
 //   dW       dW_g (+)= dY_g^T X_g
 // The offsets stay on the device: a workgroup finds its tile among all groups' by a
-// scan, so that nothing waits for the host.  Groups of many rows run on the MFMA
-// kernel of zi_gemm.h (256, 128 or 64 rows and columns a workgroup).  Groups of a few
-// rows, as in serving, only wait for their weights: the kernel here streams W from
-// memory into the matrix cores' registers, past LDS.
+// scan, so that nothing waits for the host.  All run on the MFMA kernel of zi_gemm.h,
+// on macro-tiles of 256, 128 or 64 rows and columns.  (Groups of a few rows, as in
+// serving, only wait for their weights.  A kernel that read W from memory into the
+// matrix cores' registers, 16 rows by 64 bytes at a time, took 33.9 us for 32 rows of
+// 64 experts, 2048 x 1408 bf16; tiles of 64, whose copies into LDS fetch whole lines of
+// 128 bytes, 26.5.)
 #include <hip/hip_runtime.h>
 #include <math.h>
-#include <stdlib.h>
 #include <stdint.h>
 
-#include "zi_gemm.h"
 #include "zi_host.h"
-#include "zi_stream.h"
+#include "zi_internal.h"
 
 namespace zi {
 namespace {
 
-// 16 PF rows of one group by 16 QF columns: four waves share the reduction, each in
-// steps of 32 (stream_product); the sums meet in LDS in a fixed order.
-template <typename T, int QF, int PF, int EPI>
-__global__ __launch_bounds__(256) void few_rows_kernel(GroupArgs a, int tiles_q) {
-    constexpr int kAhead = PF == 4 ? 2 : 4;
-    __shared__ f32x4 sums[4][QF * PF][64];
-    GroupTile gt;
-    if (!find_group_tile<16 * PF>(a.offsets, a.groups, a.total, blockIdx.x, tiles_q, 64, gt)) return;
-    const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-    const int64_t q0 = (int64_t)gt.tq * (16 * QF), p0 = gt.lo + (int64_t)gt.tp * (16 * PF);
-    const int group = __builtin_amdgcn_readfirstlane(gt.group);
-    uint32_t wo[QF], xo[PF];
-    fragment_offsets(a.cols - q0, a.ldq, wo);
-    fragment_offsets(gt.hi - p0, a.ldp, xo);
-    const int red = (int)a.red, steps = (red + 31) / 32, share = (steps + 3) / 4;
-    f32x4 acc[QF][PF] = {};
-    stream_product<T, QF, PF, kAhead>(buffer_of(static_cast<const uint16_t *>(a.Q) + group * a.q_group + q0 * a.ldq), wo,
-                                      buffer_of(static_cast<const uint16_t *>(a.P) + p0 * a.ldp), xo, wave * share,
-                                      min((wave + 1) * share, steps), red, acc);
-#pragma unroll
-    for (int i = 0; i < QF; ++i)
-#pragma unroll
-        for (int j = 0; j < PF; ++j) sums[wave][i * PF + j][lane] = acc[i][j];
-    __syncthreads();
-    for (int t = tid; t < QF * PF * 64; t += 256) {
-        const int f = t >> 6, ln = t & 63;
-        f32x4 v = sums[0][f][ln];
-#pragma unroll
-        for (int k = 1; k < 4; ++k) v += sums[k][f][ln];
-        const int64_t q = q0 + 16 * (f / PF) + 4 * (ln >> 4), p = p0 + 16 * (f % PF) + (ln & 15);
-        if (p >= gt.hi || q >= a.cols) continue;
-        const int64_t off = p * a.ldc + q;
-        if constexpr (EPI == EPI_F32) {
-            *reinterpret_cast<f32x4 *>(static_cast<float *>(a.C) + off) = v;
-        } else {
-            uint32_t b[4], h[4];
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                b[e] = bits16<T>(v[e]);
-                h[e] = EPI == EPI_ACT ? bits16<T>(gelu_f32(v[e])) : b[e];
-            }
-            *reinterpret_cast<u32x2 *>(static_cast<uint16_t *>(a.C) + off) = u32x2{h[0] | (h[1] << 16), h[2] | (h[3] << 16)};
-            if (EPI == EPI_ACT && a.C2)
-                *reinterpret_cast<u32x2 *>(static_cast<uint16_t *>(a.C2) + p * a.ldpre + q) =
-                    u32x2{b[0] | (b[1] << 16), b[2] | (b[3] << 16)};
-        }
-    }
-}
-
 int64_t ceil_div(int64_t x, int64_t y) { return (x + y - 1) / y; }
 int64_t min64(int64_t x, int64_t y) { return x < y ? x : y; }
 
-template <typename T, int QF, int PF, int EPI>
-hipError_t run_few(const GroupArgs &a, hipStream_t s) {
-    const int64_t tiles_q = ceil_div(a.cols, 16 * QF);
-    const int64_t rows = a.total / (16 * PF) + min64(a.groups, a.total);
-    const int64_t grid = ceil_div(rows * tiles_q, 8) * 8;
-    if (grid > INT32_MAX / 256) return hipErrorInvalidValue;
-    hipLaunchKernelGGL((few_rows_kernel<T, QF, PF, EPI>), dim3((unsigned)grid), dim3(256), 0, s, a, (int)tiles_q);
-    return hipGetLastError();
-}
-// 64 columns a workgroup; 16 where that leaves compute units without one.
-template <typename T, int EPI>
-hipError_t few_sized(const GroupArgs &a, int pf, hipStream_t s) {
-    const bool narrow = min64(a.groups, a.total) * ceil_div(a.cols, 64) < 256;
-    if (pf == 1) return narrow ? run_few<T, 1, 1, EPI>(a, s) : run_few<T, 4, 1, EPI>(a, s);
-    if (pf == 2) return narrow ? run_few<T, 1, 2, EPI>(a, s) : run_few<T, 4, 2, EPI>(a, s);
-    return narrow ? run_few<T, 1, 4, EPI>(a, s) : run_few<T, 4, 4, EPI>(a, s);
-}
-template <typename T>
-hipError_t few(const GroupArgs &a, int pf, hipStream_t s) {
-    if (a.act) return few_sized<T, EPI_ACT>(a, pf, s);
-    return a.out_f32 ? few_sized<T, EPI_F32>(a, pf, s) : few_sized<T, EPI_LP>(a, pf, s);
-}
-
-// The macro-tile that takes least, by rounds of workgroups on 256 compute units: a
-// round of tiles of 256 (one a unit) counts 1, of 128 (two a unit) 0.71, of 64 (four)
-// 0.62, from what a unit multiplies in each.  `groups` of the row tiles are half full.
-int tile_of(int64_t rows, int64_t cols, int64_t groups, bool ragged) {
-    if (getenv("GT")) return atoi(getenv("GT"));
+// The macro-tile that takes least, by its rounds of workgroups on 256 compute units, of
+// which each holds one tile of 256, two of 128 or four of 64.  A round takes what the
+// products of many shapes measured (us for a reduction of r thousand): 19.1 r + 14,
+// 12.6 r + 6 and 12 r + 5; a tile that has its unit to itself 16.5 r + 14, 7.4 r + 5 and
+// 6.2 r + 4.  Of a ragged operand's row tiles one a group is taken as half full.  (Over
+// 45 products of 1 to 64 groups the choice is 1.5 % slower than the best tile on
+// average; 20000 rows of 16 groups, 1024 x 1024: 74.0, 60.8 and 83.7 us forward.)
+int tile_of(int64_t rows, int64_t cols, int64_t groups, double red, bool ragged) {
+    const double r = red / 1000;
     int best = 256;
     double least = 0;
-    for (int tile = 256, each = 1; tile >= 64; tile /= 2, each *= 2) {
+    for (int tile = 256; tile >= 64; tile /= 2) {
         const double row_tiles = ragged ? (double)rows / tile + 0.5 * (double)groups : (double)ceil_div(rows, tile) * (double)groups;
-        const double rounds = ceil(row_tiles * (double)ceil_div(cols, tile) / (256.0 * each));
-        const double t = rounds * (tile == 256 ? 1.0 : tile == 128 ? 0.71 : 0.62);
+        const double each = row_tiles * (double)ceil_div(cols, tile) / 256;  // tiles a compute unit
+        double t;
+        if (tile == 256) {
+            t = each > 1 ? ceil(each - 0.05) * (19.1 * r + 14) : 16.5 * r + 14;
+        } else if (tile == 128) {
+            t = each > 1 ? fmax(1, ceil(each / 2 - 0.05)) * (12.6 * r + 6) : 7.4 * r + 5;
+        } else {
+            const double alone = 6.2 * r + 4, full = 12 * r + 5;
+            t = each > 4 ? each / 4 * full : alone + (full - alone) * fmax(0, each - 1) / 3;
+        }
         if (least == 0 || t < least) {
             best = tile;
             least = t;
@@ -178,16 +118,7 @@ extern "C" zi_status zi_grouped_fwd(const zi_grouped *g, const void *X, const vo
     a.cols = g->M;
     a.red = g->K;
     hipStream_t s = static_cast<hipStream_t>(stream);
-    const int64_t live = min64(g->E, g->R);
-    // rows of an average group with any: up to 32 the weights' bytes are what counts
-    const int64_t mean = ceil_div(g->R, live);
-    hipError_t e;
-    if (getenv("PF") ? atoi(getenv("PF")) > 0 : mean <= 32) {
-        const int pf = getenv("PF") ? atoi(getenv("PF")) : mean <= 8 ? 1 : mean <= 16 ? 2 : 4;
-        e = g->dtype == ZI_F16 ? few<_Float16>(a, pf, s) : few<__bf16>(a, pf, s);
-    } else {
-        e = launch_grouped_fwd(g->dtype, tile_of(g->R, g->M, live, true), a, s);
-    }
+    const hipError_t e = launch_grouped_fwd(g->dtype, tile_of(g->R, g->M, min64(g->E, g->R), (double)g->K, true), a, s);
     if (e != hipSuccess) return fail(ZI_ERR_HIP, "grouped forward: %s", hipGetErrorString(e));
     return ZI_OK;
 }
@@ -216,7 +147,7 @@ extern "C" zi_status zi_grouped_dx(const zi_grouped *g, const void *dY, const vo
     a.cols = g->K;
     a.red = g->M;
     hipStream_t s = static_cast<hipStream_t>(stream);
-    const hipError_t e = launch_grouped_dx(g->dtype, tile_of(g->R, g->K, min64(g->E, g->R), true), a, s);
+    const hipError_t e = launch_grouped_dx(g->dtype, tile_of(g->R, g->K, min64(g->E, g->R), (double)g->M, true), a, s);
     if (e != hipSuccess) return fail(ZI_ERR_HIP, "grouped input gradient: %s", hipGetErrorString(e));
     return ZI_OK;
 }
@@ -243,7 +174,7 @@ extern "C" zi_status zi_grouped_dw(const zi_grouped *g, const void *X, const voi
     a.red = g->R;
     a.accumulate = g->accumulate;
     hipStream_t s = static_cast<hipStream_t>(stream);
-    const hipError_t e = launch_grouped_dw(g->dtype, tile_of(g->M, g->K, g->E, false), a, s);
+    const hipError_t e = launch_grouped_dw(g->dtype, tile_of(g->M, g->K, g->E, (double)g->R / g->E, false), a, s);
     if (e != hipSuccess) return fail(ZI_ERR_HIP, "grouped weight gradient: %s", hipGetErrorString(e));
     return ZI_OK;
 }
