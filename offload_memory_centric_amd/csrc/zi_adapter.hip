@@ -10,12 +10,12 @@
 //   expand  Y from U and B, dX from dU and A      reads and writes the wide rows once
 //   grad    dA from dU and X, dB from U and dY    reads the wide rows once
 // All are bound by the bytes of the wide rows while r is small.  U is kept in fp32 and
-// multiplied as such: the fp32 matrix instruction (16 x 16 x 4, 157 TFLOP/s) is as fast
-// as HBM up to a rank of about 64 (expand) or 32 (grad), needs no second rounding of U,
-// and takes the other operand as it lies in memory: a lane's 16 bytes are eight
-// columns of one row, which go to eight instructions whose results are eight
-// consecutive columns again.  shrink's operands are 16-bit inputs, multiplied exactly
-// by the 16-bit instruction.
+// rounded nowhere.  expand multiplies it by the fp32 matrix instruction (16 x 16 x 4,
+// 157 TFLOP/s), which is as fast as HBM up to a rank of about 64 and takes the other
+// operand as it lies in memory: a lane's 16 bytes are eight columns of one row, which go
+// to eight instructions whose results are eight consecutive columns again.  grad, whose
+// reduction runs over the rows, splits it into planes of 16 bits.  shrink's operands
+// are 16-bit inputs, multiplied exactly by the 16-bit instruction.
 //
 // A row's result depends on that row and its adapter alone: segments are multiplied one
 // by one, so that an infinity or a NaN in one request or adapter reaches no other.
@@ -329,101 +329,212 @@ struct GradArgs {
     int32_t K, r, splits, accumulate;
 };
 
+// V in planes of the 16-bit type that X has, so that the 16-bit instruction multiplies
+// it: three of bf16 (24 bits, at any scale), two of fp16 (22 bits below the largest value
+// of the rank's 32 rows, which the scale 2^(15 - e) takes into [2^14, 2^15)).
+template <typename T>
+struct Planes;
+template <>
+struct Planes<bf16_t> {
+    static constexpr int N = 3;
+    static constexpr bool kScaled = false;
+};
+template <>
+struct Planes<f16_t> {
+    static constexpr int N = 2;
+    static constexpr bool kScaled = true;
+};
+template <typename T, int N>
+__device__ __forceinline__ void split_planes(const float (&v)[8], u32x4 (&out)[N]) {
+    float r[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) r[i] = v[i];
+#pragma unroll
+    for (int p = 0; p < N; ++p) {
+#pragma unroll
+        for (int h = 0; h < 4; ++h) {
+            uint32_t b[2];
+#pragma unroll
+            for (int q = 0; q < 2; ++q) {
+                b[q] = bits16<T>(r[2 * h + q]);
+                const float rest = r[2 * h + q] - value16<T>(b[q]);
+                r[2 * h + q] = fabsf(rest) < INFINITY ? rest : 0.f;  // nothing is left of an infinity or a NaN
+            }
+            out[p][h] = b[0] | (b[1] << 16);
+        }
+    }
+}
+
 // One adapter by 128 columns by 16 F ranks a workgroup, over one split of the adapter's
-// rows (columns first in the grid, so that every XCD gets its share of each adapter); its four waves take chunks of 16 rows in turn, the next one on its way while
-// one is multiplied.  Of a chunk a lane reads V at rank lane % 16 of four rows and, of
-// each of those, eight columns.
+// rows (columns first in the grid, so that every XCD gets its share of each adapter).
+// Its four waves take chunks of 32 rows in turn, each by itself: the chunk's columns are
+// copied into the wave's part of LDS (16 bytes a lane, whole rows of 256 bytes), the
+// next chunk's while this one is multiplied, and read back across the rows
+// (ds_read_b64_tr_b16); V comes to registers as eight rows of a rank a lane.  (In fp32,
+// 16 x 16 x 4 at a time, 32768 rows of 8192 with r = 32 took 183 us, 109 of them the
+// matrix cores' at their rate.)
 template <typename T, int F>
 __global__ __launch_bounds__(256) void grad_kernel(GradArgs a) {
-    __shared__ f32x4 sums[4][8][64];
+    constexpr int NP = Planes<T>::N;
+    constexpr bool kScaled = Planes<T>::kScaled;
+    constexpr int kChunk = 32, kRowB = 256, kStage = kChunk * kRowB;
+    __shared__ __attribute__((aligned(1024))) char lds[4 * 2 * kStage];
     const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int c = lane & 15, g = lane >> 4;
     const int n = blockIdx.y / a.splits, split = blockIdx.y % a.splits;
     const int k0 = blockIdx.x * 128, r0 = blockIdx.z * (16 * F);
-    const bool in = k0 + 8 * c < a.K;
-    // ranks and columns past the last read the last one's values and are not stored
-    const uint16_t *X = a.X + min(k0 + 8 * c, a.K - 8);
+    char *mine = lds + wave * (2 * kStage);
+    const uint32_t at = lds_addr(mine);
+
+    // Copy i of a chunk fills its rows 4 i .. 4 i + 3, 16 lanes a row.  The 32-byte
+    // segments of a row are permuted as in RsOperand, so that a transposing read falls
+    // on distinct banks.
+    auto swizzle = [](int row) { return (row & 3) | ((row >> 1) & 4); };
+    uint32_t xo[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        const int row = 4 * i + g, col = ((((c >> 1) ^ swizzle(row)) << 1) | (c & 1)) * 8;
+        xo[i] = k0 + col < a.K ? (uint32_t)((row * a.ldx + col) * 2) : kOOB;
+    }
+    // fragment j (16 columns): this lane's part of rows 0 .. 3 of each eight; the others are 4 rows on
+    const int kl = 8 * g + (c >> 2);
+    uint32_t fo[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) fo[j] = (uint32_t)(kl * kRowB + ((j ^ swizzle(kl)) << 5) + 8 * (c & 3));
+    // ranks past the last read the last one's values and are not stored
     const float *V[F];
 #pragma unroll
     for (int f = 0; f < F; ++f) V[f] = a.V + (int64_t)min(r0 + 16 * f + c, a.r - 1) * a.seg.rows;
+
+    // the chunks of this wave, over all segments of the adapter
+    const int step = 4 * kChunk * a.splits, first = kChunk * (split * 4 + wave);
+    int s0 = -64, hi = 0, t = -step;
+    uint64_t left = 0;
+    auto next = [&]() __attribute__((always_inline)) -> bool {
+        t += step;
+        while (t >= hi) {
+            while (!left) {
+                s0 += 64;
+                if (s0 >= a.seg.count) return false;
+                left = __ballot(s0 + lane < a.seg.count && a.seg.ids[min(s0 + lane, a.seg.count - 1)] == n);
+            }
+            const int s = s0 + __builtin_ctzll(left);
+            left &= left - 1;
+            const int lo = min(max(a.seg.offsets[s], 0), a.seg.rows);
+            hi = min(max(a.seg.offsets[s + 1], lo), a.seg.rows);
+            t = lo + first;
+        }
+        return true;
+    };
+    auto copy = [&](int stage) __attribute__((always_inline)) {
+        const rsrc_t rs = make_rsrc(reinterpret_cast<const char *>(a.X + t * a.ldx + k0));
+        if (t + kChunk <= hi) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) copy16(rs, at + stage * kStage + i * 1024, xo[i]);
+        } else {  // rows past the segment read as zero
+#pragma unroll
+            for (int i = 0; i < 8; ++i) copy16(rs, at + stage * kStage + i * 1024, t + 4 * i + g < hi ? xo[i] : kOOB);
+        }
+    };
+    float v[F][8];
+    auto load_v = [&]() __attribute__((always_inline)) {
+        const int row = t + 8 * g;
+        if (t + kChunk <= hi) {
+#pragma unroll
+            for (int f = 0; f < F; ++f) load8(V[f] + row, v[f]);
+        } else {
+#pragma unroll
+            for (int f = 0; f < F; ++f)
+#pragma unroll
+                for (int i = 0; i < 8; ++i) v[f][i] = row + i < hi ? V[f][row + i] : 0.f;
+        }
+    };
+
     f32x4 acc[F][8] = {};
-    for (int s0 = 0; s0 < a.seg.count; s0 += 64) {
-        uint64_t mine = __ballot(s0 + lane < a.seg.count && a.seg.ids[min(s0 + lane, a.seg.count - 1)] == n);
-        while (mine) {
-            const int s = s0 + __builtin_ctzll(mine);
-            mine &= mine - 1;
-            const int lo = min(max(a.seg.offsets[s], 0), a.seg.rows), hi = min(max(a.seg.offsets[s + 1], lo), a.seg.rows);
-            const int first = lo + 16 * (split * 4 + wave), step = 64 * a.splits;
-            u32x4 x[2][4];
-            f32x4_u v[2][F];
-            auto load = [&](int t0, u32x4 (&xs)[4], f32x4_u (&vs)[F]) __attribute__((always_inline)) {
-                const int t = t0 + 4 * g;  // this lane's four rows
-                if (t0 + 16 <= hi) {
+    int stage = 0;
+    bool more = next();
+    if (more) {
+        copy(0);
+        load_v();
+    }
+    while (more) {
+        // this chunk is in LDS, its V in registers
+        asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+        u32x4 pl[F][NP];
+        [[maybe_unused]] float unscale[F][4];
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) xs[i] = *reinterpret_cast<const u32x4 *>(X + (t + i) * a.ldx);
+        for (int f = 0; f < F; ++f) {
+            if constexpr (kScaled) {
+                float most = 0.f;
 #pragma unroll
-                    for (int f = 0; f < F; ++f) vs[f] = *reinterpret_cast<const f32x4_u *>(V[f] + t);
+                for (int i = 0; i < 8; ++i) most = fmaxf(most, fabsf(v[f][i]));
+                most = fmaxf(most, __shfl_xor(most, 16, 64));
+                most = fmaxf(most, __shfl_xor(most, 32, 64));
+                const int e = max(__builtin_amdgcn_frexp_expf(most), -110);
+#pragma unroll
+                for (int i = 0; i < 8; ++i) v[f][i] = ldexpf(v[f][i], 15 - e);
+                const float back = ldexpf(1.f, e - 15);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) unscale[f][i] = __shfl(back, 4 * g + i, 64);
+            }
+            split_planes<T>(v[f], pl[f]);
+        }
+        more = next();
+        if (more) {
+            copy(stage ^ 1);
+            load_v();
+        }
+        const uint32_t base = at + stage * kStage;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            const s16x4 x0 =
+                __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) s16x4 *)(uintptr_t)(base + fo[j]));
+            const s16x4 x1 = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+                (__attribute__((address_space(3))) s16x4 *)(uintptr_t)(base + fo[j] + 4 * kRowB));
+            const u32x2 w0 = __builtin_bit_cast(u32x2, x0), w1 = __builtin_bit_cast(u32x2, x1);
+            const u32x4 x = {w0[0], w0[1], w1[0], w1[1]};
+#pragma unroll
+            for (int f = 0; f < F; ++f) {
+                if constexpr (kScaled) {
+                    f32x4 part = {};
+#pragma unroll
+                    for (int p = 0; p < NP; ++p) part = mfma<_Float16>(pl[f][p], x, part);
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) acc[f][j][e] += part[e] * unscale[f][e];
                 } else {
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        xs[i] = u32x4{0, 0, 0, 0};
-                        if (t + i < hi) xs[i] = *reinterpret_cast<const u32x4 *>(X + (t + i) * a.ldx);
-#pragma unroll
-                        for (int f = 0; f < F; ++f) vs[f][i] = t + i < hi ? V[f][t + i] : 0.f;
-                    }
+                    for (int p = 0; p < NP; ++p) acc[f][j] = mfma<__bf16>(pl[f][p], x, acc[f][j]);
                 }
-            };
-            auto multiply = [&](u32x4 (&xs)[4], f32x4_u (&vs)[F]) __attribute__((always_inline)) {
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-#pragma unroll
-                    for (int j = 0; j < 8; ++j) {
-                        const float b = value16<T>((xs[i][j >> 1] >> (16 * (j & 1))) & 0xffffu);
-#pragma unroll
-                        for (int f = 0; f < F; ++f)
-                            acc[f][j] = __builtin_amdgcn_mfma_f32_16x16x4f32(vs[f][i], b, acc[f][j], 0, 0, 0);
-                    }
-                }
-            };
-            if (first >= hi) continue;
-            load(first, x[0], v[0]);
-            for (int t0 = first; t0 < hi; t0 += 2 * step) {
-                if (t0 + step < hi) load(t0 + step, x[1], v[1]);
-                multiply(x[0], v[0]);
-                if (t0 + step >= hi) break;
-                if (t0 + 2 * step < hi) load(t0 + 2 * step, x[0], v[0]);
-                multiply(x[1], v[1]);
             }
         }
+        stage ^= 1;
     }
+    __builtin_amdgcn_sched_barrier(0);
+    asm volatile("s_nop 7\n\ts_nop 7" ::: "memory");  // the last products, before anything reads the sums
+
+    // the four waves' sums meet in LDS, one fragment of ranks at a time
     const float scale = a.scales ? a.scales[n] : 1.f;
     const bool whole = a.splits == 1;
     float *out = (whole ? a.G : a.part + (int64_t)split * a.seg.adapters * a.r * a.K) + (int64_t)n * a.r * a.K;
+    f32x4(*sums)[8][64] = reinterpret_cast<f32x4(*)[8][64]>(lds);
 #pragma unroll
     for (int f = 0; f < F; ++f) {
         __syncthreads();
 #pragma unroll
         for (int j = 0; j < 8; ++j) sums[wave][j][lane] = acc[f][j];
         __syncthreads();
-        // thread (lane, wave): row 4 (lane / 16) + wave of the fragment, eight columns
-        float v[8];
+        // thread (lane, wave): rank 4 (lane / 16) + wave of the fragment, columns 16 j + lane % 16
+        const int rank = r0 + 16 * f + 4 * g + wave;
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
-            v[j] = sums[0][j][lane][wave];
+            float sum = sums[0][j][lane][wave];
 #pragma unroll
-            for (int k = 1; k < 4; ++k) v[j] += sums[k][j][lane][wave];
-            v[j] *= scale;
-        }
-        const int rank = r0 + 16 * f + 4 * g + wave;
-        if (in && rank < a.r) {
-            float *p = out + (int64_t)rank * a.K + k0 + 8 * c;
-            if (whole && a.accumulate) {
-                float old[8];
-                load8(p, old);
-#pragma unroll
-                for (int j = 0; j < 8; ++j) v[j] += old[j];
+            for (int k = 1; k < 4; ++k) sum += sums[k][j][lane][wave];
+            const int col = k0 + 16 * j + c;
+            if (col < a.K && rank < a.r) {
+                float *p = out + (int64_t)rank * a.K + col;
+                *p = (whole && a.accumulate ? *p : 0.f) + sum * scale;
             }
-            store8(p, v);
         }
     }
 }
