@@ -87,11 +87,17 @@ struct ShrinkArgs {
     int32_t K, r, block, parts;  // rows a workgroup; shares of the reduction
 };
 
-// A workgroup: `block` rows (at most 16 PF) by 16 QF ranks at a time, one part of the
-// reduction, which its four waves share.
-template <typename T, int QF, int PF>
+__device__ __forceinline__ void zero_u(float *U, int r, int ld, int lo, int hi) {
+    const int rows = hi - lo;
+    for (int i = threadIdx.x; i < r * rows; i += 256) U[(int64_t)(i / rows) * ld + lo + i % rows] = 0.f;
+}
+
+// For a few rows each: `block` rows (at most 16) by 16 QF ranks at a time a workgroup,
+// one part of the reduction, which its four waves share.
+template <typename T, int QF>
 __global__ __launch_bounds__(256) void shrink_kernel(ShrinkArgs a) {
-    __shared__ f32x4 sums[4][QF * PF][64];
+    constexpr int PF = 1;
+    __shared__ f32x4 sums[4][QF][64];
     const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int b0 = blockIdx.x * a.block, b1 = min(b0 + a.block, a.seg.rows);
     const int steps = (a.K + 31) / 32;
@@ -99,11 +105,7 @@ __global__ __launch_bounds__(256) void shrink_kernel(ShrinkArgs a) {
     const int share = (to - from + 3) / 4, s0 = from + wave * share, s1 = min(s0 + share, to);
     float *U = a.U + (int64_t)blockIdx.y * a.r * a.seg.rows;
     for_runs(a.seg, b0, b1, [&](int n, int lo, int hi) __attribute__((always_inline)) {
-        if (n < 0) {
-            const int rows = hi - lo;
-            for (int i = tid; i < a.r * rows; i += 256) U[(int64_t)(i / rows) * a.seg.rows + lo + i % rows] = 0.f;
-            return;
-        }
+        if (n < 0) return zero_u(U, a.r, a.seg.rows, lo, hi);
         const float scale = a.scales ? a.scales[n] : 1.f;
         uint32_t xo[PF];
         fragment_offsets(hi - lo, a.ldx, xo);
@@ -111,7 +113,7 @@ __global__ __launch_bounds__(256) void shrink_kernel(ShrinkArgs a) {
             uint32_t ao[QF];
             fragment_offsets(a.r - r0, a.K, ao);
             f32x4 acc[QF][PF] = {};
-            stream_product<T, QF, PF, (QF * PF > 8 ? 2 : 4)>(buffer_of(a.A + ((int64_t)n * a.r + r0) * a.K), ao,
+            stream_product<T, QF, PF, 4>(buffer_of(a.A + ((int64_t)n * a.r + r0) * a.K), ao,
                                                              buffer_of(a.X + lo * a.ldx), xo, s0, s1, a.K, acc);
 #pragma unroll
             for (int i = 0; i < QF; ++i)
@@ -131,6 +133,104 @@ __global__ __launch_bounds__(256) void shrink_kernel(ShrinkArgs a) {
                 }
             }
             __syncthreads();
+        }
+    });
+}
+
+// For many rows: 64 a workgroup, 16 a wave, by 16 QF ranks at a time.  X and A_n are
+// copied into LDS in steps of 64 reduction values (whole lines of 128 bytes, as
+// RcOperand's), DEPTH steps at a time; a wave copies its own rows of X and a quarter of
+// A_n's.  (Reading fragments of 16 rows by 64 bytes straight into registers, 32768 rows
+// of 8192 took 148 us with r = 32, 20011 rows 95 with r = 16.)
+template <typename T, int QF>
+__global__ __launch_bounds__(256) void shrink_block_kernel(ShrinkArgs a) {
+    constexpr int DEPTH = QF == 1 ? 6 : QF == 2 ? 5 : 4;
+    constexpr int XB = 64 * 128, AB = 16 * QF * 128, STAGE = XB + AB;
+    constexpr int NA = QF <= 2 ? 1 : QF / 2;  // copies of A_n a wave and step (half a copy with QF = 1)
+    constexpr int NC = 2 + NA;
+    __shared__ __attribute__((aligned(1024))) char lds[DEPTH * STAGE];
+    const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int c = lane & 15, g = lane >> 4;
+    const int b0 = blockIdx.x * a.block, b1 = min(b0 + a.block, a.seg.rows);
+    const int all = (a.K + 63) / 64;
+    const int from = (int)((int64_t)all * blockIdx.y / a.parts), steps = (int)((int64_t)all * (blockIdx.y + 1) / a.parts) - from;
+    float *U = a.U + (int64_t)blockIdx.y * a.r * a.seg.rows;
+    const uint32_t at = lds_addr(lds);
+    // Each workgroup begins at another step: where rows are a power of two apart, the
+    // same columns of all rows lie in few of the memory's channels.
+    const int turn = (int)((int64_t)steps * blockIdx.x / gridDim.x);
+    // a copy is 8 rows of 128 bytes: lane l has chunk (l % 8) ^ (row / 2 % 8) of row l / 8
+    const int row8 = lane >> 3, a_first = QF == 1 ? wave * 4 : wave * 8 * NA;
+    uint32_t xf[2], af[2];  // this lane's fragments of the two halves of a step, within a stage
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+        const int slot = (4 * h + g) ^ ((c >> 1) & 7);
+        xf[h] = (uint32_t)((16 * wave + c) * 128 + slot * 16);
+        af[h] = (uint32_t)(XB + c * 128 + slot * 16);
+    }
+    for_runs(a.seg, b0, b1, [&](int n, int lo, int hi) __attribute__((always_inline)) {
+        if (n < 0) return zero_u(U, a.r, a.seg.rows, lo, hi);
+        const float scale = a.scales ? a.scales[n] : 1.f;
+        const int mine = lo + 16 * wave;  // this wave's rows
+        for (int r0 = 0; r0 < a.r; r0 += 16 * QF) {
+            uint32_t xo[2], ao[NA], xk[2], ak[NA];  // offsets of a lane's copies, and their first reduction values
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                const int row = 8 * j + row8;
+                xk[j] = (uint32_t)(((lane & 7) ^ ((row >> 1) & 7)) * 8);
+                xo[j] = mine + row < hi ? (uint32_t)((row * a.ldx + xk[j]) * 2) : kOOB;
+            }
+#pragma unroll
+            for (int j = 0; j < NA; ++j) {
+                const int row = a_first + 8 * j + row8;
+                ak[j] = (uint32_t)(((lane & 7) ^ ((row >> 1) & 7)) * 8);
+                ao[j] = r0 + row < a.r ? (uint32_t)(((int64_t)row * a.K + ak[j]) * 2) : kOOB;
+            }
+            const rsrc_t xr = make_rsrc(reinterpret_cast<const char *>(a.X + (mine < hi ? mine : lo) * a.ldx));
+            const rsrc_t ar = make_rsrc(reinterpret_cast<const char *>(a.A + ((int64_t)n * a.r + r0) * a.K));
+            auto issue = [&](int s) __attribute__((always_inline)) {  // past the last step: zeros
+                const uint32_t stage = at + (uint32_t)(s % DEPTH) * STAGE;
+                const int turned = s + turn < steps ? s + turn : s + turn - steps;
+                const uint32_t k0 = s < steps ? (uint32_t)(from + turned) * 64 : (uint32_t)a.K;
+                const uint32_t left = (uint32_t)a.K - k0;
+#pragma unroll
+                for (int j = 0; j < 2; ++j) copy16(xr, stage + wave * 2048 + j * 1024, xk[j] < left ? xo[j] + k0 * 2 : kOOB);
+                if constexpr (QF == 1) {
+                    if (lane < 32) copy16(ar, stage + XB + wave * 512, ak[0] < left ? ao[0] + k0 * 2 : kOOB);
+                } else {
+#pragma unroll
+                    for (int j = 0; j < NA; ++j)
+                        copy16(ar, stage + XB + (wave * NA + j) * 1024, ak[j] < left ? ao[j] + k0 * 2 : kOOB);
+                }
+            };
+            f32x4 acc[QF] = {};
+#pragma unroll
+            for (int s = 0; s < DEPTH - 1; ++s) issue(s);
+            for (int s = 0; s < steps; ++s) {
+                // step s has landed, and every wave has read step s - 1
+                asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"((DEPTH - 2) * NC) : "memory");
+                issue(s + DEPTH - 1);
+                const uint32_t stage = at + (uint32_t)(s % DEPTH) * STAGE;
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    const u32x4 x = *reinterpret_cast<const __attribute__((address_space(3))) u32x4 *>((uintptr_t)(stage + xf[h]));
+#pragma unroll
+                    for (int i = 0; i < QF; ++i)
+                        acc[i] = mfma<T>(
+                            *reinterpret_cast<const __attribute__((address_space(3))) u32x4 *>((uintptr_t)(stage + af[h] + i * 2048)), x,
+                            acc[i]);
+                }
+            }
+            // every copy has landed and every read returned, before LDS is filled again
+            __builtin_amdgcn_sched_barrier(0);
+            asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier\n\ts_nop 7\n\ts_nop 7" ::: "memory");
+#pragma unroll
+            for (int i = 0; i < QF; ++i)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const int rank = r0 + 16 * i + 4 * g + e, row = mine + c;
+                    if (rank < a.r && row < hi) U[(int64_t)rank * a.seg.rows + row] = acc[i][e] * scale;
+                }
         }
     });
 }
@@ -550,16 +650,10 @@ __global__ __launch_bounds__(256) void sum_parts_kernel(const float *part, int p
 
 // ---- launches ------------------------------------------------------------------------------
 
-// Rows a workgroup of shrink: one where segments are of a token or so, otherwise up to
-// 64, a number of which every compute unit gets as many (20011 rows of 8192 with
-// r = 16: 135 us in blocks of 64, which leave a fifth of the second round; 32768 rows
-// with r = 32: 144 us in blocks of 64, 180 in blocks of 32, which read A_n twice as
-// often).
+// Rows a workgroup of shrink: one where segments are of a token or so.
 int block_of(int64_t T, int64_t S) {
     const int64_t mean = T / S;
-    if (mean <= 32) return mean < 4 ? 1 : 16;
-    const int64_t rounds = ceil_div(T, 256 * 64);
-    return (int)max64(16, ceil_div(T, 256 * rounds));
+    return mean < 4 ? 1 : mean <= 32 ? 16 : 64;
 }
 // Shares of the reduction, so that a few rows still occupy the chip: at least 512
 // columns each.
@@ -573,7 +667,7 @@ uint64_t u_bytes(int64_t T, int64_t r) { return (uint64_t)max64(T, min64(kMostPa
 uint64_t round_up(uint64_t n) { return (n + 255) / 256 * 256; }
 
 // Splits of the adapters' rows, so that a few adapters still occupy the chip.
-constexpr int64_t kGradGroups = 1024;
+constexpr int64_t kGradGroups = 512;
 int64_t splits_of(int64_t T, int64_t N, int64_t K) {
     return max64(1, min64(kGradGroups / (N * ceil_div(K, 128)), ceil_div(T, 256)));
 }
@@ -583,13 +677,9 @@ template <typename T, int QF>
 hipError_t shrink_blocks(const ShrinkArgs &a, hipStream_t s) {
     const dim3 grid((unsigned)ceil_div(a.seg.rows, a.block), (unsigned)a.parts);
     if (a.block <= 16)
-        hipLaunchKernelGGL((shrink_kernel<T, QF, 1>), grid, dim3(256), 0, s, a);
-    else if (a.block <= 32)
-        hipLaunchKernelGGL((shrink_kernel<T, QF, 2>), grid, dim3(256), 0, s, a);
-    else if (a.block <= 48)
-        hipLaunchKernelGGL((shrink_kernel<T, QF, 3>), grid, dim3(256), 0, s, a);
+        hipLaunchKernelGGL((shrink_kernel<T, QF>), grid, dim3(256), 0, s, a);
     else
-        hipLaunchKernelGGL((shrink_kernel<T, QF, 4>), grid, dim3(256), 0, s, a);
+        hipLaunchKernelGGL((shrink_block_kernel<T, QF>), grid, dim3(256), 0, s, a);
     return hipGetLastError();
 }
 hipError_t shrink(int dtype, const ShrinkArgs &a, hipStream_t s) {
