@@ -33,6 +33,7 @@ namespace {
 int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 int64_t min64(int64_t a, int64_t b) { return a < b ? a : b; }
 int64_t max64(int64_t a, int64_t b) { return a > b ? a : b; }
+uint64_t round_up(uint64_t n) { return (n + 255) / 256 * 256; }
 
 struct Segments {
     const int32_t *offsets;  // [count + 1]
@@ -238,7 +239,7 @@ __global__ __launch_bounds__(256) void shrink_block_kernel(ShrinkArgs a) {
 // ---- expand --------------------------------------------------------------------------------
 
 struct ExpandArgs {
-    const float *U;       // [parts][r][T]
+    const float *U;       // [parts][r][T]; parts and U_out: of expand_row_kernel
     float *U_out;         // the parts' sum, or null
     const uint16_t *B;    // [N][r][M]
     const float *scales;  // null: one
@@ -281,12 +282,8 @@ __global__ __launch_bounds__(256) void expand_kernel(ExpandArgs a, int block) {
     const int b0 = blockIdx.x * block, b1 = min(b0 + block, a.seg.rows);
     const int m = blockIdx.y * kExpandCols + wave * 128 + 8 * c;
     const bool in = m < a.M;
-    const bool keeps = a.U_out && blockIdx.y == 0 && wave == 0;
     for_runs(a.seg, b0, b1, [&](int n, int lo, int hi) __attribute__((always_inline)) {
         if (n < 0) {
-            if (a.U_out && blockIdx.y == 0)
-                for (int i = threadIdx.x; i < a.r * (hi - lo); i += 256)
-                    a.U_out[(int64_t)(i / (hi - lo)) * a.seg.rows + lo + i % (hi - lo)] = 0.f;
             if (a.same || !in) return;
             for (int row = lo + g; row < hi; row += 4) {
                 float y[8];
@@ -311,7 +308,7 @@ __global__ __launch_bounds__(256) void expand_kernel(ExpandArgs a, int block) {
 #pragma unroll
             for (int s = 0; s < STEPS; ++s) {
                 const int rank = r0 + 4 * s + g;
-                u[s] = row < hi && rank < a.r ? u_at(a, rank, row) : 0.f;
+                u[s] = row < hi && rank < a.r ? a.U[(int64_t)rank * a.seg.rows + row] : 0.f;
             }
         };
         Raw8<YT> y[2][4];
@@ -331,8 +328,6 @@ __global__ __launch_bounds__(256) void expand_kernel(ExpandArgs a, int block) {
 #pragma unroll
                 for (int s = 0; s < STEPS; ++s) {
                     asm volatile("" : "+v"(b[s]));  // converted anew for every 16 rows: all of B_n in fp32 would spill
-                    if (keeps && row0 + c < hi && r0 + 4 * s + g < a.r)
-                        a.U_out[(int64_t)(r0 + 4 * s + g) * a.seg.rows + row0 + c] = u[s];
                     const float v = u[s] * scale;
 #pragma unroll
                     for (int j = 0; j < 8; ++j)
@@ -641,11 +636,21 @@ __global__ __launch_bounds__(256) void grad_kernel(GradArgs a) {
 
 // out[i] (+)= the sum of part[p][i] over the parts, in order.
 __global__ __launch_bounds__(256) void sum_parts_kernel(const float *part, int parts, int64_t n, float *out, int accumulate) {
-    for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < n; i += (int64_t)gridDim.x * 256) {
-        float v = part[i];
-        for (int p = 1; p < parts; ++p) v += part[p * n + i];
-        out[i] = accumulate ? out[i] + v : v;
+    const int64_t i = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 8;
+    const int64_t left = n - i;
+    float sum[8], v[8];
+    load_n(part + i, left, sum);
+    for (int p = 1; p < parts; ++p) {
+        load_n(part + p * n + i, left, v);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) sum[e] += v[e];
     }
+    if (accumulate) {
+        load_n(out + i, left, v);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) sum[e] = v[e] + sum[e];
+    }
+    store_n(out + i, left, sum);
 }
 
 // ---- launches ------------------------------------------------------------------------------
@@ -655,16 +660,17 @@ int block_of(int64_t T, int64_t S) {
     const int64_t mean = T / S;
     return mean < 4 ? 1 : mean <= 32 ? 16 : 64;
 }
-// Shares of the reduction, so that a few rows still occupy the chip: at least 512
-// columns each.
-constexpr int64_t kShrinkGroups = 512, kMostParts = 16;
+// Shares of the reduction, so that a few rows still occupy the chip, and a block that
+// takes two passes, where segments meet, holds up little: at least 512 columns each.
+// (20011 rows of 8192 in 29 segments, 313 blocks: 101 us in one share, 76 in three.)
+constexpr int64_t kMostParts = 16;
 int64_t parts_of(int64_t T, int64_t S, int64_t K) {
-    const int64_t blocks = ceil_div(T, block_of(T, S));
-    return max64(1, min64(min64(kShrinkGroups / blocks, kMostParts), K / 512));
+    const int64_t block = block_of(T, S), groups = block == 1 ? 512 : 1024;
+    return max64(1, min64(min64(groups / ceil_div(T, block), kMostParts), K / 512));
 }
-// What any T' <= T rows take: parts <= kShrinkGroups / blocks, and blocks * 64 >= T.
-uint64_t u_bytes(int64_t T, int64_t r) { return (uint64_t)max64(T, min64(kMostParts * T, 64 * kShrinkGroups)) * (uint64_t)r * 4; }
-uint64_t round_up(uint64_t n) { return (n + 255) / 256 * 256; }
+// The shares' sums for T or any fewer rows (of blocks of at most 64).
+uint64_t parts_bytes(int64_t T, int64_t r) { return round_up((uint64_t)max64(T, min64(kMostParts * T, 64 * 1024)) * (uint64_t)r * 4); }
+uint64_t u_bytes(int64_t T, int64_t r) { return round_up((uint64_t)T * (uint64_t)r * 4); }
 
 // Splits of the adapters' rows, so that a few adapters still occupy the chip.
 constexpr int64_t kGradGroups = 512;
@@ -716,7 +722,7 @@ hipError_t expand(int dtype, int out_dtype, const ExpandArgs &a, bool rows, hipS
 }
 
 hipError_t sum_parts(const float *part, int64_t parts, int64_t n, float *out, int accumulate, hipStream_t s) {
-    hipLaunchKernelGGL(sum_parts_kernel, dim3((unsigned)min64(ceil_div(n, 256), 4096)), dim3(256), 0, s, part, (int)parts, n, out,
+    hipLaunchKernelGGL(sum_parts_kernel, dim3((unsigned)ceil_div(n, 2048)), dim3(256), 0, s, part, (int)parts, n, out,
                        accumulate);
     return hipGetLastError();
 }
@@ -776,7 +782,7 @@ Segments segments_of(const zi_adapters *p, const int32_t *offsets, const int32_t
 
 using namespace zi;
 
-extern "C" uint64_t zi_adapters_fwd_bytes(int64_t T, int32_t r) { return T < 1 || r < 1 ? 0 : round_up(u_bytes(T, r)); }
+extern "C" uint64_t zi_adapters_fwd_bytes(int64_t T, int32_t r) { return T < 1 || r < 1 ? 0 : parts_bytes(T, r) + u_bytes(T, r); }
 
 extern "C" zi_status zi_adapters_fwd(const zi_adapters *p, const void *X, const void *A, const void *B, const int32_t *offsets,
                                      const int32_t *ids, const float *scales, const void *Y0, void *Y, float *U, void *workspace,
@@ -793,23 +799,25 @@ extern "C" zi_status zi_adapters_fwd(const zi_adapters *p, const void *X, const 
     if ((st = check_work(zi_adapters_fwd_bytes(p->T, p->r), workspace, workspace_bytes)) != ZI_OK) return st;
     hipStream_t s = static_cast<hipStream_t>(stream);
     const int64_t S = max64(p->S, 1), parts = parts_of(p->T, S, p->K);
-    float *u = parts == 1 && U ? U : static_cast<float *>(workspace);
-    const int block = block_of(p->T, S);
+    char *work = static_cast<char *>(workspace);
+    float *parted = reinterpret_cast<float *>(work), *u = U ? U : reinterpret_cast<float *>(work + parts_bytes(p->T, p->r));
     ShrinkArgs a = {};
     a.X = static_cast<const uint16_t *>(X);
     a.A = static_cast<const uint16_t *>(A);
     a.ldx = p->ldx ? p->ldx : p->K;
-    a.U = u;
+    a.U = parts > 1 ? parted : u;
     a.seg = segments_of(p, offsets, ids);
     a.K = (int32_t)p->K;
     a.r = p->r;
-    a.block = block;
+    a.block = block_of(p->T, S);
     a.parts = (int32_t)parts;
+    const bool rows = a.block == 1;  // a workgroup of expand a row, which adds the parts
     hipError_t e = shrink(p->dtype, a, s);
+    if (e == hipSuccess && parts > 1 && !rows) e = sum_parts(parted, parts, p->T * p->r, u, 0, s);
     if (e == hipSuccess) {
         ExpandArgs b = {};
-        b.U = u;
-        b.U_out = parts > 1 ? U : nullptr;
+        b.U = rows ? a.U : u;
+        b.U_out = rows && parts > 1 ? U : nullptr;
         b.B = static_cast<const uint16_t *>(B);
         b.scales = scales;
         b.Y0 = Y0;
@@ -819,16 +827,16 @@ extern "C" zi_status zi_adapters_fwd(const zi_adapters *p, const void *X, const 
         b.seg = a.seg;
         b.M = (int32_t)p->M;
         b.r = p->r;
-        b.parts = (int32_t)parts;
+        b.parts = rows ? (int32_t)parts : 1;
         b.same = Y0 == Y;
-        e = expand(p->dtype, p->out_dtype, b, block == 1, s);
+        e = expand(p->dtype, p->out_dtype, b, rows, s);
     }
     if (e != hipSuccess) return fail(ZI_ERR_HIP, "adapters forward: %s", hipGetErrorString(e));
     return ZI_OK;
 }
 
 extern "C" uint64_t zi_adapters_bwd_bytes(int64_t T, int32_t r) {
-    return T < 1 || r < 1 ? 0 : round_up(u_bytes(T, r)) + round_up((uint64_t)T * r * 4) + part_bytes(r);
+    return T < 1 || r < 1 ? 0 : parts_bytes(T, r) + u_bytes(T, r) + part_bytes(r);
 }
 
 extern "C" zi_status zi_adapters_bwd(const zi_adapters *p, const void *X, const void *dY, const float *U, const void *A, const void *B,
@@ -850,8 +858,8 @@ extern "C" zi_status zi_adapters_bwd(const zi_adapters *p, const void *X, const 
     hipStream_t s = static_cast<hipStream_t>(stream);
     const int64_t S = max64(p->S, 1);
     char *work = static_cast<char *>(workspace);
-    float *parted = reinterpret_cast<float *>(work), *dU = reinterpret_cast<float *>(work + round_up(u_bytes(p->T, p->r)));
-    float *part = reinterpret_cast<float *>(work + round_up(u_bytes(p->T, p->r)) + round_up((uint64_t)p->T * p->r * 4));
+    float *parted = reinterpret_cast<float *>(work), *dU = reinterpret_cast<float *>(work + parts_bytes(p->T, p->r));
+    float *part = reinterpret_cast<float *>(work + parts_bytes(p->T, p->r) + u_bytes(p->T, p->r));
     const Segments seg = segments_of(p, offsets, ids);
     hipError_t e = hipSuccess;
     if (p->T > 0) {
