@@ -264,8 +264,14 @@ __device__ __forceinline__ void load_y(const ExpandArgs &a, int64_t row, int64_t
 // U[rank][row] as the sum of its parts, in order.
 __device__ __forceinline__ float u_at(const ExpandArgs &a, int rank, int row) {
     const float *p = a.U + (int64_t)rank * a.seg.rows + row;
-    float u = *p;
-    for (int k = 1; k < a.parts; ++k) u += p[(int64_t)k * a.r * a.seg.rows];
+    float u = 0.f;
+    for (int k0 = 0; k0 < a.parts; k0 += 8) {
+        float v[8];
+#pragma unroll
+        for (int k = 0; k < 8; ++k) v[k] = k0 + k < a.parts ? p[(int64_t)(k0 + k) * a.r * a.seg.rows] : 0.f;
+#pragma unroll
+        for (int k = 0; k < 8; ++k) u += v[k];
+    }
     return u;
 }
 
@@ -376,6 +382,20 @@ __global__ __launch_bounds__(256) void expand_row_kernel(ExpandArgs a) {
         (void)lo;
         (void)hi;
         if (n < 0 && a.same && !a.U_out) return;
+        const bool in = m < a.M;
+        const T *B = reinterpret_cast<const T *>(a.B + (int64_t)(n < 0 ? 0 : n) * a.r * a.M + (in ? m : 0));
+        float y[8], d[8] = {};
+        u32x4 raw[16];
+        auto load_b = [&](int k) __attribute__((always_inline)) {
+#pragma unroll
+            for (int q = 0; q < 16; ++q) {
+                raw[q] = u32x4{0, 0, 0, 0};
+                if (k + q < a.r) raw[q] = *reinterpret_cast<const u32x4 *>(B + (int64_t)(k + q) * a.M);
+            }
+        };
+        // what the row needs of B_n and Y0 is on its way before U is read
+        if (n >= 0) load_b(0);
+        if (in) load_y<YT>(a, row, m, y);
         const float scale = n >= 0 && a.scales ? a.scales[n] : 1.f;
         for (int i = threadIdx.x; i < a.r; i += 256) {
             const float v = n >= 0 ? u_at(a, i, row) : 0.f;
@@ -383,26 +403,14 @@ __global__ __launch_bounds__(256) void expand_row_kernel(ExpandArgs a) {
             u[i] = v * scale;
         }
         __syncthreads();
-        if (m >= a.M || (n < 0 && a.same)) return;
-        float y[8], d[8] = {};
-        load_y<YT>(a, row, m, y);
-        if (n >= 0) {
-            const T *B = reinterpret_cast<const T *>(a.B + (int64_t)n * a.r * a.M + m);
-            int k = 0;
-            for (; k + 16 <= a.r; k += 16) {
-                u32x4 raw[16];
+        if (!in || (n < 0 && a.same)) return;
+        for (int k = 0; n >= 0 && k < a.r; k += 16) {
+            if (k > 0) load_b(k);
 #pragma unroll
-                for (int q = 0; q < 16; ++q) raw[q] = *reinterpret_cast<const u32x4 *>(B + (int64_t)(k + q) * a.M);
+            for (int q = 0; q < 16; ++q) {
+                if (k + q >= a.r) break;
 #pragma unroll
-                for (int q = 0; q < 16; ++q)
-#pragma unroll
-                    for (int e = 0; e < 8; ++e) d[e] += u[k + q] * value16<T>((raw[q][e >> 1] >> (16 * (e & 1))) & 0xffffu);
-            }
-            for (; k < a.r; ++k) {
-                float b[8];
-                load8(B + (int64_t)k * a.M, b);
-#pragma unroll
-                for (int e = 0; e < 8; ++e) d[e] += u[k] * b[e];
+                for (int e = 0; e < 8; ++e) d[e] += u[k + q] * value16<T>((raw[q][e >> 1] >> (16 * (e & 1))) & 0xffffu);
             }
         }
 #pragma unroll

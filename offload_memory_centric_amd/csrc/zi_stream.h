@@ -79,7 +79,7 @@ __device__ __forceinline__ void stream_product(__amdgpu_buffer_rsrc_t qr, const 
     for (int s = s0; s < s1; s += 2 * AHEAD) {
         load(B1{}, s + AHEAD);
         multiply(B0{});
-        load(B0{}, s + 2 * AHEAD);
+        if (s + 2 * AHEAD < s1) load(B0{}, s + 2 * AHEAD);
         multiply(B1{});
     }
     // The compiler has read the sums right behind the loop, before the last product
