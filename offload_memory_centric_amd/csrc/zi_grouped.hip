@@ -47,7 +47,7 @@ int tile_of(int64_t rows, int64_t cols, int64_t groups, double red, bool ragged)
             const double alone = 6.2 * r + 4, full = 12 * r + 5;
             t = each > 4 ? each / 4 * full : alone + (full - alone) * fmax(0, each - 1) / 3;
         }
-        if (least == 0 || t < least) {
+        if (least == 0 || t < 0.93 * least) {  // (where they are close, the larger)
             best = tile;
             least = t;
         }
