@@ -23,7 +23,7 @@ SOURCES = ["zi_kernels.hip", "zi_api.cpp", "zi_plan.cpp", "zi_adam.cpp", "zi_sou
 # sources with matrix-core instructions in inline assembly
 MFMA_SOURCES = ["zi_kernels.hip", "zi_orth_gemm.hip", "zi_grouped_fwd.hip", "zi_grouped_dx.hip", "zi_grouped_dw.hip"]
 # sources with matrix-core builtins
-BUILTIN_SOURCES = ["zi_adapter.hip"]
+BUILTIN_SOURCES = ["zi_grouped.hip", "zi_adapter.hip"]
 COMMON = ["-O3", "-std=c++17", "-fPIC", "-Wall", "-Wno-unused-function",
           "-I" + os.path.join(ROOT, "include")]
 # Packed fp32 VALU forms are kept out of every device code object.

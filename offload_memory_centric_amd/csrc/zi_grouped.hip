@@ -5,24 +5,141 @@
 //   dX       dX = dY W_g, with GeLU times GeLU'(A)
 //   dW       dW_g (+)= dY_g^T X_g
 // The offsets stay on the device: a workgroup finds its tile among all groups' by a
-// scan, so that nothing waits for the host.  All run on the MFMA kernel of zi_gemm.h,
-// on macro-tiles of 256, 128 or 64 rows and columns.  (Groups of a few rows, as in
-// serving, only wait for their weights.  A kernel that read W from memory into the
-// matrix cores' registers, 16 rows by 64 bytes at a time, took 33.9 us for 32 rows of
-// 64 experts, 2048 x 1408 bf16; tiles of 64, whose copies into LDS fetch whole lines of
-// 128 bytes, 26.5.)
+// scan, so that nothing waits for the host.  Most run on the MFMA kernel of zi_gemm.h,
+// on macro-tiles of 256, 128 or 64 rows and columns; groups of a few rows, as in
+// serving, which only wait for their weights, on the kernel here.
 #include <hip/hip_runtime.h>
 #include <math.h>
 #include <stdint.h>
 
 #include "zi_host.h"
-#include "zi_internal.h"
+#include "zi_stream.h"
 
 namespace zi {
 namespace {
 
+// 16 rows of one group by 16 QF columns.  The four waves share the reduction, each with
+// a ring of its own in LDS, so that none waits for another before the end: steps of 64
+// values, whose copies fetch whole lines of 128 bytes (chunks permuted as RcOperand's),
+// DEPTH steps at a time; rows past the group's are not fetched.  Each workgroup begins
+// at another step: where W's rows are a power of two apart, the same columns of all rows
+// lie in few of the memory's channels.  The sums meet in LDS in a fixed order.
+template <typename T, int QF, int EPI>
+__global__ __launch_bounds__(256) void few_rows_kernel(GroupArgs a, int tiles_q) {
+    constexpr int DEPTH = 4, STAGE = (16 * QF + 16) * 128, NC = 2 * QF + 2;
+    __shared__ __attribute__((aligned(1024))) char lds[4 * DEPTH * STAGE];
+    GroupTile gt;
+    if (!find_group_tile<16>(a.offsets, a.groups, a.total, blockIdx.x, tiles_q, 64, gt)) return;
+    const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int c = lane & 15, g = lane >> 4, row8 = lane >> 3;
+    const int64_t q0 = (int64_t)gt.tq * (16 * QF), p0 = gt.lo + (int64_t)gt.tp * 16;
+    const int group = __builtin_amdgcn_readfirstlane(gt.group);
+    const rsrc_t wr = make_rsrc(reinterpret_cast<const char *>(static_cast<const uint16_t *>(a.Q) + group * a.q_group + q0 * a.ldq));
+    const rsrc_t xr = make_rsrc(reinterpret_cast<const char *>(static_cast<const uint16_t *>(a.P) + p0 * a.ldp));
+    const int red = (int)a.red, all = (red + 63) / 64;
+    const int from = all * wave / 4, steps = all * (wave + 1) / 4 - from;
+    const int turn = steps > 0 ? (int)(blockIdx.x * 5u % (unsigned)steps) : 0;
+    const uint32_t at = lds_addr(lds) + (uint32_t)(wave * DEPTH * STAGE);
+    // a copy is 8 rows of 128 bytes; its lane's chunk depends on the row's bit 3 alone
+    uint32_t wo[2 * QF], xo[2], ck[2];
+#pragma unroll
+    for (int j = 0; j < 2; ++j) ck[j] = (uint32_t)(((lane & 7) ^ (((8 * j + row8) >> 1) & 7)) * 8);
+#pragma unroll
+    for (int j = 0; j < 2 * QF; ++j) {
+        const int row = 8 * j + row8;
+        wo[j] = q0 + row < a.cols ? (uint32_t)((row * a.ldq + ck[j & 1]) * 2) : kOOB;
+    }
+#pragma unroll
+    for (int j = 0; j < 2; ++j) xo[j] = p0 + 8 * j + row8 < gt.hi ? (uint32_t)(((8 * j + row8) * a.ldp + ck[j]) * 2) : kOOB;
+    uint32_t fo[2];  // this lane's fragment of the two halves of a step, within 16 rows
+#pragma unroll
+    for (int h = 0; h < 2; ++h) fo[h] = (uint32_t)(c * 128 + (((4 * h + g) ^ ((c >> 1) & 7)) << 4));
+
+    auto issue = [&](int s) __attribute__((always_inline)) {  // past the last step: zeros
+        const uint32_t stage = at + (uint32_t)(s % DEPTH) * STAGE;
+        const int turned = s + turn < steps ? s + turn : s + turn - steps;
+        const uint32_t k0 = s < steps ? (uint32_t)(from + turned) * 64 : (uint32_t)red;
+        const uint32_t left = (uint32_t)red - k0;
+        const uint32_t k2[2] = {ck[0] < left ? k0 * 2 : kOOB, ck[1] < left ? k0 * 2 : kOOB};
+        // (two offsets past the descriptor's range stay past it when added)
+#pragma unroll
+        for (int j = 0; j < 2 * QF; ++j) copy16(wr, stage + j * 1024, wo[j] + k2[j & 1]);
+#pragma unroll
+        for (int j = 0; j < 2; ++j) copy16(xr, stage + QF * 2048 + j * 1024, xo[j] + k2[j]);
+    };
+    f32x4 acc[QF] = {};
+#pragma unroll
+    for (int s = 0; s < DEPTH - 1; ++s) issue(s);
+    for (int s = 0; s < steps; ++s) {
+        // step s has landed, and step s - 1 has been read
+        asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" ::"n"((DEPTH - 2) * NC) : "memory");
+        issue(s + DEPTH - 1);
+        const uint32_t stage = at + (uint32_t)(s % DEPTH) * STAGE;
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const u32x4 x =
+                *reinterpret_cast<const __attribute__((address_space(3))) u32x4 *>((uintptr_t)(stage + QF * 2048 + fo[h]));
+#pragma unroll
+            for (int i = 0; i < QF; ++i)
+                acc[i] = mfma<T>(*reinterpret_cast<const __attribute__((address_space(3))) u32x4 *>((uintptr_t)(stage + i * 2048 + fo[h])),
+                                 x, acc[i]);
+        }
+    }
+    // every copy has landed and every read returned before the rings hold the sums
+    __builtin_amdgcn_sched_barrier(0);
+    asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier\n\ts_nop 7\n\ts_nop 7" ::: "memory");
+    f32x4(*sums)[QF][64] = reinterpret_cast<f32x4(*)[QF][64]>(lds);
+#pragma unroll
+    for (int i = 0; i < QF; ++i) sums[wave][i][lane] = acc[i];
+    __syncthreads();
+    for (int t = tid; t < QF * 64; t += 256) {
+        const int f = t >> 6, ln = t & 63;
+        f32x4 v = sums[0][f][ln];
+#pragma unroll
+        for (int k = 1; k < 4; ++k) v += sums[k][f][ln];
+        const int64_t q = q0 + 16 * f + 4 * (ln >> 4), p = p0 + (ln & 15);
+        if (p >= gt.hi || q >= a.cols) continue;
+        const int64_t off = p * a.ldc + q;
+        if constexpr (EPI == EPI_F32) {
+            *reinterpret_cast<f32x4 *>(static_cast<float *>(a.C) + off) = v;
+        } else {
+            uint32_t b[4], h[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                b[e] = bits16<T>(v[e]);
+                h[e] = EPI == EPI_ACT ? bits16<T>(gelu_f32(v[e])) : b[e];
+            }
+            *reinterpret_cast<u32x2 *>(static_cast<uint16_t *>(a.C) + off) = u32x2{h[0] | (h[1] << 16), h[2] | (h[3] << 16)};
+            if (EPI == EPI_ACT && a.C2)
+                *reinterpret_cast<u32x2 *>(static_cast<uint16_t *>(a.C2) + p * a.ldpre + q) =
+                    u32x2{b[0] | (b[1] << 16), b[2] | (b[3] << 16)};
+        }
+    }
+}
+
 int64_t ceil_div(int64_t x, int64_t y) { return (x + y - 1) / y; }
 int64_t min64(int64_t x, int64_t y) { return x < y ? x : y; }
+
+template <typename T, int QF, int EPI>
+hipError_t run_few(const GroupArgs &a, hipStream_t s) {
+    const int64_t tiles_q = ceil_div(a.cols, 16 * QF);
+    const int64_t rows = a.total / 16 + min64(a.groups, a.total);
+    const int64_t grid = ceil_div(rows * tiles_q, 8) * 8;
+    if (grid > INT32_MAX / 256) return hipErrorInvalidValue;
+    hipLaunchKernelGGL((few_rows_kernel<T, QF, EPI>), dim3((unsigned)grid), dim3(256), 0, s, a, (int)tiles_q);
+    return hipGetLastError();
+}
+// 64 columns a workgroup, one of which a compute unit's LDS holds; 32 where that leaves
+// compute units without one.
+template <typename T, int EPI>
+hipError_t few_sized(const GroupArgs &a, hipStream_t s) {
+    return min64(a.groups, a.total) * ceil_div(a.cols, 64) < 256 ? run_few<T, 2, EPI>(a, s) : run_few<T, 4, EPI>(a, s);
+}
+template <typename T>
+hipError_t few(const GroupArgs &a, hipStream_t s) {
+    if (a.act) return few_sized<T, EPI_ACT>(a, s);
+    return a.out_f32 ? few_sized<T, EPI_F32>(a, s) : few_sized<T, EPI_LP>(a, s);
+}
 
 // The macro-tile that takes least, by its rounds of workgroups on 256 compute units, of
 // which each holds one tile of 256, two of 128 or four of 64.  A round takes what the
@@ -118,7 +235,16 @@ extern "C" zi_status zi_grouped_fwd(const zi_grouped *g, const void *X, const vo
     a.cols = g->M;
     a.red = g->K;
     hipStream_t s = static_cast<hipStream_t>(stream);
-    const hipError_t e = launch_grouped_fwd(g->dtype, tile_of(g->R, g->M, min64(g->E, g->R), (double)g->K, true), a, s);
+    const int64_t live = min64(g->E, g->R);
+    // Up to 16 rows an average group with any: the weights' bytes are what counts.  (us
+    // from memory, few_rows_kernel and the best macro-tile: 32 rows of 64 experts, 2048 x
+    // 1408, 41.6 and 42.9; 128 rows of them 79.6, 98.7; 2 rows of 8 experts, 8192 x 4096,
+    // 27.0, 56.3; 128 rows of 8 experts, 4096 x 2048, 27.9, 36.0; 256 rows 47.5, 36.8.)
+    hipError_t e;
+    if (g->R <= 16 * live)
+        e = g->dtype == ZI_F16 ? few<_Float16>(a, s) : few<__bf16>(a, s);
+    else
+        e = launch_grouped_fwd(g->dtype, tile_of(g->R, g->M, live, (double)g->K, true), a, s);
     if (e != hipSuccess) return fail(ZI_ERR_HIP, "grouped forward: %s", hipGetErrorString(e));
     return ZI_OK;
 }
