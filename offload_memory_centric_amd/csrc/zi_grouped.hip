@@ -18,15 +18,17 @@
 namespace zi {
 namespace {
 
-// 16 rows of one group by 16 QF columns.  The four waves share the reduction, each with
+// 16 rows of one group by 32 columns.  The four waves share the reduction, each with
 // a ring of its own in LDS, so that none waits for another before the end: steps of 64
 // values, whose copies fetch whole lines of 128 bytes (chunks permuted as RcOperand's),
-// DEPTH steps at a time; rows past the group's are not fetched.  Each workgroup begins
+// three steps at a time, two workgroups a compute unit; rows past the group's are not
+// fetched.  (32 rows unevenly over 64 experts, 2048 x 1408 bf16: 33.4 us; with 64 columns
+// and four steps, one workgroup a unit, 42.8; one row, 8192 x 8192: 26.4 and 28.8.)  Each workgroup begins
 // at another step: where W's rows are a power of two apart, the same columns of all rows
 // lie in few of the memory's channels.  The sums meet in LDS in a fixed order.
-template <typename T, int QF, int EPI>
+template <typename T, int EPI>
 __global__ __launch_bounds__(256) void few_rows_kernel(GroupArgs a, int tiles_q) {
-    constexpr int DEPTH = 4, STAGE = (16 * QF + 16) * 128, NC = 2 * QF + 2;
+    constexpr int QF = 2, DEPTH = 3, STAGE = (16 * QF + 16) * 128, NC = 2 * QF + 2;
     __shared__ __attribute__((aligned(1024))) char lds[4 * DEPTH * STAGE];
     GroupTile gt;
     if (!find_group_tile<16>(a.offsets, a.groups, a.total, blockIdx.x, tiles_q, 64, gt)) return;
@@ -120,25 +122,19 @@ __global__ __launch_bounds__(256) void few_rows_kernel(GroupArgs a, int tiles_q)
 int64_t ceil_div(int64_t x, int64_t y) { return (x + y - 1) / y; }
 int64_t min64(int64_t x, int64_t y) { return x < y ? x : y; }
 
-template <typename T, int QF, int EPI>
+template <typename T, int EPI>
 hipError_t run_few(const GroupArgs &a, hipStream_t s) {
-    const int64_t tiles_q = ceil_div(a.cols, 16 * QF);
+    const int64_t tiles_q = ceil_div(a.cols, 32);
     const int64_t rows = a.total / 16 + min64(a.groups, a.total);
     const int64_t grid = ceil_div(rows * tiles_q, 8) * 8;
     if (grid > INT32_MAX / 256) return hipErrorInvalidValue;
-    hipLaunchKernelGGL((few_rows_kernel<T, QF, EPI>), dim3((unsigned)grid), dim3(256), 0, s, a, (int)tiles_q);
+    hipLaunchKernelGGL((few_rows_kernel<T, EPI>), dim3((unsigned)grid), dim3(256), 0, s, a, (int)tiles_q);
     return hipGetLastError();
-}
-// 64 columns a workgroup, one of which a compute unit's LDS holds; 32 where that leaves
-// compute units without one.
-template <typename T, int EPI>
-hipError_t few_sized(const GroupArgs &a, hipStream_t s) {
-    return min64(a.groups, a.total) * ceil_div(a.cols, 64) < 256 ? run_few<T, 2, EPI>(a, s) : run_few<T, 4, EPI>(a, s);
 }
 template <typename T>
 hipError_t few(const GroupArgs &a, hipStream_t s) {
-    if (a.act) return few_sized<T, EPI_ACT>(a, s);
-    return a.out_f32 ? few_sized<T, EPI_F32>(a, s) : few_sized<T, EPI_LP>(a, s);
+    if (a.act) return run_few<T, EPI_ACT>(a, s);
+    return a.out_f32 ? run_few<T, EPI_F32>(a, s) : run_few<T, EPI_LP>(a, s);
 }
 
 // The macro-tile that takes least, by its rounds of workgroups on 256 compute units, of
@@ -237,9 +233,9 @@ extern "C" zi_status zi_grouped_fwd(const zi_grouped *g, const void *X, const vo
     hipStream_t s = static_cast<hipStream_t>(stream);
     const int64_t live = min64(g->E, g->R);
     // Up to 16 rows an average group with any: the weights' bytes are what counts.  (us
-    // from memory, few_rows_kernel and the best macro-tile: 32 rows of 64 experts, 2048 x
-    // 1408, 41.6 and 42.9; 128 rows of them 79.6, 98.7; 2 rows of 8 experts, 8192 x 4096,
-    // 27.0, 56.3; 128 rows of 8 experts, 4096 x 2048, 27.9, 36.0; 256 rows 47.5, 36.8.)
+    // from memory, few_rows_kernel and the best macro-tile: 128 rows of 64 experts, 2048 x
+    // 1408, 72.1 and 98.7; 2 rows of 8 experts, 8192 x 4096, 26.5, 56.3; 128 rows of 8
+    // experts, 4096 x 2048, 25.5, 36.0; 256 rows of them 45.2, 36.8.)
     hipError_t e;
     if (g->R <= 16 * live)
         e = g->dtype == ZI_F16 ? few<_Float16>(a, s) : few<__bf16>(a, s);
