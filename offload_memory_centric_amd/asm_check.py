@@ -187,6 +187,20 @@ def _window(instrs: List[Instr], end: int, forward: bool) -> List[Instr]:
     return out if forward else out[::-1]
 
 
+def m0_uses(instrs: List[Instr]) -> List[str]:
+    """Uses of m0 outside a global -> LDS copy."""
+    found: List[str] = []
+    for k, ins in enumerate(instrs):
+        if not any(a == "m0" for a in ins.args):
+            continue
+        nxt = instrs[k + 1] if k + 1 < len(instrs) else None
+        ok = (ins.op == "s_mov_b32" and ins.args[0] == "m0" and nxt is not None and
+              nxt.op.startswith("buffer_load") and "lds" in nxt.args[-1].split())
+        if not ok:
+            found.append("line %d: %r uses m0 outside a global -> LDS copy" % (ins.line, ins.text))
+    return found
+
+
 def check_kernel(body: List[Tuple[int, str]]) -> List[str]:
     instrs: List[Instr] = []
     labels = {}
@@ -204,15 +218,7 @@ def check_kernel(body: List[Tuple[int, str]]) -> List[str]:
         if b:
             branches.append((len(instrs), b.group(1)))
         instrs.append(ins)
-    found = check_sequence(instrs)
-    for k, ins in enumerate(instrs):
-        if not any(a == "m0" for a in ins.args):
-            continue
-        nxt = instrs[k + 1] if k + 1 < len(instrs) else None
-        ok = (ins.op == "s_mov_b32" and ins.args[0] == "m0" and nxt is not None and
-              nxt.op.startswith("buffer_load") and "lds" in nxt.args[-1].split())
-        if not ok:
-            found.append("line %d: %r uses m0 outside a global -> LDS copy" % (ins.line, ins.text))
+    found = check_sequence(instrs) + m0_uses(instrs)
     for at, target in branches:
         if target in labels:
             found += check_sequence(_window(instrs, at + 1, False) + _window(instrs, labels[target], True))
@@ -222,7 +228,8 @@ def check_kernel(body: List[Tuple[int, str]]) -> List[str]:
 def early_reads(body: List[Tuple[int, str]]) -> List[str]:
     """Non-MFMA instructions that touch an MFMA's result before
     its BUILTIN_RESULT_WAIT wait states, in a kernel whose MFMAs the compiler made:
-    along the listing, and along every branch of it that is taken."""
+    along the listing, and along every branch of it that is taken; and uses of m0
+    outside the copies."""
     instrs: List[Instr] = []
     labels = {}
     for no, line in body:
@@ -233,7 +240,7 @@ def early_reads(body: List[Tuple[int, str]]) -> List[str]:
         ins = _parse(line, no)
         if ins is not None:
             instrs.append(ins)
-    found: List[str] = []
+    found = m0_uses(instrs)
 
     def follow(i: int, waits: int, dst: Set[Reg], mfma: Instr, jumped: bool) -> None:
         while i < len(instrs) and waits < BUILTIN_RESULT_WAIT.get(mfma.op, RESULT_WAIT):

@@ -310,6 +310,8 @@ def test_early_reads_of_a_result():
     assert findings(".LBB0_1:", read, "\ts_nop 7", mfma, "\ts_cbranch_vccnz .LBB0_1", "\ts_endpgm")
     assert not findings(".LBB0_1:", "\ts_nop 6", read, mfma, "\ts_cbranch_vccnz .LBB0_1", "\ts_nop 6", read)
     assert not findings(mfma, mfma, "\tv_add_f32 v8, v9, v10")
+    copy = ["\ts_mov_b32 m0, s3", "\tbuffer_load_dwordx4 v1, s[4:7], 0 offen lds"]
+    assert not findings(*copy) and findings(copy[0], mfma) and findings("\tv_mov_b32 v1, m0")
     slow = "\tv_mfma_f32_16x16x4_f32 a[0:3], v0, v1, a[0:3]"
     assert findings(slow, "\ts_nop 6", read) and not findings(slow, "\ts_nop 7", "\ts_nop 1", read)
 

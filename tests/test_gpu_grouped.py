@@ -289,6 +289,35 @@ def test_offsets_outside_the_rows():
             assert (Y == -7.0).all()
 
 
+def test_no_rows():
+    from offload_memory_centric_amd import layers
+    offsets = torch.zeros(4, dtype=torch.int32, device="cuda")
+    X, dY = (torch.empty((0, n), dtype=torch.bfloat16, device="cuda") for n in (64, 72))
+    for dt in (torch.bfloat16, torch.float32):
+        dW = torch.full((3, 72, 64), 2.0, dtype=dt, device="cuda")
+        layers.grouped_dw(X, dY, offsets, dW)
+        assert (dW == 0).all()
+    dW.fill_(2.0)
+    layers.grouped_dw(X, dY, offsets, dW, accumulate=True)
+    assert (dW == 2.0).all()
+    layers.grouped_fwd(X, dW.bfloat16(), offsets, dY)
+    layers.grouped_dx(dY, dW.bfloat16(), offsets, X)
+
+
+def test_many_groups():
+    """More groups than a wave has lanes many times over, few with rows."""
+    from offload_memory_centric_amd import layers
+    E, K, M = 4096, 64, 40
+    for rows in (1, 40):
+        sizes = [0] * E
+        for e in (0, 63, 64, 1000, 4095):
+            sizes[e] = rows
+        c = Case(sizes, K, M, "bf16", whole=True)
+        c.fwd(layers, "bf16", exact=True)
+        c.dx(layers, "f32", exact=True)
+        c.dw(layers, "f32", exact=True)
+
+
 def test_far_rows():
     """Rows and weights past 2^32 bytes."""
     from offload_memory_centric_amd import layers
