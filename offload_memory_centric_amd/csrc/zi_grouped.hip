@@ -137,17 +137,20 @@ hipError_t few(const GroupArgs &a, hipStream_t s) {
     return a.out_f32 ? run_few<T, EPI_F32>(a, s) : run_few<T, EPI_LP>(a, s);
 }
 
-// The macro-tile that takes least, by its rounds of workgroups on 256 compute units, of
-// which each holds one tile of 256, two of 128 or four of 64.  A round takes what the
-// products of many shapes measured (us for a reduction of r thousand): 19.1 r + 14,
-// 12.6 r + 6 and 12 r + 5; a tile that has its unit to itself 16.5 r + 14, 7.4 r + 5 and
-// 6.2 r + 4.  Of a ragged operand's row tiles one a group is taken as half full.  (Over
-// 45 products of 1 to 64 groups the choice is 1.5 % slower than the best tile on
-// average; 20000 rows of 16 groups, 1024 x 1024: 74.0, 60.8 and 83.7 us forward.)
-int tile_of(int64_t rows, int64_t cols, int64_t groups, double red, bool ragged) {
+// The macro-tile that takes least, and how long (us), by its rounds of workgroups on 256
+// compute units, of which each holds one tile of 256, two of 128 or four of 64.  A round
+// takes what the products of many shapes measured (us for a reduction of r thousand):
+// 19.1 r + 14, 12.6 r + 6 and 12 r + 5; a tile that has its unit to itself 16.5 r + 14,
+// 7.4 r + 5 and 6.2 r + 4.  Of a ragged operand's row tiles one a group is taken as half
+// full.  (Over 45 products of 1 to 64 groups the choice is 1.7 % slower than the best
+// tile on average; 20000 rows of 16 groups, 1024 x 1024: 74.0, 60.8 and 83.7 us forward.)
+struct Choice {
+    int tile;
+    double us;
+};
+Choice tile_of(int64_t rows, int64_t cols, int64_t groups, double red, bool ragged) {
     const double r = red / 1000;
-    int best = 256;
-    double least = 0;
+    Choice best = {256, 0};
     for (int tile = 256; tile >= 64; tile /= 2) {
         const double row_tiles = ragged ? (double)rows / tile + 0.5 * (double)groups : (double)ceil_div(rows, tile) * (double)groups;
         const double each = row_tiles * (double)ceil_div(cols, tile) / 256;  // tiles a compute unit
@@ -160,12 +163,21 @@ int tile_of(int64_t rows, int64_t cols, int64_t groups, double red, bool ragged)
             const double alone = 6.2 * r + 4, full = 12 * r + 5;
             t = each > 4 ? each / 4 * full : alone + (full - alone) * fmax(0, each - 1) / 3;
         }
-        if (least == 0 || t < 0.93 * least) {  // (where they are close, the larger)
-            best = tile;
-            least = t;
-        }
+        if (best.us == 0 || t < 0.93 * best.us) best = {tile, t};  // where they are close, the larger
     }
     return best;
+}
+
+// Whether few_rows_kernel takes less than the best macro-tile: it reads W once for every
+// 16 rows, at 8.7 TB/s from the L2s, and from memory at 5.1 TB/s, the macro-tiles at 4.2.
+// (us, few rows and best tile: 128 rows of 64 groups, 2048 x 1408, 72.1 and 98.7; 2 rows
+// of 8, 8192 x 4096, 26.5, 56.3; 128 rows of 8, 4096 x 2048, 25.5, 36.0; 256 rows of them
+// 45.2, 36.8.)
+bool few_rows(int64_t R, int64_t K, int64_t M, int64_t live, double best_us) {
+    const double tiles = R <= 16 * live ? (double)live : (double)R / 16 + 0.5 * (double)live;
+    const double weights = (double)live * (double)K * (double)M * 2e-6;  // MB
+    const double t = 5 + tiles * (double)ceil_div(M, 32) * 48 * (double)K * 2e-6 / 8.7;
+    return fmax(t, weights / 5.1) < fmax(best_us, weights / 4.2);
 }
 
 bool aligned(const void *p, uint64_t to) { return ((uintptr_t)p & (to - 1)) == 0; }
@@ -232,15 +244,12 @@ extern "C" zi_status zi_grouped_fwd(const zi_grouped *g, const void *X, const vo
     a.red = g->K;
     hipStream_t s = static_cast<hipStream_t>(stream);
     const int64_t live = min64(g->E, g->R);
-    // Up to 16 rows an average group with any: the weights' bytes are what counts.  (us
-    // from memory, few_rows_kernel and the best macro-tile: 128 rows of 64 experts, 2048 x
-    // 1408, 72.1 and 98.7; 2 rows of 8 experts, 8192 x 4096, 26.5, 56.3; 128 rows of 8
-    // experts, 4096 x 2048, 25.5, 36.0; 256 rows of them 45.2, 36.8.)
+    const Choice best = tile_of(g->R, g->M, live, (double)g->K, true);
     hipError_t e;
-    if (g->R <= 16 * live)
+    if (few_rows(g->R, g->K, g->M, live, best.us))
         e = g->dtype == ZI_F16 ? few<_Float16>(a, s) : few<__bf16>(a, s);
     else
-        e = launch_grouped_fwd(g->dtype, tile_of(g->R, g->M, live, (double)g->K, true), a, s);
+        e = launch_grouped_fwd(g->dtype, best.tile, a, s);
     if (e != hipSuccess) return fail(ZI_ERR_HIP, "grouped forward: %s", hipGetErrorString(e));
     return ZI_OK;
 }
@@ -269,7 +278,7 @@ extern "C" zi_status zi_grouped_dx(const zi_grouped *g, const void *dY, const vo
     a.cols = g->K;
     a.red = g->M;
     hipStream_t s = static_cast<hipStream_t>(stream);
-    const hipError_t e = launch_grouped_dx(g->dtype, tile_of(g->R, g->K, min64(g->E, g->R), (double)g->M, true), a, s);
+    const hipError_t e = launch_grouped_dx(g->dtype, tile_of(g->R, g->K, min64(g->E, g->R), (double)g->M, true).tile, a, s);
     if (e != hipSuccess) return fail(ZI_ERR_HIP, "grouped input gradient: %s", hipGetErrorString(e));
     return ZI_OK;
 }
@@ -296,7 +305,7 @@ extern "C" zi_status zi_grouped_dw(const zi_grouped *g, const void *X, const voi
     a.red = g->R;
     a.accumulate = g->accumulate;
     hipStream_t s = static_cast<hipStream_t>(stream);
-    const hipError_t e = launch_grouped_dw(g->dtype, tile_of(g->M, g->K, g->E, (double)g->R / g->E, false), a, s);
+    const hipError_t e = launch_grouped_dw(g->dtype, tile_of(g->M, g->K, g->E, (double)g->R / g->E, false).tile, a, s);
     if (e != hipSuccess) return fail(ZI_ERR_HIP, "grouped weight gradient: %s", hipGetErrorString(e));
     return ZI_OK;
 }

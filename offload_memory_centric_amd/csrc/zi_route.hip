@@ -516,7 +516,7 @@ __global__ __launch_bounds__(256) void combine_fwd_kernel(const ZT *Z, int64_t l
     const int per = 256 / row_threads, lane = threadIdx.x % row_threads;
     const int64_t vecs = (D + 7) / 8;
     for (int64_t t = (int64_t)blockIdx.x * per + threadIdx.x / row_threads; t < T; t += (int64_t)gridDim.x * per) {
-        for (int64_t v = lane; v < vecs; v += row_threads) {
+        for (int64_t v = lane + (int64_t)blockIdx.y * row_threads; v < vecs; v += (int64_t)gridDim.y * row_threads) {
             const Vec at = D >= 8 ? vec_of(v, D) : Vec{0, 0};
             float y[8] = {};
             for (int j0 = 0; j0 < k; j0 += kRowsAhead) {
@@ -557,7 +557,7 @@ __global__ __launch_bounds__(256) void combine_bwd_kernel(const ZT *dY, int64_t 
     // every thread takes as many turns, since they meet
     for (int64_t t0 = (int64_t)blockIdx.x * per; t0 < T; t0 += (int64_t)gridDim.x * per) {
         const int64_t t = t0 + threadIdx.x / row_threads;
-        for (int j0 = 0; j0 < k; j0 += KP) {
+        for (int j0 = blockIdx.y * KP; j0 < k; j0 += gridDim.y * KP) {
             int64_t slot[KP];
             float w[KP], sum[KP];
 #pragma unroll
@@ -622,6 +622,10 @@ __global__ __launch_bounds__(256) void combine_bwd_kernel(const ZT *dY, int64_t 
         }
     }
 }
+
+// Workgroups below which a combination of few tokens is shared out further.  (31 tokens
+// of 4 x 13011 bf16, backward: 22.9 us with one workgroup a token.)
+constexpr int64_t kFewTokens = 512;
 
 // ---- launches ----------------------------------------------------------------------------
 
@@ -780,7 +784,9 @@ extern "C" zi_status zi_combine_fwd(const zi_combine *c, const void *Z, const in
     const int64_t groups = ceil_div(c->T, 256 / row);
     const hipError_t e = with_type(c->dtype, [&](auto type) {
         using ZT = decltype(type);
-        hipLaunchKernelGGL((combine_fwd_kernel<ZT>), dim3((unsigned)(groups < (1 << 20) ? groups : (1 << 20))), dim3(256), 0, s,
+        // few tokens: their columns are shared out too
+        const int64_t parts = groups < kFewTokens ? ceil_div(c->D, 8 * row) : 1;
+        hipLaunchKernelGGL((combine_fwd_kernel<ZT>), dim3((unsigned)(groups < (1 << 20) ? groups : (1 << 20)), (unsigned)(parts < 1024 ? parts : 1024)), dim3(256), 0, s,
                            static_cast<const ZT *>(Z), c->ldz ? c->ldz : c->D, c->R, slots, weights, c->T, c->D, c->k, row,
                            static_cast<ZT *>(Y), c->ldy ? c->ldy : c->D);
         return hipGetLastError();
@@ -802,7 +808,8 @@ extern "C" zi_status zi_combine_bwd(const zi_combine *c, const void *dY, const v
     hipStream_t s = static_cast<hipStream_t>(stream);
     const int row = row_threads_of(c->D);
     const int64_t groups = ceil_div(c->T, 256 / row);
-    const dim3 grid((unsigned)(groups < (1 << 20) ? groups : (1 << 20)));
+    // few tokens: a workgroup a pair of rows
+    const dim3 grid((unsigned)(groups < (1 << 20) ? groups : (1 << 20)), groups < kFewTokens ? (unsigned)ceil_div(c->k, KP) : 1u);
     const hipError_t e = with_type(c->dtype, [&](auto type) {
         using ZT = decltype(type);
         hipLaunchKernelGGL((combine_bwd_kernel<ZT>), grid, dim3(256), 0, s, static_cast<const ZT *>(dY), c->ldy ? c->ldy : c->D,
