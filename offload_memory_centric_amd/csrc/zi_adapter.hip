@@ -10,12 +10,9 @@
 //   expand  Y from U and B, dX from dU and A      reads and writes the wide rows once
 //   grad    dA from dU and X, dB from U and dY    reads the wide rows once
 // All are bound by the bytes of the wide rows while r is small.  U is kept in fp32 and
-// rounded nowhere.  expand multiplies it by the fp32 matrix instruction (16 x 16 x 4,
-// 157 TFLOP/s), which is as fast as HBM up to a rank of about 64 and takes the other
-// operand as it lies in memory: a lane's 16 bytes are eight columns of one row, which go
-// to eight instructions whose results are eight consecutive columns again.  grad, whose
-// reduction runs over the rows, splits it into planes of 16 bits.  shrink's operands
-// are 16-bit inputs, multiplied exactly by the 16-bit instruction.
+// rounded nowhere: where it is multiplied it is split into planes of the other operand's
+// 16 bits, which the 16-bit matrix instruction takes at sixteen times the rate of the
+// fp32 one.  shrink's operands are 16-bit inputs, multiplied exactly.
 //
 // A row's result depends on that row and its adapter alone: segments are multiplied one
 // by one, so that an infinity or a NaN in one request or adapter reaches no other.
@@ -275,15 +272,65 @@ __device__ __forceinline__ float u_at(const ExpandArgs &a, int rank, int row) {
     return u;
 }
 
-// A wave: 128 columns of a run of rows, 16 rows at a time.  Per step of four ranks a
-// lane has eight columns of one row of B_n, held in registers over the run (r <= 64:
-// HOLD of 4, 8 or 16 steps; more ranks are read again for every 16 rows), and one value
-// of U; instruction j gives rows 4 (lane / 16) .. +3 of column 8 (lane % 16) + j.  U and
-// Y0 of the next 16 rows are on their way while these are multiplied and stored.
+// Eight fp32 values in planes of the 16-bit type that the other operand has, so that the
+// 16-bit instruction multiplies them: three of bf16 (24 bits, at any scale), two of fp16
+// (22 bits below the largest value of those that share a scale, 2^(15 - e), which takes
+// it into [2^14, 2^15)).
+template <typename T>
+struct Planes;
+template <>
+struct Planes<bf16_t> {
+    static constexpr int N = 3;
+    static constexpr bool kScaled = false;
+};
+template <>
+struct Planes<f16_t> {
+    static constexpr int N = 2;
+    static constexpr bool kScaled = true;
+};
+template <typename T, int N>
+__device__ __forceinline__ void split_planes(const float (&v)[8], u32x4 (&out)[N]) {
+    float r[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) r[i] = v[i];
+#pragma unroll
+    for (int p = 0; p < N; ++p) {
+#pragma unroll
+        for (int h = 0; h < 4; ++h) {
+            uint32_t b[2];
+#pragma unroll
+            for (int q = 0; q < 2; ++q) {
+                b[q] = bits16<T>(r[2 * h + q]);
+                const float rest = r[2 * h + q] - value16<T>(b[q]);
+                r[2 * h + q] = fabsf(rest) < INFINITY ? rest : 0.f;  // nothing is left of an infinity or a NaN
+            }
+            out[p][h] = b[0] | (b[1] << 16);
+        }
+    }
+}
+
+// The exponent e of that scale for the largest of `most` over the wave's lanes of equal
+// lane % 16 (not so low that 2^(e - 15) is no normal number).
+__device__ __forceinline__ int scale_exponent(float most) {
+    most = fmaxf(most, __shfl_xor(most, 16, 64));
+    most = fmaxf(most, __shfl_xor(most, 32, 64));
+    return max(__builtin_amdgcn_frexp_expf(most), -110);
+}
+
+// A wave: 128 columns of a run of rows, 16 rows at a time.  Per step of 32 ranks a lane
+// reads eight columns of eight rows of B_n and turns them, in its own registers, into one
+// operand for each of the columns, held over the run (STEPS of 1 or 2, r <= 64; with 0,
+// more ranks, read again for every 16 rows); of U it has eight ranks of a row, split into
+// planes.  Instruction j gives rows 4 (lane / 16) .. +3 of column 8 (lane % 16) + j, so
+// that a lane has eight consecutive columns of Y.  U and Y0 of the next 16 rows are on
+// their way while these are multiplied and stored.  (On the fp32 instruction, 4508 rows
+// of 2384 in 61 segments, r = 64, took 50 us, 37 so; 32768 of 8192 into fp32, r = 32, 462
+// and 406.)
 constexpr int kExpandCols = 512;
-template <typename T, typename YT, int HOLD>
+template <typename T, typename YT, int STEPS>
 __global__ __launch_bounds__(256) void expand_kernel(ExpandArgs a, int block) {
-    constexpr int STEPS = HOLD > 0 ? HOLD : 16;
+    constexpr int NP = Planes<T>::N, HELD = STEPS > 0 ? STEPS : 1;
+    constexpr bool kScaled = Planes<T>::kScaled;
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, c = lane & 15, g = lane >> 4;
     const int b0 = blockIdx.x * block, b1 = min(b0 + block, a.seg.rows);
     const int m = blockIdx.y * kExpandCols + wave * 128 + 8 * c;
@@ -300,71 +347,106 @@ __global__ __launch_bounds__(256) void expand_kernel(ExpandArgs a, int block) {
         }
         const float scale = a.scales ? a.scales[n] : 1.f;
         const uint16_t *B = a.B + (int64_t)n * a.r * a.M + m;
-        u32x4 b[STEPS];
-        auto load_b = [&](int r0) __attribute__((always_inline)) {
+        u32x4 b[HELD][8];  // column j's eight ranks of each step
+        auto load_b = [&](int s, int r0) __attribute__((always_inline)) {
+            u32x4 raw[8];
 #pragma unroll
-            for (int s = 0; s < STEPS; ++s) {
-                const int rank = r0 + 4 * s + g;
-                b[s] = u32x4{0, 0, 0, 0};
-                if (in && rank < a.r) b[s] = *reinterpret_cast<const u32x4 *>(B + (int64_t)rank * a.M);
+            for (int i = 0; i < 8; ++i) {
+                const int rank = r0 + 8 * g + i;
+                raw[i] = u32x4{0, 0, 0, 0};
+                if (in && rank < a.r) raw[i] = *reinterpret_cast<const u32x4 *>(B + (int64_t)rank * a.M);
             }
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+#pragma unroll
+                for (int h = 0; h < 4; ++h)  // the low or the high halves of two rows' words
+                    b[s][j][h] = __builtin_amdgcn_perm(raw[2 * h + 1][j >> 1], raw[2 * h][j >> 1], j & 1 ? 0x07060302u : 0x05040100u);
         };
-        auto load_u = [&](int row0, int r0, float (&u)[STEPS]) __attribute__((always_inline)) {
+        auto load_u = [&](int row0, int r0, float (&u)[8]) __attribute__((always_inline)) {
             const int row = row0 + c;
 #pragma unroll
-            for (int s = 0; s < STEPS; ++s) {
-                const int rank = r0 + 4 * s + g;
-                u[s] = row < hi && rank < a.r ? a.U[(int64_t)rank * a.seg.rows + row] : 0.f;
+            for (int i = 0; i < 8; ++i) {
+                const int rank = r0 + 8 * g + i;
+                u[i] = row < hi && rank < a.r ? a.U[(int64_t)rank * a.seg.rows + row] : 0.f;
             }
         };
-        Raw8<YT> y[2][4];
         auto load_y0 = [&](int row0, Raw8<YT> (&out)[4]) __attribute__((always_inline)) {
             if (!a.Y0 || !in) return;
 #pragma unroll
             for (int e = 0; e < 4; ++e)
                 out[e].load(static_cast<const YT *>(a.Y0) + min(row0 + 4 * g + e, hi - 1) * a.ldy0 + m);
         };
-        auto rows16 = [&](int row0, float (&u)[STEPS], Raw8<YT> (&y0)[4]) __attribute__((always_inline)) {
+        // acc += the product of 32 ranks of U, whose rows have the exponent e
+        auto multiply = [&](float (&u)[8], int s, int e, f32x4 (&acc)[8]) __attribute__((always_inline)) {
+            float v[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) v[i] = kScaled ? ldexpf(u[i] * scale, 15 - e) : u[i] * scale;
+            u32x4 pl[NP];
+            split_planes<T>(v, pl);
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+#pragma unroll
+                for (int p = 0; p < NP; ++p) acc[j] = mfma<T>(pl[p], b[s][j], acc[j]);
+        };
+        auto largest = [&](float (&u)[8], float most) __attribute__((always_inline)) -> float {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) most = fmaxf(most, fabsf(u[i] * scale));
+            return most;
+        };
+        auto rows16 = [&](int row0, float (&u)[HELD][8], Raw8<YT> (&y0)[4]) __attribute__((always_inline)) {
             f32x4 acc[8] = {};
-            for (int r0 = 0;; r0 += 4 * STEPS) {
-                if constexpr (HOLD == 0) {
-                    load_b(r0);
-                    load_u(row0, r0, u);
-                }
+            int e = 0;
+            if constexpr (kScaled) {
+                float most = 0.f;
+                if constexpr (STEPS > 0) {
 #pragma unroll
-                for (int s = 0; s < STEPS; ++s) {
-                    asm volatile("" : "+v"(b[s]));  // converted anew for every 16 rows: all of B_n in fp32 would spill
-                    const float v = u[s] * scale;
-#pragma unroll
-                    for (int j = 0; j < 8; ++j)
-                        acc[j] = __builtin_amdgcn_mfma_f32_16x16x4f32(v, value16<T>((b[s][j >> 1] >> (16 * (j & 1))) & 0xffffu),
-                                                                     acc[j], 0, 0, 0);
+                    for (int s = 0; s < STEPS; ++s) most = largest(u[s], most);
+                } else {
+                    for (int r0 = 0; r0 < a.r; r0 += 32) {
+                        load_u(row0, r0, u[0]);
+                        most = largest(u[0], most);
+                    }
                 }
-                if (HOLD > 0 || r0 + 4 * STEPS >= a.r) break;
+                e = scale_exponent(most);
             }
-            if (!in) return;
+            if constexpr (STEPS > 0) {
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                const int row = row0 + 4 * g + e;
+                for (int s = 0; s < STEPS; ++s) multiply(u[s], s, e, acc);
+            } else {
+                for (int r0 = 0; r0 < a.r; r0 += 32) {
+                    load_b(0, r0);
+                    load_u(row0, r0, u[0]);
+                    multiply(u[0], 0, e, acc);
+                }
+            }
+            __builtin_amdgcn_sched_barrier(0);
+            asm volatile("s_nop 7" ::: "memory");  // the last products, before anything reads the sums
+            const float back = kScaled ? ldexpf(1.f, e - 15) : 1.f;
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                const int row = row0 + 4 * g + q;
+                const float f = kScaled ? __shfl(back, 4 * g + q, 64) : 1.f;
                 float o[8];
 #pragma unroll
-                for (int j = 0; j < 8; ++j) o[j] = acc[j][e] + (a.Y0 ? y0[e][j] : 0.f);
-                if (row < hi) stream8(static_cast<YT *>(a.Y) + row * a.ldy + m, o);
+                for (int j = 0; j < 8; ++j) o[j] = acc[j][q] * f + (a.Y0 ? y0[q][j] : 0.f);
+                if (in && row < hi) stream8(static_cast<YT *>(a.Y) + row * a.ldy + m, o);
             }
         };
-        float u[2][STEPS];
-        if constexpr (HOLD > 0) {
-            load_b(0);
-            load_u(lo, 0, u[0]);
-        }
-        load_y0(lo, y[0]);
+        Raw8<YT> y[2][4];
+        float u[2][HELD][8];
+        auto fetch = [&](int row0, float (&to)[HELD][8], Raw8<YT> (&y0)[4]) __attribute__((always_inline)) {
+#pragma unroll
+            for (int s = 0; s < STEPS; ++s) load_u(row0, 32 * s, to[s]);
+            load_y0(row0, y0);
+        };
+#pragma unroll
+        for (int s = 0; s < STEPS; ++s) load_b(s, 32 * s);
+        fetch(lo, u[0], y[0]);
         for (int row = lo; row < hi; row += 32) {
-            if constexpr (HOLD > 0) load_u(row + 16, 0, u[1]);
-            load_y0(row + 16, y[1]);
+            fetch(row + 16, u[1], y[1]);
             rows16(row, u[0], y[0]);
             if (row + 16 >= hi) break;
-            if constexpr (HOLD > 0) load_u(row + 32, 0, u[0]);
-            load_y0(row + 32, y[0]);
+            fetch(row + 32, u[0], y[0]);
             rows16(row + 16, u[1], y[1]);
         }
     });
@@ -431,42 +513,6 @@ struct GradArgs {
     Segments seg;
     int32_t K, r, splits, accumulate;
 };
-
-// V in planes of the 16-bit type that X has, so that the 16-bit instruction multiplies
-// it: three of bf16 (24 bits, at any scale), two of fp16 (22 bits below the largest value
-// of the rank's 32 rows, which the scale 2^(15 - e) takes into [2^14, 2^15)).
-template <typename T>
-struct Planes;
-template <>
-struct Planes<bf16_t> {
-    static constexpr int N = 3;
-    static constexpr bool kScaled = false;
-};
-template <>
-struct Planes<f16_t> {
-    static constexpr int N = 2;
-    static constexpr bool kScaled = true;
-};
-template <typename T, int N>
-__device__ __forceinline__ void split_planes(const float (&v)[8], u32x4 (&out)[N]) {
-    float r[8];
-#pragma unroll
-    for (int i = 0; i < 8; ++i) r[i] = v[i];
-#pragma unroll
-    for (int p = 0; p < N; ++p) {
-#pragma unroll
-        for (int h = 0; h < 4; ++h) {
-            uint32_t b[2];
-#pragma unroll
-            for (int q = 0; q < 2; ++q) {
-                b[q] = bits16<T>(r[2 * h + q]);
-                const float rest = r[2 * h + q] - value16<T>(b[q]);
-                r[2 * h + q] = fabsf(rest) < INFINITY ? rest : 0.f;  // nothing is left of an infinity or a NaN
-            }
-            out[p][h] = b[0] | (b[1] << 16);
-        }
-    }
-}
 
 // One adapter by 128 columns by 16 F ranks a workgroup, over one split of the adapter's
 // rows (columns first in the grid, so that every XCD gets its share of each adapter).
@@ -577,9 +623,7 @@ __global__ __launch_bounds__(256) void grad_kernel(GradArgs a) {
                 float most = 0.f;
 #pragma unroll
                 for (int i = 0; i < 8; ++i) most = fmaxf(most, fabsf(v[f][i]));
-                most = fmaxf(most, __shfl_xor(most, 16, 64));
-                most = fmaxf(most, __shfl_xor(most, 32, 64));
-                const int e = max(__builtin_amdgcn_frexp_expf(most), -110);
+                const int e = scale_exponent(most);  // of the rank's 32 rows
 #pragma unroll
                 for (int i = 0; i < 8; ++i) v[f][i] = ldexpf(v[f][i], 15 - e);
                 const float back = ldexpf(1.f, e - 15);
@@ -710,7 +754,7 @@ hipError_t shrink(int dtype, const ShrinkArgs &a, hipStream_t s) {
     return dtype == ZI_F16 ? go(f16_t{}) : go(bf16_t{});
 }
 
-constexpr int64_t kExpandGroups = 1024;
+constexpr int64_t kExpandGroups = 512;
 template <typename T, typename YT>
 hipError_t expand_typed(const ExpandArgs &a, bool rows, hipStream_t s) {
     if (rows)
@@ -723,9 +767,8 @@ hipError_t expand_typed(const ExpandArgs &a, bool rows, hipStream_t s) {
         auto go = [&](auto hold) {
             hipLaunchKernelGGL((expand_kernel<T, YT, decltype(hold)::value>), grid, dim3(256), 0, s, a, block);
         };
-        if (a.r <= 16) go(std::integral_constant<int, 4>{});
-        else if (a.r <= 32) go(std::integral_constant<int, 8>{});
-        else if (a.r <= 64) go(std::integral_constant<int, 16>{});
+        if (a.r <= 32) go(std::integral_constant<int, 1>{});
+        else if (a.r <= 64) go(std::integral_constant<int, 2>{});
         else go(std::integral_constant<int, 0>{});
     }
     return hipGetLastError();
