@@ -503,19 +503,27 @@ __global__ __launch_bounds__(256) void expand_row_kernel(ExpandArgs a) {
 
 // ---- grad ----------------------------------------------------------------------------------
 
-struct GradArgs {
+// One of the two gradients that a launch forms.
+struct GradOf {
     const float *V;     // [r][T]
     const uint16_t *X;  // [T][ldx]
     int64_t ldx;
     const float *scales;  // null: one
     float *G;             // [N][r][K]
-    float *part;          // [splits][N][r][K] where splits > 1
+    float *part;          // the first split's sums, [N][r][K], where there are several
+    int32_t K;
+};
+struct GradArgs {
+    GradOf of[2];
+    int64_t part_split;  // from one split's sums to the next one's
     Segments seg;
-    int32_t K, r, splits, accumulate;
+    int32_t tiles0;      // column tiles of of[0]
+    int32_t r, splits, accumulate;
 };
 
-// One adapter by 128 columns by 16 F ranks a workgroup, over one split of the adapter's
-// rows (columns first in the grid, so that every XCD gets its share of each adapter).
+// One adapter by 128 columns of one of the two gradients by 16 F ranks a workgroup, over
+// one split of the adapter's rows (columns first in the grid, so that every XCD gets its
+// share of each adapter).
 // Its four waves take chunks of 32 rows in turn, each by itself: the chunk's columns are
 // copied into the wave's part of LDS (16 bytes a lane, whole rows of 256 bytes), the
 // next chunk's while this one is multiplied, and read back across the rows
@@ -531,7 +539,11 @@ __global__ __launch_bounds__(256) void grad_kernel(GradArgs a) {
     const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int c = lane & 15, g = lane >> 4;
     const int n = blockIdx.y / a.splits, split = blockIdx.y % a.splits;
-    const int k0 = blockIdx.x * 128, r0 = blockIdx.z * (16 * F);
+    const bool second = (int)blockIdx.x >= a.tiles0;
+    const GradOf &d = a.of[second];
+    const int64_t ldx = d.ldx;
+    const int K = d.K, k0 = ((int)blockIdx.x - (second ? a.tiles0 : 0)) * 128, r0 = blockIdx.z * (16 * F);
+    const uint16_t *X = d.X + k0;
     char *mine = lds + wave * (2 * kStage);
     const uint32_t at = lds_addr(mine);
 
@@ -543,7 +555,7 @@ __global__ __launch_bounds__(256) void grad_kernel(GradArgs a) {
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
         const int row = 4 * i + g, col = ((((c >> 1) ^ swizzle(row)) << 1) | (c & 1)) * 8;
-        xo[i] = k0 + col < a.K ? (uint32_t)((row * a.ldx + col) * 2) : kOOB;
+        xo[i] = k0 + col < K ? (uint32_t)((row * ldx + col) * 2) : kOOB;
     }
     // fragment j (16 columns): this lane's part of rows 0 .. 3 of each eight; the others are 4 rows on
     const int kl = 8 * g + (c >> 2);
@@ -553,7 +565,7 @@ __global__ __launch_bounds__(256) void grad_kernel(GradArgs a) {
     // ranks past the last read the last one's values and are not stored
     const float *V[F];
 #pragma unroll
-    for (int f = 0; f < F; ++f) V[f] = a.V + (int64_t)min(r0 + 16 * f + c, a.r - 1) * a.seg.rows;
+    for (int f = 0; f < F; ++f) V[f] = d.V + (int64_t)min(r0 + 16 * f + c, a.r - 1) * a.seg.rows;
 
     // The chunks of this wave: the workers (waves of all splits) take the adapter's chunks
     // in turn, across its segments, so that short ones are shared out too (4508 rows in
@@ -582,7 +594,7 @@ __global__ __launch_bounds__(256) void grad_kernel(GradArgs a) {
         return true;
     };
     auto copy = [&](int stage) __attribute__((always_inline)) {
-        const rsrc_t rs = make_rsrc(reinterpret_cast<const char *>(a.X + t * a.ldx + k0));
+        const rsrc_t rs = make_rsrc(reinterpret_cast<const char *>(X + t * ldx));
         if (t + kChunk <= hi) {
 #pragma unroll
             for (int i = 0; i < 8; ++i) copy16(rs, at + stage * kStage + i * 1024, xo[i]);
@@ -666,9 +678,9 @@ __global__ __launch_bounds__(256) void grad_kernel(GradArgs a) {
     asm volatile("s_nop 7\n\ts_nop 7" ::: "memory");  // the last products, before anything reads the sums
 
     // the four waves' sums meet in LDS, one fragment of ranks at a time
-    const float scale = a.scales ? a.scales[n] : 1.f;
+    const float scale = d.scales ? d.scales[n] : 1.f;
     const bool whole = a.splits == 1;
-    float *out = (whole ? a.G : a.part + (int64_t)split * a.seg.adapters * a.r * a.K) + (int64_t)n * a.r * a.K;
+    float *out = (whole ? d.G : d.part + split * a.part_split) + (int64_t)n * a.r * K;
     f32x4(*sums)[8][64] = reinterpret_cast<f32x4(*)[8][64]>(lds);
 #pragma unroll
     for (int f = 0; f < F; ++f) {
@@ -684,22 +696,33 @@ __global__ __launch_bounds__(256) void grad_kernel(GradArgs a) {
 #pragma unroll
             for (int k = 1; k < 4; ++k) sum += sums[k][j][lane][wave];
             const int col = k0 + 16 * j + c;
-            if (col < a.K && rank < a.r) {
-                float *p = out + (int64_t)rank * a.K + col;
+            if (col < K && rank < a.r) {
+                float *p = out + (int64_t)rank * K + col;
                 *p = (whole && a.accumulate ? *p : 0.f) + sum * scale;
             }
         }
     }
 }
 
-// out[i] (+)= the sum of part[p][i] over the parts, in order.
-__global__ __launch_bounds__(256) void sum_parts_kernel(const float *part, int parts, int64_t n, float *out, int accumulate) {
-    const int64_t i = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 8;
-    const int64_t left = n - i;
+// out[i] (+)= the sum of part[p stride + i] over the parts p, in order, for two arrays,
+// one behind the other in each part: n values of out, n2 of out2 (0: none).
+__global__ __launch_bounds__(256) void sum_parts_kernel(const float *part, int parts, int64_t stride, int64_t n, float *out, int64_t n2,
+                                                        float *out2, int accumulate) {
+    const int64_t groups = (n + 7) / 8;
+    int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
+    const bool second = i >= groups;
+    if (second) {
+        i -= groups;
+        part += n;
+        out = out2;
+    }
+    i *= 8;
+    const int64_t left = (second ? n2 : n) - i;
+    if (left <= 0) return;
     float sum[8], v[8];
     load_n(part + i, left, sum);
     for (int p = 1; p < parts; ++p) {
-        load_n(part + p * n + i, left, v);
+        load_n(part + p * stride + i, left, v);
 #pragma unroll
         for (int e = 0; e < 8; ++e) sum[e] += v[e];
     }
@@ -730,11 +753,10 @@ int64_t parts_of(int64_t T, int64_t S, int64_t K) {
 uint64_t parts_bytes(int64_t T, int64_t r) { return round_up((uint64_t)max64(T, min64(kMostParts * T, 64 * 1024)) * (uint64_t)r * 4); }
 uint64_t u_bytes(int64_t T, int64_t r) { return round_up((uint64_t)T * (uint64_t)r * 4); }
 
-// Splits of the adapters' rows, so that a few adapters still occupy the chip.
+// Splits of the adapters' rows, so that a few adapters still occupy the chip (two
+// workgroups a compute unit), each of a thousand rows or more.
 constexpr int64_t kGradGroups = 512;
-int64_t splits_of(int64_t T, int64_t N, int64_t K) {
-    return max64(1, min64(kGradGroups / (N * ceil_div(K, 128)), ceil_div(T, 256)));
-}
+int64_t splits_of(int64_t T, int64_t N, int64_t tiles) { return max64(1, min64(kGradGroups / (N * tiles), ceil_div(T, 1024))); }
 uint64_t part_bytes(int64_t r) { return (uint64_t)kGradGroups * 128 * (uint64_t)r * 4; }
 
 template <typename T, int QF>
@@ -778,19 +800,18 @@ hipError_t expand(int dtype, int out_dtype, const ExpandArgs &a, bool rows, hipS
     return out_dtype == ZI_F32 ? expand_typed<bf16_t, float>(a, rows, s) : expand_typed<bf16_t, bf16_t>(a, rows, s);
 }
 
-hipError_t sum_parts(const float *part, int64_t parts, int64_t n, float *out, int accumulate, hipStream_t s) {
-    hipLaunchKernelGGL(sum_parts_kernel, dim3((unsigned)ceil_div(n, 2048)), dim3(256), 0, s, part, (int)parts, n, out,
-                       accumulate);
+hipError_t sum_parts(const float *part, int64_t parts, int64_t n, float *out, int64_t n2, float *out2, int accumulate, hipStream_t s) {
+    hipLaunchKernelGGL(sum_parts_kernel, dim3((unsigned)ceil_div(ceil_div(n, 8) + ceil_div(n2, 8), 256)), dim3(256), 0, s, part,
+                       (int)parts, n + n2, n, out, n2, out2, accumulate);
     return hipGetLastError();
 }
 
-hipError_t grad(int dtype, GradArgs a, hipStream_t s) {
-    a.splits = (int32_t)splits_of(a.seg.rows, a.seg.adapters, a.K);
+hipError_t grad(int dtype, const GradArgs &a, int64_t tiles, hipStream_t s) {
     auto go = [&](auto type, auto frags) {
         constexpr int F = decltype(frags)::value;
         hipLaunchKernelGGL((grad_kernel<decltype(type), F>),
-                           dim3((unsigned)ceil_div(a.K, 128), (unsigned)(a.seg.adapters * a.splits), (unsigned)ceil_div(a.r, 16 * F)),
-                           dim3(256), 0, s, a);
+                           dim3((unsigned)tiles, (unsigned)(a.seg.adapters * a.splits), (unsigned)ceil_div(a.r, 16 * F)), dim3(256), 0, s,
+                           a);
         return hipGetLastError();
     };
     auto sized = [&](auto type) {
@@ -799,7 +820,8 @@ hipError_t grad(int dtype, GradArgs a, hipStream_t s) {
     };
     const hipError_t e = dtype == ZI_F16 ? sized(f16_t{}) : sized(bf16_t{});
     if (e != hipSuccess || a.splits == 1) return e;
-    return sum_parts(a.part, a.splits, (int64_t)a.seg.adapters * a.r * a.K, a.G, a.accumulate, s);
+    const int64_t n = (int64_t)a.seg.adapters * a.r;
+    return sum_parts(a.of[0].part, a.splits, n * a.of[0].K, a.of[0].G, n * a.of[1].K, a.of[1].G, a.accumulate, s);
 }
 
 bool aligned(const void *p, uint64_t to) { return ((uintptr_t)p & (to - 1)) == 0; }
@@ -870,7 +892,7 @@ extern "C" zi_status zi_adapters_fwd(const zi_adapters *p, const void *X, const 
     a.parts = (int32_t)parts;
     const bool rows = a.block == 1;  // a workgroup of expand a row, which adds the parts
     hipError_t e = shrink(p->dtype, a, s);
-    if (e == hipSuccess && parts > 1 && !rows) e = sum_parts(parted, parts, p->T * p->r, u, 0, s);
+    if (e == hipSuccess && parts > 1 && !rows) e = sum_parts(parted, parts, p->T * p->r, u, 0, nullptr, 0, s);
     if (e == hipSuccess) {
         ExpandArgs b = {};
         b.U = rows ? a.U : u;
@@ -933,7 +955,7 @@ extern "C" zi_status zi_adapters_bwd(const zi_adapters *p, const void *X, const 
         a.block = block_of(p->T, S);
         a.parts = (int32_t)parts;
         e = shrink(p->dtype, a, s);
-        if (e == hipSuccess && parts > 1) e = sum_parts(parted, parts, p->T * p->r, dU, 0, s);
+        if (e == hipSuccess && parts > 1) e = sum_parts(parted, parts, p->T * p->r, dU, 0, nullptr, 0, s);
         if (e == hipSuccess && dX) {
             ExpandArgs b = {};
             b.U = dU;
@@ -950,24 +972,20 @@ extern "C" zi_status zi_adapters_bwd(const zi_adapters *p, const void *X, const 
             e = expand(p->dtype, p->out_dtype, b, a.block == 1, s);
         }
     }
-    auto one = [&](const float *V, const void *rows, int64_t ld, int64_t cols, const float *by, float *out) {
-        GradArgs a = {};
-        a.V = V;
-        a.X = static_cast<const uint16_t *>(rows);
-        a.ldx = ld;
-        a.scales = by;
-        a.G = out;
-        a.part = part;
-        a.seg = seg;
-        a.K = (int32_t)cols;
-        a.r = p->r;
-        a.accumulate = p->accumulate;
-        if (p->T == 0) a.seg.count = 0;  // zeros, or nothing added
-        return grad(p->dtype, a, s);
-    };
     if (e == hipSuccess && !(p->T == 0 && p->accumulate)) {
-        e = one(dU, X, p->ldx ? p->ldx : p->K, p->K, nullptr, dA);
-        if (e == hipSuccess) e = one(U, dY, p->ldy ? p->ldy : p->M, p->M, p->T == 0 ? nullptr : scales, dB);
+        const int64_t tiles0 = ceil_div(p->K, 128), tiles = tiles0 + ceil_div(p->M, 128);
+        GradArgs a = {};
+        a.of[0] = {dU, static_cast<const uint16_t *>(X), p->ldx ? p->ldx : p->K, nullptr, dA, part, (int32_t)p->K};
+        a.of[1] = {U, static_cast<const uint16_t *>(dY), p->ldy ? p->ldy : p->M, p->T == 0 ? nullptr : scales, dB,
+                   part + (int64_t)p->N * p->r * p->K, (int32_t)p->M};
+        a.part_split = (int64_t)p->N * p->r * (p->K + p->M);
+        a.seg = seg;
+        if (p->T == 0) a.seg.count = 0;  // zeros
+        a.tiles0 = (int32_t)tiles0;
+        a.r = p->r;
+        a.splits = (int32_t)splits_of(p->T, p->N, tiles);
+        a.accumulate = p->accumulate;
+        e = grad(p->dtype, a, tiles, s);
     }
     if (e != hipSuccess) return fail(ZI_ERR_HIP, "adapters backward: %s", hipGetErrorString(e));
     return ZI_OK;
