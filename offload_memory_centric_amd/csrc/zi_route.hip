@@ -81,6 +81,18 @@ __device__ __forceinline__ float logit_of(uint32_t k) {
     return __builtin_bit_cast(float, k & 0x80000000u ? k ^ 0x80000000u : ~k);
 }
 
+// e^x of x <= 0 for a sum that has a one in it: 2^(x log2 e), the product's rounding and
+// log2 e's own put back to first order, so that the error is an ulp or so of the
+// instruction's.  Below 2^-126 zero, and NaN is not kept.  (Six instructions for some 15 of
+// expf; of the choice among 22251 x 311 logits it takes 4 us off 20.)
+__device__ __forceinline__ float exp_below(float x) {
+    constexpr float kHi = 1.44269502f, kLo = 1.92596299e-8f;  // log2 e
+    x = fmaxf(x, -104.f);
+    const float y = x * kHi, rest = __builtin_fmaf(x, kLo, __builtin_fmaf(x, kHi, -y));
+    const float e = __builtin_amdgcn_exp2f(y);
+    return __builtin_fmaf(e, rest * 0.693147181f, e);
+}
+
 // The V logits of a lane's experts, -inf past the last one (n of them are left).
 template <int V, typename LT>
 __device__ __forceinline__ void load_logits(const LT *p, int n, float (&x)[V]) {
@@ -218,10 +230,10 @@ __device__ __forceinline__ void choose(const LT *logits, int64_t ldl, int64_t t0
             for (int j = lane; j < found; j += L) total += expf(__builtin_bit_cast(float, pick[j].hi) - top);
         } else {  // over all experts
 #pragma unroll
-            for (int v = 0; v < V; ++v) total += v < n ? expf(x[v] - top) : 0.f;
+            for (int v = 0; v < V; ++v) total += exp_below(x[v] - top);
         }
         total = lanes_sum<L>(total);
-        if (lanes_max<L>(bad)) total = NAN;
+        if (lanes_max<L>(bad) || top == INFINITY) total = NAN;
         if (t < t1) {
             for (int j = lane; j < k; j += L) {
                 const bool is = j < found;
@@ -334,7 +346,7 @@ __global__ __launch_bounds__(kOneThreads) void route_kernel(const LT *logits, in
 }
 
 // Block b: tokens [b step, (b + 1) step), its counts in row b of counts: bytes where a
-// block has 128 tokens (every other block reads them: 256 blocks and experts in 32 bits
+// block has at most 128 tokens (every other block reads them: 256 blocks and experts in 32 bits
 // took 10.3 us, most of it for the 64 MB).
 template <typename LT, int L, int V>
 __global__ __launch_bounds__(kThreads) void choose_kernel(const LT *logits, int64_t ldl, int64_t T, int64_t step, int E,
@@ -646,15 +658,18 @@ hipError_t with_type(int32_t d, F &&f) {
     return f(bf16_t{});
 }
 
-// Tokens a block: few enough that the chip is full, or that a block of more lanes a token
-// takes few turns, and blocks few enough to be counted by each other.  (130 tokens of 362
-// experts, k = 15: 32.5 us with 128 a block; 22251 of 311, k = 1: 31.8.)
-int64_t step_of(int64_t T, int E) {
-    if (T > kMostBlocks / 2 * kMaskTokens) return kMaskTokens * ceil_div(T, (int64_t)kMaskTokens * kMostBlocks);
-    const int64_t blocks = E > 256 ? kMostBlocks : kMostBlocks / 2;
-    int64_t step = 32;
-    while (step < kMaskTokens && ceil_div(T, step) > blocks) step *= 2;
-    return step;
+// Tokens a block: at most 128, if kMostBlocks blocks then suffice, so that a SIMD's waves
+// take the fewest turns with L lanes a token; of equal ones the fewest blocks, which are
+// counted by each other.  (22251 tokens of 311 experts, k = 1: 24.0 us, choice and places;
+// 28 with 128 tokens a block, 32 with 64.)
+int64_t step_of(int64_t T, int L) {
+    int64_t best = kMaskTokens * ceil_div(T, (int64_t)kMaskTokens * kMostBlocks), least = INT64_MAX;
+    if (best > kMaskTokens) return best;
+    for (int64_t step = kMaskTokens; step >= 32 && ceil_div(T, step) <= kMostBlocks; step -= 32) {
+        const int64_t turns = ceil_div(ceil_div(T, step), 256) * ceil_div(step * L, 256);
+        if (turns < least) best = step, least = turns;
+    }
+    return best;
 }
 
 bool known(int32_t d) { return d == ZI_F16 || d == ZI_BF16 || d == ZI_F32; }
@@ -734,7 +749,7 @@ extern "C" zi_status zi_route_fwd(const zi_route *r, const void *logits, int32_t
                                    r->normalize, ids, weights, offsets, rows, slots);
                 return hipGetLastError();
             }
-            const int64_t step = step_of(r->T, r->E);
+            const int64_t step = step_of(r->T, L);
             const dim3 blocks((unsigned)ceil_div(r->T, step));
             hipLaunchKernelGGL((choose_kernel<LT, L, V>), blocks, dim3(kThreads), 0, s, l, ldl, r->T, step, r->E, r->k,
                                r->normalize, ids, weights, workspace);
