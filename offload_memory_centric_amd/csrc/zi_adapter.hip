@@ -309,6 +309,11 @@ __device__ __forceinline__ void split_planes(const float (&v)[8], u32x4 (&out)[N
     }
 }
 
+// A value's part in the largest of those that share a scale: an infinity (or NaN) has
+// none, so that it takes no finite value past the type's range.
+__device__ __forceinline__ float largest_of(float most, float x) {
+    return fabsf(x) < INFINITY ? fmaxf(most, fabsf(x)) : most;
+}
 // The exponent e of that scale for the largest of `most` over the wave's lanes of equal
 // lane % 16 (not so low that 2^(e - 15) is no normal number).
 __device__ __forceinline__ int scale_exponent(float most) {
@@ -390,7 +395,7 @@ __global__ __launch_bounds__(256) void expand_kernel(ExpandArgs a, int block) {
         };
         auto largest = [&](float (&u)[8], float most) __attribute__((always_inline)) -> float {
 #pragma unroll
-            for (int i = 0; i < 8; ++i) most = fmaxf(most, fabsf(u[i] * scale));
+            for (int i = 0; i < 8; ++i) most = largest_of(most, u[i] * scale);
             return most;
         };
         auto rows16 = [&](int row0, float (&u)[HELD][8], Raw8<YT> (&y0)[4]) __attribute__((always_inline)) {
@@ -625,8 +630,8 @@ __global__ __launch_bounds__(256) void grad_kernel(GradArgs a) {
         load_v();
     }
     while (more) {
-        // this chunk is in LDS, its V in registers
-        asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+        // this chunk is in LDS, its V in registers, and the other stage has been read
+        asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
         u32x4 pl[F][NP];
         [[maybe_unused]] float unscale[F][4];
 #pragma unroll
@@ -634,7 +639,7 @@ __global__ __launch_bounds__(256) void grad_kernel(GradArgs a) {
             if constexpr (kScaled) {
                 float most = 0.f;
 #pragma unroll
-                for (int i = 0; i < 8; ++i) most = fmaxf(most, fabsf(v[f][i]));
+                for (int i = 0; i < 8; ++i) most = largest_of(most, v[f][i]);
                 const int e = scale_exponent(most);  // of the rank's 32 rows
 #pragma unroll
                 for (int i = 0; i < 8; ++i) v[f][i] = ldexpf(v[f][i], 15 - e);

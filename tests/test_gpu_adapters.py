@@ -228,6 +228,30 @@ def test_requests_do_not_reach_each_other(lengths):
     assert torch.equal(dX[c.edge[5]:], c.dX0[c.edge[5]:])
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+def test_infinities_beside_finite_values(dtype):
+    """An infinity and finite values of the other sign in one sum: the sum is the infinity, not NaN."""
+    from offload_memory_centric_amd import layers
+    T, K, M, r = 40, 64, 72, 2
+    one = lambda *shape: torch.ones(shape, dtype=DT[dtype], device="cuda")
+    X, dY, A, B = one(T, K), one(T, M), one(1, r, K), one(1, r, M)
+    A[0, 1] = -0.125
+    offsets, ids = torch.tensor([0, T], dtype=torch.int32, device="cuda"), torch.zeros(1, dtype=torch.int32, device="cuda")
+    # U = 64 and -8 times 6e36: the first is past fp32's range where it is scaled
+    scales = torch.full((1,), 6e36, device="cuda")
+    U, Y = torch.empty((r, T), device="cuda"), torch.empty((T, M), device="cuda")
+    layers.adapters_fwd(X, A, B, offsets, ids, scales, Y, layers.workspace(layers.adapters_fwd_bytes(T, r)), U=U)
+    assert torch.equal(U, torch.tensor([[64.0], [-8.0]], device="cuda").expand(r, T))
+    assert (Y == INF).all()
+    U = torch.full((r, T), -4.0, device="cuda")
+    U[0, 3] = INF
+    dA, dB = torch.empty((1, r, K), device="cuda"), torch.empty((1, r, M), device="cuda")
+    layers.adapters_bwd(X, dY, U, A, B, offsets, ids, torch.ones(1, device="cuda"), dA, dB,
+                        layers.workspace(layers.adapters_bwd_bytes(T, r)))
+    assert (dB[0, 0] == INF).all() and (dB[0, 1] == -4.0 * T).all()
+    assert (dA == 1.0 * M * T).all()
+
+
 def test_offsets_outside_the_rows():
     """Offsets that are not what they should be give rows another adapter or none; nothing outside is read or written."""
     from offload_memory_centric_amd import layers
