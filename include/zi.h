@@ -667,7 +667,10 @@ zi_status zi_tier_simulate_reads(const int64_t *trace, int64_t len, int32_t buff
  *
  * What a training step runs on the device around the tiled feed-forward block:
  * the token embedding that makes its input, the layer norm in front of it with
- * the residual sum, and the orthogonalised update of a weight's gradient.
+ * the residual sum, and the orthogonalised update of a weight's gradient; where the
+ * block is a mixture of experts, the router, the products grouped by expert and the
+ * sum of the experts' rows; and low-rank adapters of many requests beside a shared
+ * projection, such as a tiled linear.
  * They take no context: every launch goes to `stream` (a hipStream_t of the
  * current device, passed as void*; NULL: the null stream), in order with what
  * the caller enqueues there, and the calls return at once.  They allocate
@@ -676,7 +679,8 @@ zi_status zi_tier_simulate_reads(const int64_t *trace, int64_t len, int32_t buff
  * need no preparation and mean nothing afterwards; calls that may overlap (on
  * two streams) need one each.  Device pointers are aligned to their element;
  * rows are contiguous, and lie a stride of elements apart (0: as many as they
- * have).  ZI_ERR_ARG, ZI_ERR_SHAPE, ZI_ERR_ALIGN and ZI_ERR_BUDGET (workspace
+ * have).  Outputs overlap neither inputs nor each other, but where a call says that
+ * one may be the other.  ZI_ERR_ARG, ZI_ERR_SHAPE, ZI_ERR_ALIGN and ZI_ERR_BUDGET (workspace
  * too small) come before anything is enqueued, ZI_ERR_HIP when a launch fails. */
 
 /* A layer norm over rows of D elements. */

@@ -583,8 +583,8 @@ __device__ __forceinline__ void group_rows(const int32_t *offsets, int64_t total
     hi = min(max((int64_t)offsets[g + 1], lo), total);
 }
 
-// Row tiles of 2^shift... rows each: the tile of workgroup w among those of all
-// groups, tiles_q columns of tiles wide.  Every wave finds it by itself: a lane takes
+// The tile of workgroup w among those of all groups, in row tiles of TP rows that are
+// tiles_q tiles wide.  Every wave finds it by itself: a lane takes
 // a group, and a scan over the wave counts the row tiles before it.  False: no tile.
 struct GroupTile {
     int group, tp, tq;

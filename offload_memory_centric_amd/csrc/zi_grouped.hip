@@ -8,6 +8,13 @@
 // scan, so that nothing waits for the host.  Most run on the MFMA kernel of zi_gemm.h,
 // on macro-tiles of 256, 128 or 64 rows and columns; groups of a few rows, as in
 // serving, which only wait for their weights, on the kernel here.
+//
+// Long reductions run at the matrix cores' rate under the card's power (32768 rows of
+// 8 groups, 8192 x 32768 bf16, GeLU with both outputs: 12.8 ms, 1380 TFLOP/s).  With one
+// macro-tile of 256 a compute unit nothing overlaps its epilogue, so shorter ones lose
+// that share: dW of 16 groups, 32768 rows, 2048 x 8192 into fp32, 930 to 950 us, 1170
+// TFLOP/s; dX with GeLU' of 24 groups, 14211 rows, 5000 x 2048 fp16, 371 to 385 us, 770
+// TFLOP/s, of whose tiles a sixth are the groups' ragged ends.
 #include <hip/hip_runtime.h>
 #include <math.h>
 #include <stdint.h>
@@ -22,8 +29,9 @@ namespace {
 // a ring of its own in LDS, so that none waits for another before the end: steps of 64
 // values, whose copies fetch whole lines of 128 bytes (chunks permuted as RcOperand's),
 // three steps at a time, two workgroups a compute unit; rows past the group's are not
-// fetched.  (32 rows unevenly over 64 experts, 2048 x 1408 bf16: 33.4 us; with 64 columns
-// and four steps, one workgroup a unit, 42.8; one row, 8192 x 8192: 26.4 and 28.8.)  Each workgroup begins
+// fetched.  Bound by HBM, once W streams: 179 MB in 31.8 us are 5.6 TB/s.  (32 rows
+// unevenly over 64 experts, 2048 x 1408 bf16: 33.4 us; with 64 columns and four steps,
+// one workgroup a unit, 42.8; one row, 8192 x 8192: 26.4 and 28.8.)  Each workgroup begins
 // at another step: where W's rows are a power of two apart, the same columns of all rows
 // lie in few of the memory's channels.  The sums meet in LDS in a fixed order.
 template <typename T, int EPI>

@@ -4,9 +4,9 @@ Layer norm with the residual sum, the token embedding and its gradient, each
 in its forward and its backward call, and the orthogonalised update of a
 weight; for a block that is a mixture of experts the router, the products
 grouped by expert and the combination, and low-rank adapters beside the tiled
-linear, forward and backward; over caller-owned outputs; every step runs in libzi.so.  Calls enqueue on ``stream`` (a torch stream or a handle such
-as ``Context.streams[0]``; by default torch's current stream) and return at
-once.  As with any stream, tensors made on another one must be complete
+linear, forward and backward; over caller-owned outputs; every step runs in
+libzi.so.  Calls enqueue on ``stream`` (a torch stream or a handle such as
+``Context.streams[0]``; by default torch's current stream) and return at once.  As with any stream, tensors made on another one must be complete
 before, and be kept until the work is done.  A call's tensors and stream are of
 one device, which need not be the current one.
 """
