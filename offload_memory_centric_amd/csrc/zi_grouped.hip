@@ -148,10 +148,14 @@ hipError_t few(const GroupArgs &a, hipStream_t s) {
 // The macro-tile that takes least, and how long (us), by its rounds of workgroups on 256
 // compute units, of which each holds one tile of 256, two of 128 or four of 64.  A round
 // takes what the products of many shapes measured (us for a reduction of r thousand):
-// 19.1 r + 14, 12.6 r + 6 and 12 r + 5; a tile that has its unit to itself 16.5 r + 14,
-// 7.4 r + 5 and 6.2 r + 4.  Of a ragged operand's row tiles one a group is taken as half
-// full.  (Over 45 products of 1 to 64 groups the choice is 1.7 % slower than the best
-// tile on average; 20000 rows of 16 groups, 1024 x 1024: 74.0, 60.8 and 83.7 us forward.)
+// 19.1 r + 14, 12.6 r + 0.3 r^2 + 6 and 12 r + 0.3 r^2 + 5; a tile that has its unit to
+// itself 16.5 r + 14, 7.4 r + 5 and 6.2 r + 4.  (The smaller tiles of a long reduction
+// drift apart and share less in the L2s: 13570 rows of 31 groups, 24320 x 2048, 1463 us
+// with tiles of 256, 1773 with 128.)  A group's row tiles are estimated for sizes that
+// fall off exponentially: one at least, and half of one unused where there are many.
+// (8000 rows of 60 groups, 4096 x 1024: 196 us with 256, 158 with 128, as chosen; 20000
+// of 16, 1024 x 1024: 74.0 and 60.8, and 83.7 with 64.  Over 45 products of 1 to 64 groups
+// the choice takes 2 % longer than the best tile on average.)
 struct Choice {
     int tile;
     double us;
@@ -160,15 +164,16 @@ Choice tile_of(int64_t rows, int64_t cols, int64_t groups, double red, bool ragg
     const double r = red / 1000;
     Choice best = {256, 0};
     for (int tile = 256; tile >= 64; tile /= 2) {
-        const double row_tiles = ragged ? (double)rows / tile + 0.5 * (double)groups : (double)ceil_div(rows, tile) * (double)groups;
+        const double row_tiles =
+            (double)groups * (ragged ? 1 / (1 - exp(-(double)tile * (double)groups / (double)rows)) : (double)ceil_div(rows, tile));
         const double each = row_tiles * (double)ceil_div(cols, tile) / 256;  // tiles a compute unit
         double t;
         if (tile == 256) {
             t = each > 1 ? ceil(each - 0.05) * (19.1 * r + 14) : 16.5 * r + 14;
         } else if (tile == 128) {
-            t = each > 1 ? fmax(1, ceil(each / 2 - 0.05)) * (12.6 * r + 6) : 7.4 * r + 5;
+            t = each > 1 ? fmax(1, ceil(each / 2 - 0.05)) * (12.6 * r + 0.3 * r * r + 6) : 7.4 * r + 5;
         } else {
-            const double alone = 6.2 * r + 4, full = 12 * r + 5;
+            const double alone = 6.2 * r + 4, full = 12 * r + 0.3 * r * r + 5;
             t = each > 4 ? each / 4 * full : alone + (full - alone) * fmax(0, each - 1) / 3;
         }
         if (best.us == 0 || t < 0.93 * best.us) best = {tile, t};  // where they are close, the larger
