@@ -539,9 +539,9 @@ struct GradArgs {
 // copied into the wave's part of LDS (16 bytes a lane, whole rows of 256 bytes), the
 // next chunk's while this one is multiplied, and read back across the rows
 // (ds_read_b64_tr_b16); V comes to registers as eight rows of a rank a lane.  (32768 rows
-// of 8192 and 8192 with r = 32: 237 us, 4.5 TB/s, and 6 for the parts' sum; in two launches
-// 138 each.  In fp32, 16 x 16 x 4 at a time, each took 183, 109 of them the matrix cores'
-// at their rate.)
+// of 8192 and 8192 with r = 32: 237 us, 4.5 TB/s; in two launches with two splits 138 each,
+// and 6 for their sum.  In fp32, 16 x 16 x 4 at a time, each took 183, 109 of them the
+// matrix cores' at their rate.)
 template <typename T, int F>
 __global__ __launch_bounds__(256) void grad_kernel(GradArgs a) {
     constexpr int NP = Planes<T>::N;

@@ -1398,7 +1398,8 @@ void gemm_kernel(ARGS a, int tiles_p, int tiles_q) {
         // columns, and 2 QB lanes a row's whole part of the tile, so that every access
         // to memory is 256 bytes a row (QB = 8, 16 bits) where the accumulators' own
         // layout gives 32.  (Tiles of 256, reduction 512, us a tile: GeLU with both
-        // outputs 46.1 from the accumulators, GeLU's gradient 50.7.)  Each wave has its
+        // outputs 33.5, 46.1 from the accumulators; GeLU's gradient 34.7, 50.7; neither,
+        // 21.5: what GeLU adds is its instructions, with one wave a SIMD.)  Each wave has its
         // own part, whose accesses come in order; the ring's copies must have landed.
         constexpr int RSB = 16 * QB * 4 + 16, BUF = 16 * RSB;  // a row, sixteen rows
         static_assert(4 * 2 * BUF <= LDS_BYTES, "the waves' parts");
