@@ -25,6 +25,46 @@
 namespace zi {
 namespace {
 
+// The sums of the WAVES waves meet in LDS in a fixed order, and are stored: 16 QF columns
+// from q0 of the rows from p0.
+template <typename T, int EPI, int QF, int WAVES>
+__device__ __forceinline__ void few_store(const GroupArgs &a, const GroupTile &gt, int64_t q0, int64_t p0, const f32x4 (&acc)[QF],
+                                          char *lds) {
+    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+    f32x4(*sums)[QF][64] = reinterpret_cast<f32x4(*)[QF][64]>(lds);
+#pragma unroll
+    for (int i = 0; i < QF; ++i) sums[wave][i][lane] = acc[i];
+    __syncthreads();
+    for (int t = tid; t < QF * 64; t += 64 * WAVES) {
+        const int f = t >> 6, ln = t & 63;
+        f32x4 v = sums[0][f][ln];
+#pragma unroll
+        for (int k = 1; k < WAVES; ++k) v += sums[k][f][ln];
+        const int64_t q = q0 + 16 * f + 4 * (ln >> 4), p = p0 + (ln & 15);
+        if (p >= gt.hi || q >= a.cols) continue;
+        const int64_t off = p * a.ldc + q;
+        if constexpr (EPI == EPI_F32) {
+            *reinterpret_cast<f32x4 *>(static_cast<float *>(a.C) + off) = v;
+        } else {
+            if constexpr (EPI == EPI_DACT) {
+                const u32x2 pre = *reinterpret_cast<const u32x2 *>(a.pre + p * a.ldpre + q);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) v[e] *= gelu_slope_f32(value16<T>((pre[e >> 1] >> (16 * (e & 1))) & 0xffffu));
+            }
+            uint32_t b[4], h[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                b[e] = bits16<T>(v[e]);
+                h[e] = EPI == EPI_ACT ? bits16<T>(gelu_f32(v[e])) : b[e];
+            }
+            *reinterpret_cast<u32x2 *>(static_cast<uint16_t *>(a.C) + off) = u32x2{h[0] | (h[1] << 16), h[2] | (h[3] << 16)};
+            if (EPI == EPI_ACT && a.C2)
+                *reinterpret_cast<u32x2 *>(static_cast<uint16_t *>(a.C2) + p * a.ldpre + q) =
+                    u32x2{b[0] | (b[1] << 16), b[2] | (b[3] << 16)};
+        }
+    }
+}
+
 // 16 rows of one group by 32 columns.  The four waves share the reduction, each with
 // a ring of its own in LDS, so that none waits for another before the end: steps of 64
 // values, whose copies fetch whole lines of 128 bytes (chunks permuted as RcOperand's),
@@ -98,33 +138,67 @@ __global__ __launch_bounds__(256) void few_rows_kernel(GroupArgs a, int tiles_q)
     // every copy has landed and every read returned before the rings hold the sums
     __builtin_amdgcn_sched_barrier(0);
     asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier\n\ts_nop 7\n\ts_nop 7" ::: "memory");
-    f32x4(*sums)[QF][64] = reinterpret_cast<f32x4(*)[QF][64]>(lds);
+    few_store<T, EPI, QF, 4>(a, gt, q0, p0, acc, lds);
+}
+
+// dX of a few rows: 16 rows of one group by 32 columns, whose eight waves share the
+// reduction over W's rows, each with a ring of its own of chunks of 32 of them: 64 bytes
+// of each, read back across the rows (ds_read_b64_tr_b16), and the same values of dY's
+// rows.  Bound by what one workgroup's 120 KB in flight fetch where tiles are few, which
+// a macro-tile of 64 takes longer over.  (21 rows of 2 groups, 22488 -> 160 bf16: 46 us,
+// 146 with tiles of 64.)
+template <typename T, int EPI>
+__global__ __launch_bounds__(512) void few_rows_dx_kernel(GroupArgs a, int tiles_q) {
+    constexpr int QF = 2, DEPTH = 6, kChunk = 32, WB = kChunk * 64, STAGE = WB + 16 * 64, NC = 3;
+    __shared__ __attribute__((aligned(1024))) char lds[8 * DEPTH * STAGE];
+    GroupTile gt;
+    if (!find_group_tile<16>(a.offsets, a.groups, a.total, blockIdx.x, tiles_q, 32, gt)) return;
+    const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int c = lane & 15, g = lane >> 4, row16 = lane >> 2, piece = (lane & 3) * 8;
+    const int64_t q0 = (int64_t)gt.tq * (16 * QF), p0 = gt.lo + (int64_t)gt.tp * 16;
+    const int group = __builtin_amdgcn_readfirstlane(gt.group);
+    const uint16_t *W = static_cast<const uint16_t *>(a.Q) + group * a.q_group + q0;
+    const rsrc_t yr = make_rsrc(reinterpret_cast<const char *>(static_cast<const uint16_t *>(a.P) + p0 * a.ldp));
+    const int red = (int)a.red, all = (red + kChunk - 1) / kChunk;
+    const int from = all * wave / 8, steps = all * (wave + 1) / 8 - from;
+    const int turn = steps > 0 ? (int)(blockIdx.x * 5u % (unsigned)steps) : 0;
+    const uint32_t at = lds_addr(lds) + (uint32_t)(wave * DEPTH * STAGE);
+    // a copy is 16 rows of 64 bytes
+    const uint32_t wo = q0 + piece < a.cols ? (uint32_t)((row16 * a.ldq + piece) * 2) : kOOB, w16 = (uint32_t)(32 * a.ldq);
+    const uint32_t yo = p0 + row16 < gt.hi ? (uint32_t)((row16 * a.ldp + piece) * 2) : kOOB;
+    const uint32_t fw = (uint32_t)((8 * g + (c >> 2)) * 64 + 8 * (c & 3)), fy = (uint32_t)(WB + c * 64 + 16 * g);
+
+    auto issue = [&](int s) __attribute__((always_inline)) {  // past the last step: zeros
+        const uint32_t stage = at + (uint32_t)(s % DEPTH) * STAGE;
+        const int turned = s + turn < steps ? s + turn : s + turn - steps;
+        const int m0 = s < steps ? (from + turned) * kChunk : 0, left = s < steps ? red - m0 : 0;
+        const rsrc_t wr = make_rsrc(reinterpret_cast<const char *>(W + m0 * a.ldq));
+        copy16(wr, stage, row16 < left ? wo : kOOB);
+        copy16(wr, stage + 1024, 16 + row16 < left ? wo + w16 : kOOB);
+        copy16(yr, stage + WB, piece < left ? yo + (uint32_t)(m0 * 2) : kOOB);
+    };
+    f32x4 acc[QF] = {};
 #pragma unroll
-    for (int i = 0; i < QF; ++i) sums[wave][i][lane] = acc[i];
-    __syncthreads();
-    for (int t = tid; t < QF * 64; t += 256) {
-        const int f = t >> 6, ln = t & 63;
-        f32x4 v = sums[0][f][ln];
+    for (int s = 0; s < DEPTH - 1; ++s) issue(s);
+    for (int s = 0; s < steps; ++s) {
+        // step s has landed, and step s - 1 has been read
+        asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" ::"n"((DEPTH - 2) * NC) : "memory");
+        issue(s + DEPTH - 1);
+        const uint32_t stage = at + (uint32_t)(s % DEPTH) * STAGE;
+        const u32x4 y = *reinterpret_cast<const __attribute__((address_space(3))) u32x4 *>((uintptr_t)(stage + fy));
 #pragma unroll
-        for (int k = 1; k < 4; ++k) v += sums[k][f][ln];
-        const int64_t q = q0 + 16 * f + 4 * (ln >> 4), p = p0 + (ln & 15);
-        if (p >= gt.hi || q >= a.cols) continue;
-        const int64_t off = p * a.ldc + q;
-        if constexpr (EPI == EPI_F32) {
-            *reinterpret_cast<f32x4 *>(static_cast<float *>(a.C) + off) = v;
-        } else {
-            uint32_t b[4], h[4];
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                b[e] = bits16<T>(v[e]);
-                h[e] = EPI == EPI_ACT ? bits16<T>(gelu_f32(v[e])) : b[e];
-            }
-            *reinterpret_cast<u32x2 *>(static_cast<uint16_t *>(a.C) + off) = u32x2{h[0] | (h[1] << 16), h[2] | (h[3] << 16)};
-            if (EPI == EPI_ACT && a.C2)
-                *reinterpret_cast<u32x2 *>(static_cast<uint16_t *>(a.C2) + p * a.ldpre + q) =
-                    u32x2{b[0] | (b[1] << 16), b[2] | (b[3] << 16)};
+        for (int i = 0; i < QF; ++i) {
+            const u32x2 w0 = __builtin_bit_cast(u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+                                                           (__attribute__((address_space(3))) s16x4 *)(uintptr_t)(stage + fw + 32 * i)));
+            const u32x2 w1 = __builtin_bit_cast(u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+                                                           (__attribute__((address_space(3))) s16x4 *)(uintptr_t)(stage + fw + 32 * i + 256)));
+            acc[i] = mfma<T>(u32x4{w0[0], w0[1], w1[0], w1[1]}, y, acc[i]);
         }
     }
+    // every copy has landed and every read returned before the rings hold the sums
+    __builtin_amdgcn_sched_barrier(0);
+    asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier\n\ts_nop 7\n\ts_nop 7" ::: "memory");
+    few_store<T, EPI, QF, 8>(a, gt, q0, p0, acc, lds);
 }
 
 int64_t ceil_div(int64_t x, int64_t y) { return (x + y - 1) / y; }
@@ -138,6 +212,20 @@ hipError_t run_few(const GroupArgs &a, hipStream_t s) {
     if (grid > INT32_MAX / 256) return hipErrorInvalidValue;
     hipLaunchKernelGGL((few_rows_kernel<T, EPI>), dim3((unsigned)grid), dim3(256), 0, s, a, (int)tiles_q);
     return hipGetLastError();
+}
+template <typename T, int EPI>
+hipError_t run_few_dx(const GroupArgs &a, hipStream_t s) {
+    const int64_t tiles_q = ceil_div(a.cols, 32);
+    const int64_t rows = a.total / 16 + min64(a.groups, a.total);
+    const int64_t grid = ceil_div(rows * tiles_q, 8) * 8;
+    if (grid > INT32_MAX / 512) return hipErrorInvalidValue;
+    hipLaunchKernelGGL((few_rows_dx_kernel<T, EPI>), dim3((unsigned)grid), dim3(512), 0, s, a, (int)tiles_q);
+    return hipGetLastError();
+}
+template <typename T>
+hipError_t few_dx(const GroupArgs &a, hipStream_t s) {
+    if (a.pre) return run_few_dx<T, EPI_DACT>(a, s);
+    return a.out_f32 ? run_few_dx<T, EPI_F32>(a, s) : run_few_dx<T, EPI_LP>(a, s);
 }
 template <typename T>
 hipError_t few(const GroupArgs &a, hipStream_t s) {
@@ -182,15 +270,28 @@ Choice tile_of(int64_t rows, int64_t cols, int64_t groups, double red, bool ragg
 }
 
 // Whether few_rows_kernel takes less than the best macro-tile: it reads W once for every
-// 16 rows, at 8.7 TB/s from the L2s, and from memory at 5.1 TB/s, the macro-tiles at 4.2.
+// 16 rows, at 8.7 TB/s from the L2s, and from memory at 5.1 TB/s, the macro-tiles at 4.2;
+// a round of its workgroups takes 3 us besides.
 // (us, few rows and best tile: 128 rows of 64 groups, 2048 x 1408, 72.1 and 98.7; 2 rows
 // of 8, 8192 x 4096, 26.5, 56.3; 128 rows of 8, 4096 x 2048, 25.5, 36.0; 256 rows of them
 // 45.2, 36.8.)
 bool few_rows(int64_t R, int64_t K, int64_t M, int64_t live, double best_us) {
     const double tiles = R <= 16 * live ? (double)live : (double)R / 16 + 0.5 * (double)live;
     const double weights = (double)live * (double)K * (double)M * 2e-6;  // MB
-    const double t = 5 + tiles * (double)ceil_div(M, 32) * 48 * (double)K * 2e-6 / 8.7;
+    const double groups = tiles * (double)ceil_div(M, 32);  // workgroups, of which a compute unit holds two
+    const double t = fmax(3 * ceil(groups / 512), 5 + groups * 48 * (double)K * 2e-6 / 8.7);
     return fmax(t, weights / 5.1) < fmax(best_us, weights / 4.2);
+}
+
+// Whether few_rows_dx_kernel takes less than the best macro-tile: a workgroup takes 3 us
+// and 1.2 ns for one of W's rows, all of them together their 64 bytes at 3.5 TB/s.  (us, few rows and
+// best tile: 10 rows of one group, 9568 -> 6768, 28.2 and 63.5; 25 of 18, 6128 -> 88, 11.0
+// and 25.5; one, 8192 -> 8192, 42.7 and 47.8; 32 rows of 64, 2048 -> 1408, 45.8 and 29.8;
+// 500 of 4, 8192 -> 512, 53.0 and 57.5, of which it takes the tile.)
+bool few_rows_dx(int64_t R, int64_t K, int64_t M, int64_t live, double best_us) {
+    const double row_tiles = R <= 16 * live ? (double)live : (double)R / 16 + 0.5 * (double)live;
+    const double tiles = row_tiles * (double)ceil_div(K, 32);
+    return 2 + fmax(ceil(tiles / 256) * (3 + 1.2e-3 * (double)M), 3 + tiles * 64e-6 / 3.5 * (double)M) < best_us;
 }
 
 bool aligned(const void *p, uint64_t to) { return ((uintptr_t)p & (to - 1)) == 0; }
@@ -291,7 +392,13 @@ extern "C" zi_status zi_grouped_dx(const zi_grouped *g, const void *dY, const vo
     a.cols = g->K;
     a.red = g->M;
     hipStream_t s = static_cast<hipStream_t>(stream);
-    const hipError_t e = launch_grouped_dx(g->dtype, tile_of(g->R, g->K, min64(g->E, g->R), (double)g->M, true).tile, a, s);
+    const int64_t live = min64(g->E, g->R);
+    const Choice best = tile_of(g->R, g->K, live, (double)g->M, true);
+    hipError_t e;
+    if (few_rows_dx(g->R, g->K, g->M, live, best.us))
+        e = g->dtype == ZI_F16 ? few_dx<_Float16>(a, s) : few_dx<__bf16>(a, s);
+    else
+        e = launch_grouped_dx(g->dtype, best.tile, a, s);
     if (e != hipSuccess) return fail(ZI_ERR_HIP, "grouped input gradient: %s", hipGetErrorString(e));
     return ZI_OK;
 }

@@ -221,6 +221,22 @@ def test_larger(sizes, K, M):
     c.dw(layers, "f16")
 
 
+# input gradients of few rows over a long reduction: one tile and several, ends inside a step of 32 and a tile of 16 x 32
+@pytest.mark.parametrize("sizes,K,M", [([21], 160, 5000), ([3, 0, 16, 17, 1, 40], 88, 1704), ([1], 520, 4104), ([9, 2], 1032, 2000),
+                                       ([2, 5, 0, 1], 8, 648), ([16], 2048, 2048)])
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
+def test_input_gradient_of_few_rows(sizes, K, M, dtype):
+    from offload_memory_centric_amd import layers
+    say("grouped dX of few rows", sizes, K, M, dtype)
+    c = Case(sizes, K, M, dtype, pad=8, whole=True, front=3)
+    for out in (dtype, "f32"):
+        c.dx(layers, out, exact=True)
+    c = Case(sizes, K, M, dtype, pad=16, seed=5)
+    c.dx(layers, dtype, gelu=True)
+    c.dx(layers, dtype)
+    c.dx(layers, "f32")
+
+
 def test_gelu_over_its_range():
     """Every finite fp16 value as A, forward and backward, by products with one."""
     from offload_memory_centric_amd import layers
