@@ -7,7 +7,7 @@
 // The offsets stay on the device: a workgroup finds its tile among all groups' by a
 // scan, so that nothing waits for the host.  Most run on the MFMA kernel of zi_gemm.h,
 // on macro-tiles of 256, 128 or 64 rows and columns; groups of a few rows, as in
-// serving, which only wait for their weights, on the kernel here.
+// serving, which only wait for their weights, on the kernels here (forward and dX).
 //
 // Long reductions run at the matrix cores' rate under the card's power (32768 rows of
 // 8 groups, 8192 x 32768 bf16, GeLU with both outputs: 12.8 ms, 1380 TFLOP/s).  With one
