@@ -891,7 +891,7 @@ zi_status zi_adapters_fwd(const zi_adapters *adapters, const void *X, const void
 /* From the forward's U, with dU = scales[n] B_n dY^T: dX = RNE(dX0 + dU^T A_n) (dX NULL:
  * not formed; dX0 NULL: zero; it may be dX itself), dA_n (+)= sum dU X and
  * dB_n (+)= scales[n] sum U dY over the rows of adapter n (fp32, the same bits every
- * time; zero, or as they were, for adapters without rows). */
+ * time; zero, or as they were, for adapters without rows, whatever their scales). */
 uint64_t zi_adapters_bwd_bytes(int64_t T, int32_t r);
 zi_status zi_adapters_bwd(const zi_adapters *adapters, const void *X, const void *dY, const float *U, const void *A,
                           const void *B, const int32_t *offsets, const int32_t *ids, const float *scales,

@@ -548,6 +548,7 @@ __global__ __launch_bounds__(256) void grad_kernel(GradArgs a) {
     constexpr bool kScaled = Planes<T>::kScaled;
     constexpr int kChunk = 32, kRowB = 256, kStage = kChunk * kRowB;
     __shared__ __attribute__((aligned(1024))) char lds[4 * 2 * kStage];
+    __shared__ int any[4];  // of each wave: it has multiplied rows
     const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int c = lane & 15, g = lane >> 4;
     const int n = blockIdx.y / a.splits, split = blockIdx.y % a.splits;
@@ -632,6 +633,7 @@ __global__ __launch_bounds__(256) void grad_kernel(GradArgs a) {
     f32x4 acc[F][8] = {};
     int stage = 0;
     bool more = next();
+    if (lane == 0) any[wave] = more;
     if (more) {
         copy(0);
         load_v();
@@ -691,7 +693,10 @@ __global__ __launch_bounds__(256) void grad_kernel(GradArgs a) {
 
     // the four waves' sums meet in LDS, one fragment of ranks at a time
     const float scale = d.scales ? d.scales[n] : 1.f;
-    const bool whole = a.splits == 1;
+    const bool whole = a.splits == 1, adds = whole && a.accumulate;
+    // Without rows nothing is scaled, whatever the scale; -0 added to what was there
+    // leaves its bits.
+    const float none = a.accumulate ? -0.f : 0.f;
     float *out = (whole ? d.G : d.part + split * a.part_split) + (int64_t)n * a.r * K;
     f32x4(*sums)[8][64] = reinterpret_cast<f32x4(*)[8][64]>(lds);
 #pragma unroll
@@ -700,6 +705,7 @@ __global__ __launch_bounds__(256) void grad_kernel(GradArgs a) {
 #pragma unroll
         for (int j = 0; j < 8; ++j) sums[wave][j][lane] = acc[f][j];
         __syncthreads();
+        const bool rows = any[0] | any[1] | any[2] | any[3];
         // thread (lane, wave): rank 4 (lane / 16) + wave of the fragment, columns 16 j + lane % 16
         const int rank = r0 + 16 * f + 4 * g + wave;
 #pragma unroll
@@ -710,7 +716,8 @@ __global__ __launch_bounds__(256) void grad_kernel(GradArgs a) {
             const int col = k0 + 16 * j + c;
             if (col < K && rank < a.r) {
                 float *p = out + (int64_t)rank * K + col;
-                *p = (whole && a.accumulate ? *p : 0.f) + sum * scale;
+                if (rows) *p = (adds ? *p : 0.f) + sum * scale;
+                else if (!adds) *p = none;
             }
         }
     }
