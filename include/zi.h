@@ -814,7 +814,9 @@ zi_status zi_route_bwd(const zi_route *route, const void *logits, const int32_t 
  * in device memory, ascending; what lies outside [0, R] is left out) and the weight
  * W_e [M x K], out-major as the tiled linear's.  Rows in no group are neither read nor
  * written.  K, M and the strides are multiples of 8, matrices 16-byte aligned.  Sums
- * are held in fp32 and rounded once. */
+ * are held in fp32 and rounded once.  A launch has at most 2^23 - 8 tiles of 256 x 256,
+ * more are ZI_ERR_SHAPE: the forward floor(R / 256) + min(E, R) by ceil(M / 256) of them,
+ * dX the same by ceil(K / 256), dW E by ceil(M / 256) by ceil(K / 256). */
 #define ZI_GROUPS_MOST 4096
 typedef struct {
     int64_t R;            /* rows: 0 .. 2^30                                             */

@@ -16,9 +16,9 @@
 // TFLOP/s; dX with GeLU' of 24 groups, 14211 rows, 5000 x 2048 fp16, 371 to 385 us, 770
 // TFLOP/s, of whose tiles a sixth are the groups' ragged ends.
 #include <hip/hip_runtime.h>
-#include <math.h>
 #include <stdint.h>
 
+#include "zi_grouped_choice.h"
 #include "zi_host.h"
 #include "zi_stream.h"
 
@@ -201,25 +201,16 @@ __global__ __launch_bounds__(512) void few_rows_dx_kernel(GroupArgs a, int tiles
     few_store<T, EPI, QF, 8>(a, gt, q0, p0, acc, lds);
 }
 
-int64_t ceil_div(int64_t x, int64_t y) { return (x + y - 1) / y; }
-int64_t min64(int64_t x, int64_t y) { return x < y ? x : y; }
-
 template <typename T, int EPI>
 hipError_t run_few(const GroupArgs &a, hipStream_t s) {
-    const int64_t tiles_q = ceil_div(a.cols, 32);
-    const int64_t rows = a.total / 16 + min64(a.groups, a.total);
-    const int64_t grid = ceil_div(rows * tiles_q, 8) * 8;
-    if (grid > INT32_MAX / 256) return hipErrorInvalidValue;
-    hipLaunchKernelGGL((few_rows_kernel<T, EPI>), dim3((unsigned)grid), dim3(256), 0, s, a, (int)tiles_q);
+    const int64_t grid = row_grid(a.total, a.groups, a.cols, 16, 32);
+    hipLaunchKernelGGL((few_rows_kernel<T, EPI>), dim3((unsigned)grid), dim3(256), 0, s, a, (int)ceil_div(a.cols, 32));
     return hipGetLastError();
 }
 template <typename T, int EPI>
 hipError_t run_few_dx(const GroupArgs &a, hipStream_t s) {
-    const int64_t tiles_q = ceil_div(a.cols, 32);
-    const int64_t rows = a.total / 16 + min64(a.groups, a.total);
-    const int64_t grid = ceil_div(rows * tiles_q, 8) * 8;
-    if (grid > INT32_MAX / 512) return hipErrorInvalidValue;
-    hipLaunchKernelGGL((few_rows_dx_kernel<T, EPI>), dim3((unsigned)grid), dim3(512), 0, s, a, (int)tiles_q);
+    const int64_t grid = row_grid(a.total, a.groups, a.cols, 16, 32);
+    hipLaunchKernelGGL((few_rows_dx_kernel<T, EPI>), dim3((unsigned)grid), dim3(512), 0, s, a, (int)ceil_div(a.cols, 32));
     return hipGetLastError();
 }
 template <typename T>
@@ -231,67 +222,6 @@ template <typename T>
 hipError_t few(const GroupArgs &a, hipStream_t s) {
     if (a.act) return run_few<T, EPI_ACT>(a, s);
     return a.out_f32 ? run_few<T, EPI_F32>(a, s) : run_few<T, EPI_LP>(a, s);
-}
-
-// The macro-tile that takes least, and how long (us), by its rounds of workgroups on 256
-// compute units, of which each holds one tile of 256, two of 128 or four of 64.  A round
-// takes what the products of many shapes measured (us for a reduction of r thousand):
-// 19.1 r + 14, 12.6 r + 0.3 r^2 + 6 and 12 r + 0.3 r^2 + 5; a tile that has its unit to
-// itself 16.5 r + 14, 7.4 r + 5 and 6.2 r + 4.  (The smaller tiles of a long reduction
-// drift apart and share less in the L2s: 13570 rows of 31 groups, 24320 x 2048, 1463 us
-// with tiles of 256, 1773 with 128.)  A group's row tiles are estimated for sizes that
-// fall off exponentially: one at least, and half of one unused where there are many.
-// (8000 rows of 60 groups, 4096 x 1024: 196 us with 256, 158 with 128, as chosen; 20000
-// of 16, 1024 x 1024: 74.0 and 60.8, and 83.7 with 64.  Over 45 products of 1 to 64 groups
-// the choice takes 2 % longer than the best tile on average.)
-struct Choice {
-    int tile;
-    double us;
-};
-Choice tile_of(int64_t rows, int64_t cols, int64_t groups, double red, bool ragged) {
-    const double r = red / 1000;
-    Choice best = {256, 0};
-    for (int tile = 256; tile >= 64; tile /= 2) {
-        const double row_tiles =
-            (double)groups * (ragged ? 1 / (1 - exp(-(double)tile * (double)groups / (double)rows)) : (double)ceil_div(rows, tile));
-        const double each = row_tiles * (double)ceil_div(cols, tile) / 256;  // tiles a compute unit
-        double t;
-        if (tile == 256) {
-            t = each > 1 ? ceil(each - 0.05) * (19.1 * r + 14) : 16.5 * r + 14;
-        } else if (tile == 128) {
-            t = each > 1 ? fmax(1, ceil(each / 2 - 0.05)) * (12.6 * r + 0.3 * r * r + 6) : 7.4 * r + 5;
-        } else {
-            const double alone = 6.2 * r + 4, full = 12 * r + 0.3 * r * r + 5;
-            t = each > 4 ? each / 4 * full : alone + (full - alone) * fmax(0, each - 1) / 3;
-        }
-        if (best.us == 0 || t < 0.93 * best.us) best = {tile, t};  // where they are close, the larger
-    }
-    return best;
-}
-
-// Whether few_rows_kernel takes less than the best macro-tile: it reads W once for every
-// 16 rows, at 8.7 TB/s from the L2s, and from memory at 5.1 TB/s, the macro-tiles at 4.2;
-// a round of its workgroups takes 3 us besides.
-// (us, few rows and best tile: 128 rows of 64 groups, 2048 x 1408, 72.1 and 98.7; 2 rows
-// of 8, 8192 x 4096, 26.5, 56.3; 128 rows of 8, 4096 x 2048, 25.5, 36.0; 256 rows of them
-// 45.2, 36.8.)
-bool few_rows(int64_t R, int64_t K, int64_t M, int64_t live, double best_us) {
-    const double tiles = R <= 16 * live ? (double)live : (double)R / 16 + 0.5 * (double)live;
-    const double weights = (double)live * (double)K * (double)M * 2e-6;  // MB
-    const double groups = tiles * (double)ceil_div(M, 32);  // workgroups, of which a compute unit holds two
-    const double t = fmax(3 * ceil(groups / 512), 5 + groups * 48 * (double)K * 2e-6 / 8.7);
-    return fmax(t, weights / 5.1) < fmax(best_us, weights / 4.2);
-}
-
-// Whether few_rows_dx_kernel takes less than the best macro-tile: a workgroup takes 3 us
-// and 1.2 ns for one of W's rows, all of them together their 64 bytes at 3.5 TB/s.  (us, few rows and
-// best tile: 10 rows of one group, 9568 -> 6768, 28.2 and 63.5; 25 of 18, 6128 -> 88, 11.0
-// and 25.5; one, 8192 -> 8192, 42.7 and 47.8; 32 rows of 64, 2048 -> 1408, 45.8 and 29.8;
-// 500 of 4, 8192 -> 512, 53.0 and 57.5, of which it takes the tile.)
-bool few_rows_dx(int64_t R, int64_t K, int64_t M, int64_t live, double best_us) {
-    const double row_tiles = R <= 16 * live ? (double)live : (double)R / 16 + 0.5 * (double)live;
-    const double tiles = row_tiles * (double)ceil_div(K, 32);
-    return 2 + fmax(ceil(tiles / 256) * (3 + 1.2e-3 * (double)M), 3 + tiles * 64e-6 / 3.5 * (double)M) < best_us;
 }
 
 bool aligned(const void *p, uint64_t to) { return ((uintptr_t)p & (to - 1)) == 0; }
@@ -312,6 +242,11 @@ zi_status check(const zi_grouped *g) {
     if (g->dtype != ZI_F16 && g->dtype != ZI_BF16) return fail(ZI_ERR_ARG, "dtype %d: fp16 or bf16", g->dtype);
     if (g->out_dtype != g->dtype && g->out_dtype != ZI_F32) return fail(ZI_ERR_ARG, "out_dtype %d: dtype or fp32", g->out_dtype);
     return ZI_OK;
+}
+
+zi_status too_many_tiles(const zi_grouped *g) {
+    return fail(ZI_ERR_SHAPE, "R = %lld, K = %lld, M = %lld, E = %d: more than 2^23 - 8 tiles of 256 x 256", (long long)g->R,
+                (long long)g->K, (long long)g->M, g->E);
 }
 
 // What the products share.
@@ -357,13 +292,13 @@ extern "C" zi_status zi_grouped_fwd(const zi_grouped *g, const void *X, const vo
     a.cols = g->M;
     a.red = g->K;
     hipStream_t s = static_cast<hipStream_t>(stream);
-    const int64_t live = min64(g->E, g->R);
-    const Choice best = tile_of(g->R, g->M, live, (double)g->K, true);
+    const int tile = grouped_fwd_tile(g->R, g->K, g->M, g->E);
+    if (!tile) return too_many_tiles(g);
     hipError_t e;
-    if (few_rows(g->R, g->K, g->M, live, best.us))
+    if (tile == kFewRows)
         e = g->dtype == ZI_F16 ? few<_Float16>(a, s) : few<__bf16>(a, s);
     else
-        e = launch_grouped_fwd(g->dtype, best.tile, a, s);
+        e = launch_grouped_fwd(g->dtype, tile, a, s);
     if (e != hipSuccess) return fail(ZI_ERR_HIP, "grouped forward: %s", hipGetErrorString(e));
     return ZI_OK;
 }
@@ -392,13 +327,13 @@ extern "C" zi_status zi_grouped_dx(const zi_grouped *g, const void *dY, const vo
     a.cols = g->K;
     a.red = g->M;
     hipStream_t s = static_cast<hipStream_t>(stream);
-    const int64_t live = min64(g->E, g->R);
-    const Choice best = tile_of(g->R, g->K, live, (double)g->M, true);
+    const int tile = grouped_dx_tile(g->R, g->K, g->M, g->E);
+    if (!tile) return too_many_tiles(g);
     hipError_t e;
-    if (few_rows_dx(g->R, g->K, g->M, live, best.us))
+    if (tile == kFewRows)
         e = g->dtype == ZI_F16 ? few_dx<_Float16>(a, s) : few_dx<__bf16>(a, s);
     else
-        e = launch_grouped_dx(g->dtype, best.tile, a, s);
+        e = launch_grouped_dx(g->dtype, tile, a, s);
     if (e != hipSuccess) return fail(ZI_ERR_HIP, "grouped input gradient: %s", hipGetErrorString(e));
     return ZI_OK;
 }
@@ -425,7 +360,9 @@ extern "C" zi_status zi_grouped_dw(const zi_grouped *g, const void *X, const voi
     a.red = g->R;
     a.accumulate = g->accumulate;
     hipStream_t s = static_cast<hipStream_t>(stream);
-    const hipError_t e = launch_grouped_dw(g->dtype, tile_of(g->M, g->K, g->E, (double)g->R / g->E, false).tile, a, s);
+    const int tile = grouped_dw_tile(g->R, g->K, g->M, g->E, g->accumulate != 0);
+    if (!tile) return too_many_tiles(g);
+    const hipError_t e = launch_grouped_dw(g->dtype, tile, a, s);
     if (e != hipSuccess) return fail(ZI_ERR_HIP, "grouped weight gradient: %s", hipGetErrorString(e));
     return ZI_OK;
 }

@@ -6,24 +6,23 @@
 #include <stdint.h>
 
 #include "zi_gemm.h"
+#include "zi_grouped_choice.h"
 #include "zi_internal.h"
 
 namespace zi {
 namespace {
 
-// One workgroup a macro-tile.  The groups' sizes are known on the device only: of row
-// tiles there are at most rows / TILE and one more for every group with rows, and
-// workgroups without a tile end at once.
+// One workgroup a macro-tile (row_grid and dw_grid, which the choice of the tile keeps
+// within a launch's bounds).
 template <typename T, bool Q_RS, bool P_RS, int EPI, bool ALIGNED, int B>
 hipError_t run_grouped(const GroupArgs &a, hipStream_t s) {
     constexpr int TILE = 32 * B;
     constexpr bool DW = Q_RS && P_RS;
-    const int64_t tiles_q = (a.cols + TILE - 1) / TILE;
-    const int64_t tiles_p = DW ? (a.rows + TILE - 1) / TILE : a.total / TILE + (a.groups < a.total ? a.groups : a.total);
-    int64_t grid = tiles_p * tiles_q * (DW ? a.groups : 1);
-    grid = (grid + 7) / 8 * 8;
+    const int64_t tiles_q = ceil_div(a.cols, TILE);
+    const int64_t tiles_p = DW ? ceil_div(a.rows, TILE) : a.total / TILE + min64(a.groups, a.total);
+    const int64_t grid = DW ? dw_grid(a.rows, a.cols, a.groups, TILE) : row_grid(a.total, a.groups, a.cols, TILE, TILE);
     if (grid <= 0) return hipSuccess;
-    if (grid > INT32_MAX / kThreads) return hipErrorInvalidValue;
+    if (grid > most_workgroups(kThreads)) return hipErrorInvalidValue;
     // a lane's offset inside a tile or a step stays below the descriptors' range
     if (a.ldq > kGroupLd || a.ldp > kGroupLd || a.red >= ((int64_t)1 << 31)) return hipErrorInvalidValue;
     hipLaunchKernelGGL((gemm_kernel<T, Q_RS, P_RS, EPI, ALIGNED, B, B, false, GroupArgs>), dim3((unsigned)grid), dim3(kThreads), 0, s,
