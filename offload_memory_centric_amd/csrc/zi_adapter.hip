@@ -293,8 +293,17 @@ struct Planes<f16_t> {
     static constexpr int N = 2;
     static constexpr bool kScaled = true;
 };
-template <typename T, int N>
-__device__ __forceinline__ void split_planes(const float (&v)[8], u32x4 (&out)[N]) {
+// An infinity among the other operand's elements makes the sum of the planes' products NaN
+// where it should be the infinity: the planes past the first may be zero, or of the other
+// sign.  So sums that are not finite are formed once more (expand in fp32, grad as below);
+// what a finite product takes does not change.
+//
+// ODD: for products with infinities.  The first plane of a value x (v is x scaled) is not
+// zero where x is not, and the others are given finite_only of the other operand, zeros in
+// place of its infinities and NaN.  (Always so, the gradient of 16384 fp16 rows of 4096,
+// r = 48, took 318 us in place of 260.)
+template <bool ODD, typename T, int N>
+__device__ __forceinline__ void split_planes(const float (&x)[8], const float (&v)[8], u32x4 (&out)[N]) {
     float r[8];
 #pragma unroll
     for (int i = 0; i < 8; ++i) r[i] = v[i];
@@ -306,12 +315,26 @@ __device__ __forceinline__ void split_planes(const float (&v)[8], u32x4 (&out)[N
 #pragma unroll
             for (int q = 0; q < 2; ++q) {
                 b[q] = bits16<T>(r[2 * h + q]);
+                if (ODD && p == 0) {
+                    const uint32_t least = min(__builtin_bit_cast(uint32_t, x[2 * h + q]) << 1, 1u);
+                    b[q] = (b[q] & 0x8000u) | max(b[q] & 0x7fffu, least);
+                }
                 const float rest = r[2 * h + q] - value16<T>(b[q]);
                 r[2 * h + q] = fabsf(rest) < INFINITY ? rest : 0.f;  // nothing is left of an infinity or a NaN
             }
             out[p][h] = b[0] | (b[1] << 16);
         }
     }
+}
+
+typedef int16_t s16x8 __attribute__((ext_vector_type(8)));
+template <typename T>
+constexpr int16_t kInf16 = std::is_same<T, f16_t>::value ? 0x7c00 : 0x7f80;
+template <typename T>
+__device__ __forceinline__ u32x4 finite_only(u32x4 x) {
+    const s16x8 v = __builtin_bit_cast(s16x8, x);
+    const s16x8 keep = ((v & (int16_t)0x7fff) - kInf16<T>) >> (int16_t)15;
+    return __builtin_bit_cast(u32x4, v & keep);
 }
 
 // A value's part in the largest of those that share a scale: an infinity (or NaN) has
@@ -327,6 +350,20 @@ __device__ __forceinline__ int scale_exponent(float most) {
     return max(__builtin_amdgcn_frexp_expf(most), -110);
 }
 
+// Whether any lane has a sum that is infinite or NaN.
+template <int N>
+__device__ __forceinline__ bool any_infinite(const f32x4 (&acc)[N]) {
+    float none[8] = {};  // eight chains
+#pragma unroll
+    for (int j = 0; j < N; ++j)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) none[4 * (j & 1) + e] = __builtin_fmaf(acc[j][e], 0.f, none[4 * (j & 1) + e]);
+    float sum = 0.f;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) sum += none[i];
+    return __ballot(sum != 0.f) != 0;  // NaN
+}
+
 // A wave: 128 columns of a run of rows, 16 rows at a time.  Per step of 32 ranks a lane
 // reads eight columns of eight rows of B_n and turns them, in its own registers, into one
 // operand for each of the columns, held over the run (STEPS of 1 or 2, r <= 64; with 0,
@@ -336,9 +373,11 @@ __device__ __forceinline__ int scale_exponent(float most) {
 // their way while these are multiplied and stored.  (On the fp32 instruction, 4508 rows
 // of 2384 in 61 segments, r = 64, took 50 us, 37 so; 32768 of 8192 into fp32, r = 32, 462
 // and 406.)
+// With one step held two waves a SIMD fit: their bound keeps the sums' second form, which is
+// hardly ever run, from costing registers.
 constexpr int kExpandCols = 512;
 template <typename T, typename YT, int STEPS>
-__global__ __launch_bounds__(256) void expand_kernel(ExpandArgs a, int block) {
+__global__ __launch_bounds__(256, STEPS == 1 ? 2 : 1) void expand_kernel(ExpandArgs a, int block) {
     constexpr int NP = Planes<T>::N, HELD = STEPS > 0 ? STEPS : 1;
     constexpr bool kScaled = Planes<T>::kScaled;
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, c = lane & 15, g = lane >> 4;
@@ -392,11 +431,31 @@ __global__ __launch_bounds__(256) void expand_kernel(ExpandArgs a, int block) {
 #pragma unroll
             for (int i = 0; i < 8; ++i) v[i] = kScaled ? ldexpf(u[i] * scale, 15 - e) : u[i] * scale;
             u32x4 pl[NP];
-            split_planes<T>(v, pl);
+            split_planes<false, T>(v, v, pl);
 #pragma unroll
             for (int j = 0; j < 8; ++j)
 #pragma unroll
                 for (int p = 0; p < NP; ++p) acc[j] = mfma<T>(pl[p], b[s][j], acc[j]);
+        };
+        // Where a sum is infinite or NaN, the same in fp32, a rank after another: planes do not
+        // multiply infinities.  (Under a scale no finite product comes near fp32's range, so that
+        // this sum is not finite either, and the scale changes nothing.)
+        auto in_f32 = [&](int row0, f32x4 (&acc)[8]) __attribute__((always_inline)) {
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                const int row = row0 + 4 * g + q;
+                float d[8] = {};
+#pragma unroll 1
+                for (int k = 0; k < (in && row < hi ? a.r : 0); ++k) {
+                    float x[8];
+                    load8(reinterpret_cast<const T *>(B + (int64_t)k * a.M), x);
+                    const float w = a.U[(int64_t)k * a.seg.rows + row] * scale;
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) d[e] += w * x[e];
+                }
+#pragma unroll
+                for (int j = 0; j < 8; ++j) acc[j][q] = fabsf(acc[j][q]) < INFINITY ? acc[j][q] : d[j];
+            }
         };
         auto largest = [&](float (&u)[8], float most) __attribute__((always_inline)) -> float {
 #pragma unroll
@@ -431,6 +490,7 @@ __global__ __launch_bounds__(256) void expand_kernel(ExpandArgs a, int block) {
             }
             __builtin_amdgcn_sched_barrier(0);
             asm volatile("s_nop 7" ::: "memory");  // the last products, before anything reads the sums
+            if (__builtin_expect(any_infinite(acc), 0)) in_f32(row0, acc);
             const float back = kScaled ? ldexpf(1.f, e - 15) : 1.f;
 #pragma unroll
             for (int q = 0; q < 4; ++q) {
@@ -541,9 +601,10 @@ struct GradArgs {
 // (ds_read_b64_tr_b16); V comes to registers as eight rows of a rank a lane.  (32768 rows
 // of 8192 and 8192 with r = 32: 237 us, 4.5 TB/s; in two launches with two splits 138 each,
 // and 6 for their sum.  In fp32, 16 x 16 x 4 at a time, each took 183, 109 of them the
-// matrix cores' at their rate.)
+// matrix cores' at their rate.)  A wave whose sums are not finite forms them again, as ODD
+// products.  (Two waves a SIMD fit, but for four fragments of fp16.)
 template <typename T, int F>
-__global__ __launch_bounds__(256) void grad_kernel(GradArgs a) {
+__global__ __launch_bounds__(256, Planes<T>::kScaled ? 1 : 2) void grad_kernel(GradArgs a) {
     constexpr int NP = Planes<T>::N;
     constexpr bool kScaled = Planes<T>::kScaled;
     constexpr int kChunk = 32, kRowB = 256, kStage = kChunk * kRowB;
@@ -570,11 +631,10 @@ __global__ __launch_bounds__(256) void grad_kernel(GradArgs a) {
         const int row = 4 * i + g, col = ((((c >> 1) ^ swizzle(row)) << 1) | (c & 1)) * 8;
         xo[i] = k0 + col < K ? (uint32_t)((row * ldx + col) * 2) : kOOB;
     }
-    // fragment j (16 columns): this lane's part of rows 0 .. 3 of each eight; the others are 4 rows on
+    // fragment 0 (16 columns): this lane's part of rows 0 .. 3 of each eight; the others are 4
+    // rows on, and fragment j's at the address with bits 5 .. 7 changed by j
     const int kl = 8 * g + (c >> 2);
-    uint32_t fo[8];
-#pragma unroll
-    for (int j = 0; j < 8; ++j) fo[j] = (uint32_t)(kl * kRowB + ((j ^ swizzle(kl)) << 5) + 8 * (c & 3));
+    const uint32_t fo = (uint32_t)(kl * kRowB + (swizzle(kl) << 5) + 8 * (c & 3));
     // ranks past the last read the last one's values and are not stored
     const float *V[F];
 #pragma unroll
@@ -586,8 +646,8 @@ __global__ __launch_bounds__(256) void grad_kernel(GradArgs a) {
     // began with the first worker).  `due`: chunks of the next segment before this
     // wave's first.
     const int workers = 4 * a.splits, step = workers * kChunk;
-    int s0 = -64, hi = 0, t = -step, due = split * 4 + wave;
-    uint64_t left = 0;
+    int s0, hi, t, due;
+    uint64_t left;
     auto next = [&]() __attribute__((always_inline)) -> bool {
         t += step;
         while (t >= hi) {
@@ -630,66 +690,84 @@ __global__ __launch_bounds__(256) void grad_kernel(GradArgs a) {
         }
     };
 
-    f32x4 acc[F][8] = {};
-    int stage = 0;
-    bool more = next();
-    if (lane == 0) any[wave] = more;
-    if (more) {
-        copy(0);
-        load_v();
-    }
-    while (more) {
-        // this chunk is in LDS, its V in registers, and the other stage has been read
-        asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
-        u32x4 pl[F][NP];
-        [[maybe_unused]] float unscale[F][4];
+    f32x4 acc[F][8];
+    auto sum = [&](auto odd) __attribute__((always_inline)) {
+        constexpr bool ODD = decltype(odd)::value;
+        s0 = -64, hi = 0, t = -step, due = split * 4 + wave;
+        left = 0;
 #pragma unroll
-        for (int f = 0; f < F; ++f) {
-            if constexpr (kScaled) {
-                float most = 0.f;
+        for (int f = 0; f < F; ++f)
 #pragma unroll
-                for (int i = 0; i < 8; ++i) most = largest_of(most, v[f][i]);
-                const int e = scale_exponent(most);  // of the rank's 32 rows
-#pragma unroll
-                for (int i = 0; i < 8; ++i) v[f][i] = ldexpf(v[f][i], 15 - e);
-                const float back = ldexpf(1.f, e - 15);
-#pragma unroll
-                for (int i = 0; i < 4; ++i) unscale[f][i] = __shfl(back, 4 * g + i, 64);
-            }
-            split_planes<T>(v[f], pl[f]);
-        }
-        more = next();
+            for (int j = 0; j < 8; ++j) acc[f][j] = f32x4{0.f, 0.f, 0.f, 0.f};
+        int stage = 0;
+        bool more = next();
+        if (lane == 0) any[wave] = more;
         if (more) {
-            copy(stage ^ 1);
+            copy(0);
             load_v();
         }
-        const uint32_t base = at + stage * kStage;
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            const s16x4 x0 =
-                __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) s16x4 *)(uintptr_t)(base + fo[j]));
-            const s16x4 x1 = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
-                (__attribute__((address_space(3))) s16x4 *)(uintptr_t)(base + fo[j] + 4 * kRowB));
-            const u32x2 w0 = __builtin_bit_cast(u32x2, x0), w1 = __builtin_bit_cast(u32x2, x1);
-            const u32x4 x = {w0[0], w0[1], w1[0], w1[1]};
+        while (more) {
+            // this chunk is in LDS, its V in registers, and the other stage has been read
+            asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
+            u32x4 pl[F][NP];
+            [[maybe_unused]] float unscale[F][4];
 #pragma unroll
             for (int f = 0; f < F; ++f) {
+                float w[8];
+#pragma unroll
+                for (int i = 0; i < 8; ++i) w[i] = v[f][i];
                 if constexpr (kScaled) {
-                    f32x4 part = {};
+                    float most = 0.f;
 #pragma unroll
-                    for (int p = 0; p < NP; ++p) part = mfma<_Float16>(pl[f][p], x, part);
+                    for (int i = 0; i < 8; ++i) most = largest_of(most, w[i]);
+                    const int e = scale_exponent(most);  // of the rank's 32 rows
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) acc[f][j][e] += part[e] * unscale[f][e];
-                } else {
+                    for (int i = 0; i < 8; ++i) w[i] = ldexpf(w[i], 15 - e);
+                    const float back = ldexpf(1.f, e - 15);
 #pragma unroll
-                    for (int p = 0; p < NP; ++p) acc[f][j] = mfma<__bf16>(pl[f][p], x, acc[f][j]);
+                    for (int i = 0; i < 4; ++i) unscale[f][i] = __shfl(back, 4 * g + i, 64);
+                }
+                split_planes<ODD, T>(v[f], w, pl[f]);
+            }
+            more = next();
+            if (more) {
+                copy(stage ^ 1);
+                load_v();
+            }
+            const uint32_t base = at + stage * kStage + fo;
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                const uint32_t from = base ^ (uint32_t)(j << 5);
+                const s16x4 x0 =
+                    __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) s16x4 *)(uintptr_t)from);
+                const s16x4 x1 = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+                    (__attribute__((address_space(3))) s16x4 *)(uintptr_t)(from + 4 * kRowB));
+                const u32x2 w0 = __builtin_bit_cast(u32x2, x0), w1 = __builtin_bit_cast(u32x2, x1);
+                const u32x4 x = {w0[0], w0[1], w1[0], w1[1]}, rest = ODD ? finite_only<T>(x) : x;
+#pragma unroll
+                for (int f = 0; f < F; ++f) {
+                    if constexpr (kScaled) {
+                        f32x4 part = {};
+#pragma unroll
+                        for (int p = 0; p < NP; ++p) part = mfma<_Float16>(pl[f][p], p ? rest : x, part);
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) acc[f][j][e] += part[e] * unscale[f][e];
+                    } else {
+#pragma unroll
+                        for (int p = 0; p < NP; ++p) acc[f][j] = mfma<__bf16>(pl[f][p], p ? rest : x, acc[f][j]);
+                    }
                 }
             }
+            stage ^= 1;
         }
-        stage ^= 1;
-    }
-    __builtin_amdgcn_sched_barrier(0);
-    asm volatile("s_nop 7\n\ts_nop 7" ::: "memory");  // the last products, before anything reads the sums
+        __builtin_amdgcn_sched_barrier(0);
+        asm volatile("s_nop 7\n\ts_nop 7" ::: "memory");  // the last products, before anything reads the sums
+    };
+    sum(std::integral_constant<bool, false>{});
+    bool infinite = false;
+#pragma unroll
+    for (int f = 0; f < F; ++f) infinite |= any_infinite(acc[f]);
+    if (__builtin_expect(infinite, 0)) sum(std::integral_constant<bool, true>{});
 
     // the four waves' sums meet in LDS, one fragment of ranks at a time
     const float scale = d.scales ? d.scales[n] : 1.f;
