@@ -277,6 +277,10 @@ __device__ __forceinline__ float u_at(const ExpandArgs &a, int rank, int row) {
     return u;
 }
 
+typedef int16_t s16x8 __attribute__((ext_vector_type(8)));
+template <typename T>
+constexpr int16_t kInf16 = std::is_same<T, f16_t>::value ? 0x7c00 : 0x7f80;
+
 // Eight fp32 values in planes of the 16-bit type that the other operand has, so that the
 // 16-bit instruction multiplies them: three of bf16 (24 bits, at any scale), two of fp16
 // (22 bits below the largest value of those that share a scale, 2^(15 - e), which takes
@@ -298,10 +302,11 @@ struct Planes<f16_t> {
 // sign.  So sums that are not finite are formed once more (expand in fp32, grad as below);
 // what a finite product takes does not change.
 //
-// ODD: for products with infinities.  The first plane of a value x (v is x scaled) is not
-// zero where x is not, and the others are given finite_only of the other operand, zeros in
-// place of its infinities and NaN.  (Always so, the gradient of 16384 fp16 rows of 4096,
-// r = 48, took 318 us in place of 260.)
+// ODD: for products with infinities.  The first plane of a value x (v is x scaled) is neither
+// zero nor an infinity where x is not (fp32's largest values round up past bf16's), and the
+// others are given finite_only of the other operand, zeros in place of its infinities and
+// NaN.  (Always so, the gradient of 16384 fp16 rows of 4096, r = 48, took 318 us in place of
+// 260.)
 template <bool ODD, typename T, int N>
 __device__ __forceinline__ void split_planes(const float (&x)[8], const float (&v)[8], u32x4 (&out)[N]) {
     float r[8];
@@ -317,7 +322,10 @@ __device__ __forceinline__ void split_planes(const float (&x)[8], const float (&
                 b[q] = bits16<T>(r[2 * h + q]);
                 if (ODD && p == 0) {
                     const uint32_t least = min(__builtin_bit_cast(uint32_t, x[2 * h + q]) << 1, 1u);
-                    b[q] = (b[q] & 0x8000u) | max(b[q] & 0x7fffu, least);
+                    uint32_t size = max(b[q] & 0x7fffu, least);
+                    if (!Planes<T>::kScaled && size == (uint32_t)kInf16<T>)  // cut off, not rounded
+                        size = __builtin_bit_cast(uint32_t, r[2 * h + q]) >> 16 & 0x7fffu;
+                    b[q] = (b[q] & 0x8000u) | size;
                 }
                 const float rest = r[2 * h + q] - value16<T>(b[q]);
                 r[2 * h + q] = fabsf(rest) < INFINITY ? rest : 0.f;  // nothing is left of an infinity or a NaN
@@ -327,9 +335,6 @@ __device__ __forceinline__ void split_planes(const float (&x)[8], const float (&
     }
 }
 
-typedef int16_t s16x8 __attribute__((ext_vector_type(8)));
-template <typename T>
-constexpr int16_t kInf16 = std::is_same<T, f16_t>::value ? 0x7c00 : 0x7f80;
 template <typename T>
 __device__ __forceinline__ u32x4 finite_only(u32x4 x) {
     const s16x8 v = __builtin_bit_cast(s16x8, x);

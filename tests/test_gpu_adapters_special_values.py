@@ -181,3 +181,29 @@ def test_scales_of_adapters_without_rows(scale, lengths, dtype):
                     assert torch.equal(got[n].view(torch.int32), want.view(torch.int32)), (n, accumulate, bad)
             out.append((dA, dB))
         assert torch.equal(out[0][0], out[1][0]) and torch.equal(out[0][1], out[1][1])
+
+
+@pytest.mark.parametrize("lengths", [[1] * 5, [40]])
+def test_bf16_values_at_the_end_of_fp32s_range(lengths):
+    """A finite factor that rounds to bf16's infinity is still finite: Y and the gradients are, too."""
+    from offload_memory_centric_amd import layers
+    say("end of the range", lengths)
+    T, K, M, r, S = sum(lengths), 64, 72, 2, len(lengths)
+    top = float(torch.finfo(torch.float32).max)
+    bf = torch.bfloat16
+    X, dY = torch.zeros((T, K), dtype=bf, device="cuda"), torch.zeros((T, M), dtype=bf, device="cuda")
+    A, B = torch.zeros((1, r, K), dtype=bf, device="cuda"), torch.zeros((1, r, M), dtype=bf, device="cuda")
+    X[:, 0], A[0, 0, 0], B[0, 0] = 1.0, 1.0, 2.0 ** -10
+    offsets, ids = index(*range(0, T, 1), T) if S > 1 else index(0, T), index(*[0] * S)
+    Y = torch.empty((T, M), device="cuda")
+    layers.adapters_fwd(X, A, B, offsets, ids, torch.full((1,), top, device="cuda"), Y,
+                        layers.workspace(layers.adapters_fwd_bytes(T, r)))
+    assert torch.isfinite(Y).all() and ((Y.double() / (top * 2.0 ** -10) - 1).abs() <= 4 * U2).all()
+    U = torch.zeros((r, T), device="cuda")
+    U[0, T - 1] = -top
+    dY[:, 0] = 2.0 ** -10
+    dA, dB = torch.empty((1, r, K), device="cuda"), torch.empty((1, r, M), device="cuda")
+    layers.adapters_bwd(X, dY, U, A, B, offsets, ids, torch.ones(1, device="cuda"), dA, dB,
+                        layers.workspace(layers.adapters_bwd_bytes(T, r)))
+    assert torch.isfinite(dB).all() and abs(float(dB[0, 0, 0]) / (-top * 2.0 ** -10) - 1) <= 4 * U2
+    assert (dB[0, 1] == 0).all() and (dB[0, 0, 1:] == 0).all()
