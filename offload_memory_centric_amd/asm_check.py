@@ -45,9 +45,11 @@ from typing import Iterable, List, Optional, Set, Tuple
 RESULT_WAIT = 18
 # MFMAs that the compiler knows (builtins) are spaced by it, except that it has been
 # seen to read a result right behind the loop that made it, with no wait states at
-# all: a kernel then lost its last product now and then.  The wait states of the
-# forms used: 16-bit ones of 4 passes, fp32 ones of 8.
+# all: a kernel then lost its last product now and then.  Wait states of 16-bit
+# forms of 4 passes and of an fp32 one of 8, and those that the compiler itself keeps
+# on gfx950 after the forms the sources use, one more, which the build asks for.
 BUILTIN_RESULT_WAIT = {"v_mfma_f32_16x16x32_f16": 7, "v_mfma_f32_16x16x32_bf16": 7, "v_mfma_f32_16x16x4_f32": 10}
+GFX950_RESULT_WAIT = {"v_mfma_f32_16x16x32_f16": 8, "v_mfma_f32_16x16x32_bf16": 8}
 VALU_TO_MFMA = 2
 
 Reg = Tuple[str, int]
@@ -225,10 +227,10 @@ def check_kernel(body: List[Tuple[int, str]]) -> List[str]:
     return sorted(set(found))
 
 
-def early_reads(body: List[Tuple[int, str]]) -> List[str]:
-    """Non-MFMA instructions that touch an MFMA's result before
-    its BUILTIN_RESULT_WAIT wait states, in a kernel whose MFMAs the compiler made:
-    along the listing, and along every branch of it that is taken; and uses of m0
+def early_reads(body: List[Tuple[int, str]], result_wait=BUILTIN_RESULT_WAIT) -> List[str]:
+    """Non-MFMA instructions that touch an MFMA's result before its `result_wait` wait
+    states (RESULT_WAIT for a form that it does not list), in a kernel whose MFMAs the
+    compiler made: along the listing, and along every branch of it that is taken; and uses of m0
     outside the copies."""
     instrs: List[Instr] = []
     labels = {}
@@ -243,7 +245,7 @@ def early_reads(body: List[Tuple[int, str]]) -> List[str]:
     found = m0_uses(instrs)
 
     def follow(i: int, waits: int, dst: Set[Reg], mfma: Instr, jumped: bool) -> None:
-        while i < len(instrs) and waits < BUILTIN_RESULT_WAIT.get(mfma.op, RESULT_WAIT):
+        while i < len(instrs) and waits < result_wait.get(mfma.op, RESULT_WAIT):
             ins = instrs[i]
             if ins.is_mfma:
                 dst = dst - regs(ins.args[0])  # overwritten, and followed from there
@@ -263,6 +265,11 @@ def early_reads(body: List[Tuple[int, str]]) -> List[str]:
         if ins.is_mfma:
             follow(i + 1, 0, regs(ins.args[0]), ins, False)
     return sorted(set(found))
+
+
+def gfx950_early_reads(body: List[Tuple[int, str]]) -> List[str]:
+    """early_reads with the wait states that the compiler keeps on gfx950."""
+    return early_reads(body, GFX950_RESULT_WAIT)
 
 
 def check_file(path: str, kernel_filter: str = "", check=check_kernel) -> dict:

@@ -68,7 +68,7 @@ def check_device_asm(src: str = "zi_kernels.hip") -> None:
     pad; of builtins it misses some)."""
     from . import asm_check
     path = device_asm(src)
-    res = asm_check.check_file(path, check=asm_check.early_reads if src in BUILTIN_SOURCES else asm_check.check_kernel)
+    res = asm_check.check_file(path, check=asm_check.gfx950_early_reads if src in BUILTIN_SOURCES else asm_check.check_kernel)
     bad = {k: v for k, v in res.items() if v}
     if not res:
         raise RuntimeError("no kernels found in %s" % path)

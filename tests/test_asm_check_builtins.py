@@ -1,0 +1,32 @@
+"""The wait states after a builtin MFMA that the build asks for."""
+import os
+
+import pytest
+
+from offload_memory_centric_amd import asm_check, build
+
+MFMA = "\tv_mfma_f32_16x16x32_bf16 v[0:3], v[8:11], v[4:7], v[0:3]"
+READ = "\tv_add_f32 v12, v13, v2"
+
+
+def findings(*lines):
+    return asm_check.gfx950_early_reads(list(enumerate(lines, 1)))
+
+
+def test_eight_wait_states():
+    """As many as the compiler puts between the instruction and a read of its result."""
+    for op in ("f16", "bf16"):
+        mfma = MFMA.replace("bf16", op)
+        assert findings(mfma, "\ts_nop 6", READ) and not findings(mfma, "\ts_nop 7", READ)
+    # a form that is not listed has the longest latency's
+    slow = "\tv_mfma_f32_32x32x16_f16 v[0:15], v[16:19], v[20:23], v[0:15]"
+    assert findings(slow, "\ts_nop 7", "\ts_nop 7", READ) and not findings(slow, "\ts_nop 7", "\ts_nop 7", "\ts_nop 1", READ)
+
+
+def test_built_sources_keep_them():
+    for src in build.BUILTIN_SOURCES:
+        path = build.device_asm(src)
+        if not os.path.exists(path):
+            pytest.skip("no kept assembly")
+        found = asm_check.check_file(path, check=asm_check.gfx950_early_reads)
+        assert found and not any(found.values()), {k: v[:3] for k, v in found.items() if v}
