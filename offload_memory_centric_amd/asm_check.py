@@ -230,8 +230,8 @@ def check_kernel(body: List[Tuple[int, str]]) -> List[str]:
 def early_reads(body: List[Tuple[int, str]], result_wait=BUILTIN_RESULT_WAIT) -> List[str]:
     """Non-MFMA instructions that touch an MFMA's result before its `result_wait` wait
     states (RESULT_WAIT for a form that it does not list), in a kernel whose MFMAs the
-    compiler made: along the listing, and along every branch of it that is taken; and uses of m0
-    outside the copies."""
+    compiler made: along the listing and every way through its branches, as far as the
+    wait states reach; and uses of m0 outside the copies."""
     instrs: List[Instr] = []
     labels = {}
     for no, line in body:
@@ -244,26 +244,32 @@ def early_reads(body: List[Tuple[int, str]], result_wait=BUILTIN_RESULT_WAIT) ->
             instrs.append(ins)
     found = m0_uses(instrs)
 
-    def follow(i: int, waits: int, dst: Set[Reg], mfma: Instr, jumped: bool) -> None:
-        while i < len(instrs) and waits < result_wait.get(mfma.op, RESULT_WAIT):
+    for first, mfma in enumerate(instrs):
+        if not mfma.is_mfma:
+            continue
+        need = result_wait.get(mfma.op, RESULT_WAIT)
+        ways = [(first + 1, 0, frozenset(regs(mfma.args[0])))]
+        seen = set(ways)
+        while ways:
+            i, waits, dst = ways.pop()
+            if i >= len(instrs) or waits >= need or not dst:
+                continue
             ins = instrs[i]
             if ins.is_mfma:
                 dst = dst - regs(ins.args[0])  # overwritten, and followed from there
             elif ins.touched() & dst:
                 found.append("line %d: %r touches the result of MFMA %r (line %d) after %d wait states"
                              % (ins.line, ins.text, mfma.text, mfma.line, waits))
-                return
+                continue
             b = _BRANCH.match(ins.text)
-            if b and b.group(1) in labels and not jumped:
-                follow(labels[b.group(1)], waits + 1, dst, mfma, True)
-            if ins.op == "s_branch" or ins.op == "s_endpgm":
-                return
-            waits += ins.waits
-            i += 1
-
-    for i, ins in enumerate(instrs):
-        if ins.is_mfma:
-            follow(i + 1, 0, regs(ins.args[0]), ins, False)
+            nexts = [labels[b.group(1)]] if b and b.group(1) in labels else []
+            if ins.op not in ("s_branch", "s_endpgm"):
+                nexts.append(i + 1)
+            for n in nexts:
+                way = (n, waits + ins.waits, dst)
+                if way not in seen:
+                    seen.add(way)
+                    ways.append(way)
     return sorted(set(found))
 
 

@@ -1,4 +1,4 @@
-"""The wait states after a builtin MFMA that the build asks for."""
+"""The wait states after a builtin MFMA that the build asks for, and the ways through branches that it follows."""
 import os
 
 import pytest
@@ -7,6 +7,7 @@ from offload_memory_centric_amd import asm_check, build
 
 MFMA = "\tv_mfma_f32_16x16x32_bf16 v[0:3], v[8:11], v[4:7], v[0:3]"
 READ = "\tv_add_f32 v12, v13, v2"
+END = "\ts_endpgm"
 
 
 def findings(*lines):
@@ -21,6 +22,31 @@ def test_eight_wait_states():
     # a form that is not listed has the longest latency's
     slow = "\tv_mfma_f32_32x32x16_f16 v[0:15], v[16:19], v[20:23], v[0:15]"
     assert findings(slow, "\ts_nop 7", "\ts_nop 7", READ) and not findings(slow, "\ts_nop 7", "\ts_nop 7", "\ts_nop 1", READ)
+
+
+def test_two_jumps_to_a_read():
+    """Out of a loop, and on from the block behind it: two jumps between the instruction and the read."""
+    out = [".LBB0_1:", MFMA, "\ts_cbranch_scc1 .LBB0_3", "\ts_branch .LBB0_1", ".LBB0_3:", "\ts_branch .LBB0_5", ".LBB0_4:",
+           "\tv_mov_b32 v20, v21", ".LBB0_5:"]
+    assert findings(*out, READ, END)
+    assert findings(*out, "\ts_nop 4", READ, END)
+    assert not findings(*out, "\ts_nop 5", READ, END)
+    # three, and conditional ones
+    ways = [MFMA, "\ts_cbranch_vccz .LBB0_1", END, ".LBB0_1:", "\ts_cbranch_execz .LBB0_2", END, ".LBB0_2:",
+            "\ts_cbranch_scc0 .LBB0_3", END, ".LBB0_3:"]
+    assert findings(*ways, READ, END)
+    assert not findings(*ways, "\ts_nop 4", READ, END)
+
+
+def test_a_loop_without_a_read_ends():
+    assert not findings(".LBB0_1:", "\ts_branch .LBB0_1", MFMA, ".LBB0_2:", "\ts_branch .LBB0_2")
+    assert not findings(MFMA, ".LBB0_2:", "\ts_cbranch_scc1 .LBB0_2", END)
+
+
+def test_a_result_that_is_overwritten_is_followed_from_there():
+    again = MFMA.replace("v[0:3], v[8:11]", "v[0:3], v[16:19]")
+    assert findings(MFMA, "\ts_nop 7", again, READ)
+    assert not findings(MFMA, again, "\ts_nop 7", READ)
 
 
 def test_built_sources_keep_them():
