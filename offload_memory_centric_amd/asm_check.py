@@ -128,6 +128,9 @@ def check_sequence(seq: Iterable[Instr]) -> List[str]:
     valu: List[Tuple[Set[Reg], int, Instr]] = []     # recent VALU writes: (regs, age, instr)
     loads: List[Tuple[Set[Reg], Instr]] = []         # vector memory in flight, oldest first
     for ins in seq:
+        if ins.op == "s_endpgm":  # what follows is reached by a branch, which is followed
+            recent, valu, loads = [], [], []
+            continue
         if ins.op == "s_waitcnt":
             m = _VMCNT.search(ins.text)
             if m:
@@ -285,21 +288,23 @@ def check_file(path: str, kernel_filter: str = "", check=check_kernel) -> dict:
     out = {}
     cur = None
     body: List[Tuple[int, str]] = []
+
+    def close() -> None:
+        if cur is not None and any("s_endpgm" in line for _, line in body):  # not data or metadata
+            out[cur] = check(body)
+
     for no, line in enumerate(lines, 1):
         m = _KERNEL.match(line)
         if m and not line.startswith(".") and not line.startswith(" ") and not line.startswith("\t"):
-            if cur is not None:
-                out[cur] = check(body)
+            close()
             cur = m.group(1) if kernel_filter in m.group(1) else None
             body = []
-            continue
-        if cur is None:
-            continue
-        if "s_endpgm" in line:
-            out[cur] = check(body)
+        elif line.startswith(".Lfunc_end"):  # not the first s_endpgm: blocks may follow an early one
+            close()
             cur = None
-            continue
-        body.append((no, line))
+        elif cur is not None:
+            body.append((no, line))
+    close()
     return out
 
 

@@ -56,3 +56,20 @@ def test_built_sources_keep_them():
             pytest.skip("no kept assembly")
         found = asm_check.check_file(path, check=asm_check.gfx950_early_reads)
         assert found and not any(found.values()), {k: v[:3] for k, v in found.items() if v}
+
+
+def kernels(tmp_path, check, *texts):
+    path = tmp_path / "listing.s"
+    path.write_text("".join("_ZN2zi%dk%dEv:\n%s\n.Lfunc_end%d:\n\t.section .rodata\n" % (2, i, t, i) for i, t in enumerate(texts)))
+    return asm_check.check_file(str(path), check=check)
+
+
+@pytest.mark.parametrize("check", [asm_check.check_kernel, asm_check.gfx950_early_reads])
+def test_code_behind_the_first_end_is_checked(tmp_path, check):
+    """A kernel with an early end has blocks behind it; an end holds nothing up for the block that follows it."""
+    early = "\ts_cbranch_scc1 .LBB0_2\n\ts_endpgm\n.LBB0_2:\n"
+    good = early + MFMA + "\n\ts_nop 7\n\ts_nop 7\n\ts_nop 7\n" + READ + "\n\ts_endpgm"
+    bad = early + MFMA + "\n" + READ + "\n\ts_endpgm"
+    res = kernels(tmp_path, check, good, bad, good)
+    assert [bool(v) for v in res.values()] == [False, True, False] and len(res) == 3
+    assert not any(kernels(tmp_path, check, MFMA + "\n\ts_endpgm\n.LBB0_3:\n" + READ + "\n\ts_endpgm").values())
