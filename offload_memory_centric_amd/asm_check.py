@@ -34,7 +34,8 @@ Rules (in wait states: one per instruction, n + 1 for ``s_nop n``):
 
 Control flow: the file is walked in order, and for every branch the last
 instructions before it are also checked against the first instructions at its
-target, so a loop's back edge and a forward jump are covered too.
+target, so a loop's back edge and a forward jump are covered too; an MFMA's
+result is followed along every way through the branches.
 """
 from __future__ import annotations
 
@@ -227,6 +228,7 @@ def check_kernel(body: List[Tuple[int, str]]) -> List[str]:
     for at, target in branches:
         if target in labels:
             found += check_sequence(_window(instrs, at + 1, False) + _window(instrs, labels[target], True))
+    found += early_reads(body, {})  # behind two branches and more
     return sorted(set(found))
 
 

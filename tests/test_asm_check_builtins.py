@@ -73,3 +73,12 @@ def test_code_behind_the_first_end_is_checked(tmp_path, check):
     res = kernels(tmp_path, check, good, bad, good)
     assert [bool(v) for v in res.values()] == [False, True, False] and len(res) == 3
     assert not any(kernels(tmp_path, check, MFMA + "\n\ts_endpgm\n.LBB0_3:\n" + READ + "\n\ts_endpgm").values())
+
+
+def test_two_jumps_in_a_kernel_of_inline_assembly():
+    """Its results are read through two branches as late as behind one."""
+    out = [MFMA.replace("v[0:3]", "a[0:3]"), "\ts_cbranch_scc1 .LBB0_3", END, ".LBB0_3:", "\ts_branch .LBB0_5", ".LBB0_4:", "\ts_nop 7",
+           "\ts_nop 7", "\ts_nop 7", ".LBB0_5:"]
+    drain, read = ["\ts_nop 7", "\ts_nop 7"], "\tv_accvgpr_read_b32 v8, a1"
+    assert asm_check.check_kernel(list(enumerate(out + [read, END], 1)))
+    assert not asm_check.check_kernel(list(enumerate(out + drain + [read, END], 1)))
