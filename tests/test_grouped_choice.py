@@ -104,3 +104,6 @@ def test_refused_before_anything_is_enqueued(op, R, K, M, E):
         else:
             zi.zi_grouped_dw(g, at, at, at, at)
     assert e.value.status == zi.ZI_ERR_SHAPE, str(e.value)
+    g.R = 0
+    zi.zi_grouped_fwd(g, None, None, None, None, None)  # nothing to do, whatever the sizes
+    assert zi.zi_last_error() == ""
