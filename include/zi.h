@@ -885,7 +885,10 @@ typedef struct {
 
 /* U = A_n X^T (fp32, [r x T], contiguous; zero for rows without an adapter), and
  * Y = RNE(Y0 + scales[n] U^T B_n).  Y0 NULL: zero; it may be Y itself.  U, which the
- * backward takes, may be NULL.  The workspace for T rows also serves fewer. */
+ * backward takes, may be NULL.  The workspace for T rows also serves fewer.
+ * Where U and dU are multiplied, bf16 adapters take all of their bits; fp16 ones take each
+ * value to within 2^-22 of itself or 2^-39 of the largest of its row over the ranks (for
+ * dA and dB, of its rank over 32 rows), whichever is more. */
 uint64_t zi_adapters_fwd_bytes(int64_t T, int32_t r);
 zi_status zi_adapters_fwd(const zi_adapters *adapters, const void *X, const void *A, const void *B,
                           const int32_t *offsets, const int32_t *ids, const float *scales, const void *Y0, void *Y,

@@ -9,13 +9,15 @@
 //   shrink  U from X and A, dU from dY and B      reads the wide rows once
 //   expand  Y from U and B, dX from dU and A      reads and writes the wide rows once
 //   grad    dA from dU and X, dB from U and dY    reads the wide rows once
-// All are bound by the bytes of the wide rows while r is small.  U is kept in fp32 and
-// rounded nowhere: where it is multiplied it is split into planes of the other operand's
-// 16 bits, which the 16-bit matrix instruction takes at sixteen times the rate of the
-// fp32 one (three of bf16 hold all 24, two of fp16 hold 22).  shrink's operands are 16-bit
-// inputs, multiplied exactly.
+// All are bound by the bytes of the wide rows while r is small.  U is kept in fp32; where it
+// is multiplied it is split into planes of the other operand's 16 bits, which the 16-bit
+// matrix instruction takes at sixteen times the rate of the fp32 one.  Three of bf16 hold all
+// 24 of its bits.  Two of fp16 hold 22 of those values that are no less than 2^-17 of the
+// largest that shares their scale (a row's ranks in expand, 32 rows of a rank in grad), and
+// smaller ones to within 2^-39 of that largest.  shrink's operands are 16-bit inputs,
+// multiplied exactly.
 // (20011 fp16 rows of 8192 by 8192 with r = 16: shrink 77 us, 4.3 TB/s, its parts' sum 5,
-// expand 131, 5.0 TB/s.  Backward of 32768 bf16 rows, r = 32, dX in fp32: shrink 103 us,
+// expand 131, 5.0 TB/s.  Backward of 32768 bf16 rows, r = 32, dX in fp32: shrink 102 us,
 // 5.2 TB/s, expand 405, 5.3 TB/s, grad for both 237, 4.5 TB/s.)
 //
 // A row's result depends on that row and its adapter alone: segments are multiplied one
@@ -283,8 +285,9 @@ constexpr int16_t kInf16 = std::is_same<T, f16_t>::value ? 0x7c00 : 0x7f80;
 
 // Eight fp32 values in planes of the 16-bit type that the other operand has, so that the
 // 16-bit instruction multiplies them: three of bf16 (24 bits, at any scale), two of fp16
-// (22 bits below the largest value of those that share a scale, 2^(15 - e), which takes
-// it into [2^14, 2^15)).
+// under a scale 2^(15 - e) that takes the largest of those that share it into [2^14, 2^15).
+// The second fp16 plane's unit is 2^-24: half of it is 2^-39 of the largest, and down to
+// 2^-17 of the largest it is no more than the second rounding, 2^-22 of the value.
 template <typename T>
 struct Planes;
 template <>
