@@ -37,7 +37,8 @@ inline int64_t dw_grid(int64_t rows, int64_t cols, int64_t groups, int64_t tile)
 // (8000 rows of 60 groups, 4096 x 1024: 196 us with 256, 158 with 128, as chosen; 20000
 // of 16, 1024 x 1024: 74.0 and 60.8, and 83.7 with 64.  Over 45 products of 1 to 64 groups
 // the choice takes 2 % longer than the best tile on average; equal sizes were not among them:
-// 64 groups of 128 rows, which are 64 tiles of 128, count as 101.)
+// 64 groups of 128 rows, which are 64 tiles of 128, count as 101.  The times themselves may be
+// off by more: 14211 rows of 24 groups, 5000 x 2048, 319 us estimated and 371 to 388 measured.)
 // Tiles of which a launch cannot have as many are not taken: grid(tile) workgroups.
 struct TileChoice {
     int tile;  // 0: none
